@@ -19,6 +19,12 @@
  *   4. commit  -- lengths of what each request commits and rolls back
  *                 (sections 2 and 11).
  *
+ * Between 2 and 3 the target model runs over the packed verify rows.  Of that
+ * the library has the attention step: norm and rotation of the query and key
+ * heads, the write of keys and values into the pages dspark_kv_reserve handed
+ * out, and attention over those pages, with or without a prefix that several
+ * requests share.
+ *
  * Conventions shared by every call:
  *   - Every array argument is a DEVICE pointer owned by the caller; the
  *     library allocates no memory and keeps no state between calls (apart
@@ -89,6 +95,13 @@ typedef struct CUstream_st* dspark_stream_t;
 #define DSPARK_OP_CALIBRATE 4
 #define DSPARK_OP_DRAFT_FUSED 5
 
+/* ---- flags of the attention step -------------------------------------------- */
+#define DSPARK_ROPE_INTERLEAVED 1u  /* rotate the pairs (2f, 2f + 1) instead of (f, f + rot / 2) */
+#define DSPARK_ATTN_FULL_BLOCK 1u   /* every row of a request sees all of its rows           */
+
+/* Largest head dspark_qk_norm_rope and dspark_kv_append take. */
+#define DSPARK_HEADS_MAX_D 256
+
 /* Largest hidden size dspark_markov_draft_fused takes. */
 #define DSPARK_FUSED_MAX_D 16384
 
@@ -122,7 +135,8 @@ const char* dspark_status_string(int status);
 /* Library version, major * 10000 + minor * 100 + patch (1.1.0: cutoff modes,
  * conf_min in dspark_select_prefix, dspark_plan_cycles, the wait settings,
  * dspark_fit_temperatures, dspark_kv_reserve and dspark_kv_commit; 1.2.0:
- * dspark_markov_draft_fused). */
+ * dspark_markov_draft_fused; 1.3.0: dspark_qk_norm_rope, dspark_kv_append,
+ * dspark_verify_attention, dspark_prefix_attention). */
 int dspark_version(void);
 
 /* Bytes of workspace one call of `op` needs for these sizes (0 on bad
@@ -508,6 +522,130 @@ int dspark_kv_reserve(const int32_t* kv_len, const int32_t* l, int R, int page_s
 int dspark_kv_commit(int32_t* kv_len, const int32_t* l, const int32_t* n_accepted, int R, int page_size,
                      int32_t* block_table, int max_blocks, int32_t* free_pages, int32_t* free_top, int pool_pages,
                      int32_t* dev_status, dspark_stream_t stream);
+
+/*
+ * dspark_qk_norm_rope -- RMS norm of every query and key head and the position
+ * rotation, in one pass (for a drafter's block, or a cache of the caller's own;
+ * dspark_kv_append does the same on the way into the paged cache).
+ *
+ * For each head x[0 .. head_dim) of row t, all in fp32, rounded once at the end:
+ *   y_i = x_i * w_i / sqrt(mean_j x_j^2 + eps)      (a NULL weight: y = x)
+ *   (y_a, y_b) <- (y_a cos A - y_b sin A, y_b cos A + y_a sin A),
+ *     A = positions[t] * inv_freq[f] in fp64, over the pairs f < rot_dim / 2:
+ *     (a, b) = (f, f + rot_dim / 2), or (2f, 2f + 1) with DSPARK_ROPE_INTERLEAVED;
+ *     elements from rot_dim on keep their y.
+ *
+ *   q            [rows, n_q_heads, head_dim]   in_dtype, q_stride elements from row to row
+ *   k            [rows, n_kv_heads, head_dim]  in_dtype, k_stride
+ *   q_weight, k_weight [head_dim] in_dtype, or NULL: that side is not normed
+ *   positions    [rows] int32 >= 0 (a negative one: the row's outputs are NaN, and it is
+ *                reported); inv_freq [rot_dim / 2] fp32 (both may be NULL iff rot_dim == 0)
+ *   q_out, k_out shaped as q and k, out_dtype, with row strides of their own.  They may be
+ *                q and k themselves (same pointer, stride and type).
+ * rows == 0 does nothing.  Limits (DSPARK_ERR_UNSUPPORTED): head_dim % 8 == 0 up to
+ * DSPARK_HEADS_MAX_D, rot_dim % 16 == 0; every pointer but positions and inv_freq 16-byte
+ * aligned, every stride a multiple of 16 bytes.
+ */
+int dspark_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int in_dtype,
+                        const void* q_weight, const void* k_weight, float eps, const int32_t* positions,
+                        const float* inv_freq, int rot_dim, int rows, int n_q_heads, int n_kv_heads,
+                        int head_dim, void* q_out, int64_t q_out_stride, void* k_out,
+                        int64_t k_out_stride, int out_dtype, unsigned flags, int32_t* dev_status,
+                        dspark_stream_t stream);
+
+/*
+ * dspark_kv_append -- the new rows' keys and values into the paged cache, with
+ * norm and rotation on the way, and the queries made ready for attention.
+ *
+ * Row cu_seqlens[r] + i stands at position kv_len[r] + i of request r, in page
+ * block_table[r][position / page_size], slot position % page_size (the pages
+ * dspark_kv_reserve handed out for the request's l + 1 verify rows).  Keys and
+ * queries are treated as in dspark_qk_norm_rope at that position; values are
+ * rounded to out_dtype.
+ *
+ *   q, k, v      [max_rows, heads, head_dim] in_dtype with row strides (v has n_kv_heads;
+ *                n_q_heads == 0: q and q_out are NULL and only keys and values are written)
+ *   cu_seqlens   [R + 1] int32, from 0, non-decreasing (a request may have no rows); rows from
+ *                cu_seqlens[R] up to max_rows are not touched
+ *   kv_len [R], block_table [R, max_blocks] int32, as in dspark_kv_reserve
+ *   k_cache, v_cache [pool_pages, n_kv_heads, page_size, head_dim] out_dtype (a page holds its
+ *                heads one after the other, so that a head's slots of a page are contiguous)
+ *   q_out        [max_rows, n_q_heads, head_dim] out_dtype, dense
+ * A row whose page is missing (-1 or not below pool_pages, or past max_blocks), or whose
+ * request's length is negative, writes nothing into the cache; its q_out is NaN and
+ * DSPARK_ERR_DEVICE_INPUT is reported.  Two rows of a call never share a slot (pages of
+ * different requests' new rows are different).  Limits as dspark_qk_norm_rope.
+ */
+int dspark_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                     int64_t v_stride, int in_dtype, const void* q_weight, const void* k_weight,
+                     float eps, const float* inv_freq, int rot_dim, const int32_t* cu_seqlens,
+                     const int32_t* kv_len, const int32_t* block_table, int R, int max_rows,
+                     int n_q_heads, int n_kv_heads, int head_dim, int page_size, int max_blocks,
+                     int pool_pages, void* k_cache, void* v_cache, void* q_out, int out_dtype,
+                     unsigned flags, int32_t* dev_status, dspark_stream_t stream);
+
+/* Bytes of workspace of dspark_verify_attention (n_groups = 0) and
+ * dspark_prefix_attention (0 on bad arguments). */
+size_t dspark_attention_workspace_size(int R, int n_groups, int max_rows, int n_q_heads, int n_kv_heads,
+                                       int head_dim);
+
+/*
+ * dspark_verify_attention -- attention of the packed rows of a batch over its
+ * paged cache: the l + 1 verify rows of each request, a single row for plain
+ * decoding, or a prompt's rows.
+ *
+ * Row i of request r (row cu_seqlens[r] + i of q) stands at position kv_len[r] + i;
+ * the request's n = cu_seqlens[r + 1] - cu_seqlens[r] rows are already in the cache
+ * (dspark_kv_append).  Query head a reads key head a / (n_q_heads / n_kv_heads).
+ * Over the positions j the row sees, j <= kv_len[r] + i (with
+ * DSPARK_ATTN_FULL_BLOCK: j < kv_len[r] + n, for a drafter whose block positions
+ * see each other both ways):
+ *   s_j = scale * q . K[j],  lse = log sum_j exp(s_j),  out = sum_j exp(s_j - lse) V[j]
+ * What lies in the pages past a request's last position, and what a row does not
+ * see, has no influence on it, NaN and infinities among it.
+ *
+ *   q            [max_rows, n_q_heads, head_dim] bf16
+ *   k_cache, v_cache [pool_pages, n_kv_heads, page_size, head_dim] bf16
+ *   block_table, kv_len, cu_seqlens  as in dspark_kv_append
+ *   out          [max_rows, n_q_heads, head_dim] bf16;  lse [max_rows, n_q_heads] fp32 or NULL
+ *   ws, ws_bytes dspark_attention_workspace_size(R, 0, max_rows, n_q_heads, n_kv_heads, head_dim)
+ * A request with a negative length, a position past max_blocks * page_size or a page id
+ * outside [0, pool_pages) gets NaN rows and is reported (DSPARK_ERR_DEVICE_INPUT); rows from
+ * cu_seqlens[R] on are not touched.  cu_seqlens that decreases, does not start at 0 or passes
+ * max_rows makes all max_rows rows NaN.  Limits (DSPARK_ERR_UNSUPPORTED): head_dim 64 or 128,
+ * at most 128 query heads to a key head, q, out and the caches 16-byte aligned.
+ */
+int dspark_verify_attention(const void* q, const void* k_cache, const void* v_cache,
+                            const int32_t* block_table, const int32_t* kv_len, const int32_t* cu_seqlens,
+                            float scale, int R, int max_rows, int n_q_heads, int n_kv_heads,
+                            int head_dim, int page_size, int max_blocks, int pool_pages, void* out,
+                            float* lse, unsigned flags, void* ws, size_t ws_bytes, int32_t* dev_status,
+                            dspark_stream_t stream);
+
+/*
+ * dspark_prefix_attention -- dspark_verify_attention for a batch whose requests
+ * share leading pages (a common system prompt): the shared keys are read once
+ * for all rows of a group, whose queries meet them in one dense product.
+ *
+ * Requests group_start[g] .. group_start[g + 1] - 1 form group g.  Their first
+ * shared_len[g] positions (a multiple of page_size, at most the kv_len of each of
+ * them, 0: nothing shared) lie in the same pages: the leading shared_len[g] /
+ * page_size entries of their block tables are equal, and those of the group's
+ * first request are the ones read.  Results are those of dspark_verify_attention
+ * on the same tables, up to the order of summation.
+ *
+ *   group_start  [n_groups + 1] int32, from 0 to R, non-decreasing;  shared_len [n_groups] int32
+ *   ws, ws_bytes dspark_attention_workspace_size(R, n_groups, max_rows, ...)
+ * A group whose shared_len breaks these rules, and a request whose kv_len is below it, get
+ * NaN rows and are reported; group_start that is not 0 .. R makes all rows NaN.  n_groups >= 1.
+ */
+int dspark_prefix_attention(const void* q, const void* k_cache, const void* v_cache,
+                            const int32_t* block_table, const int32_t* kv_len, const int32_t* cu_seqlens,
+                            const int32_t* group_start, const int32_t* shared_len, int n_groups,
+                            float scale, int R, int max_rows, int n_q_heads, int n_kv_heads,
+                            int head_dim, int page_size, int max_blocks, int pool_pages, void* out,
+                            float* lse, unsigned flags, void* ws, size_t ws_bytes, int32_t* dev_status,
+                            dspark_stream_t stream);
 
 /*
  * dspark_commit_lengths -- per-request commit and rollback counts

@@ -32,6 +32,9 @@ DSPARK_F32, DSPARK_BF16 = 0, 1
 DSPARK_OP_DRAFT, DSPARK_OP_VERIFY, DSPARK_OP_SELECT, DSPARK_OP_VERIFY_MARKOV, DSPARK_OP_CALIBRATE = 0, 1, 2, 3, 4
 DSPARK_OP_DRAFT_FUSED = 5
 DSPARK_FUSED_MAX_D = 16384
+DSPARK_HEADS_MAX_D = 256
+DSPARK_ROPE_INTERLEAVED = 1
+DSPARK_ATTN_FULL_BLOCK = 1
 DSPARK_DRAFT_FORCE_SIMT = 1
 DSPARK_VERIFY_HOST_TARGET = 1
 DSPARK_SELECT_FIXED, DSPARK_SELECT_HISTORY, DSPARK_SELECT_CURRENT, DSPARK_SELECT_FIRST_STOP = 0, 1, 2, 3
@@ -43,7 +46,8 @@ EXPORTED = ["dspark_status_string", "dspark_version", "dspark_workspace_size", "
             "dspark_select_prefix", "dspark_commit_lengths", "dspark_verify_static_scratch",
             "dspark_verify_markov", "dspark_set_wait_limit_ns", "dspark_set_fault_injection",
             "dspark_plan_cycles", "dspark_fit_temperatures", "dspark_kv_reserve", "dspark_kv_commit",
-            "dspark_markov_draft_fused"]
+            "dspark_markov_draft_fused", "dspark_qk_norm_rope", "dspark_kv_append",
+            "dspark_attention_workspace_size", "dspark_verify_attention", "dspark_prefix_attention"]
 
 
 class DSparkError(RuntimeError):
@@ -96,6 +100,19 @@ def _load():
     L.dspark_kv_reserve.restype = i32
     L.dspark_kv_commit.argtypes = [vp, vp, vp, i32, i32, vp, i32, vp, vp, i32, vp, vp]
     L.dspark_kv_commit.restype = i32
+    i64, u = ctypes.c_int64, ctypes.c_uint
+    L.dspark_qk_norm_rope.argtypes = [vp, i64, vp, i64, i32, vp, vp, f32, vp, vp, i32, i32, i32, i32, i32, vp, i64,
+                                      vp, i64, i32, u, vp, vp]
+    L.dspark_qk_norm_rope.restype = i32
+    L.dspark_kv_append.argtypes = [vp, i64, vp, i64, vp, i64, i32, vp, vp, f32, vp, i32, vp, vp, vp] + [i32] * 8 + \
+        [vp, vp, vp, i32, u, vp, vp]
+    L.dspark_kv_append.restype = i32
+    L.dspark_attention_workspace_size.argtypes = [i32] * 6
+    L.dspark_attention_workspace_size.restype = sz
+    L.dspark_verify_attention.argtypes = [vp] * 6 + [f32] + [i32] * 8 + [vp, vp, u, vp, sz, vp, vp]
+    L.dspark_verify_attention.restype = i32
+    L.dspark_prefix_attention.argtypes = [vp] * 8 + [i32, f32] + [i32] * 8 + [vp, vp, u, vp, sz, vp, vp]
+    L.dspark_prefix_attention.restype = i32
     L.dspark_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
     L.dspark_set_wait_limit_ns.restype = ctypes.c_uint64
     L.dspark_set_fault_injection.argtypes = [ctypes.c_uint]
@@ -405,6 +422,117 @@ def dspark_kv_commit(kv_len, l, n_accepted, page_size, block_table, free_pages, 
            _L.dspark_kv_commit(_ptr(kv_len), _ptr(l), _ptr(n_accepted), R, int(page_size), _ptr(block_table),
                                max_blocks, _ptr(free_pages), _ptr(free_top), free_pages.numel(), _ptr(dev_status),
                                _stream(stream)))
+
+
+def _rows(t, name, dtype=None, shape=None):
+    """A [rows, heads, head_dim] tensor whose rows may lie apart; the elements between rows."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must have shape {shape or '[rows, heads, head_dim]'}, got {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    rows, heads, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.stride(0) if rows > 1 else heads * d
+
+
+def dspark_qk_norm_rope(q, k, q_weight, k_weight, eps, positions, inv_freq, q_out, k_out, interleaved=False,
+                        dev_status=None, stream=None):
+    rows, hq, d = q.shape
+    hkv = k.shape[1]
+    q_stride = _rows(q, "q")
+    k_stride = _rows(k, "k", q.dtype, (rows, hkv, d))
+    qo_stride = _rows(q_out, "q_out", shape=(rows, hq, d))
+    ko_stride = _rows(k_out, "k_out", q_out.dtype, (rows, hkv, d))
+    _check(q_weight, "q_weight", q.dtype, (d,), allow_none=True)
+    _check(k_weight, "k_weight", q.dtype, (d,), allow_none=True)
+    _check(inv_freq, "inv_freq", torch.float32, allow_none=True)
+    _check(positions, "positions", torch.int32, (rows,), allow_none=inv_freq is None)
+    _check(dev_status, "dev_status", torch.int32, allow_none=True)
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    st = _L.dspark_qk_norm_rope(_ptr(q), q_stride, _ptr(k), k_stride, _dtype_code(q), _ptr(q_weight), _ptr(k_weight),
+                                float(eps), _ptr(positions), _ptr(inv_freq), rot, rows, hq, hkv, d, _ptr(q_out),
+                                qo_stride, _ptr(k_out), ko_stride, _dtype_code(q_out),
+                                DSPARK_ROPE_INTERLEAVED if interleaved else 0, _ptr(dev_status), _stream(stream))
+    _raise("dspark_qk_norm_rope", st)
+
+
+def dspark_kv_append(q, k, v, q_weight, k_weight, eps, inv_freq, cu_seqlens, kv_len, block_table, k_cache, v_cache,
+                     q_out, interleaved=False, dev_status=None, stream=None):
+    rows, hkv, d = k.shape
+    R, max_blocks = block_table.shape
+    pages, page_size = k_cache.shape[0], k_cache.shape[2]
+    k_stride = _rows(k, "k")
+    v_stride = _rows(v, "v", k.dtype, (rows, hkv, d))
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    hq = 0 if q is None else q.shape[1]
+    q_stride = 0 if q is None else _rows(q, "q", k.dtype, (rows, hq, d))
+    _check(q_out, "q_out", k_cache.dtype, (rows, hq, d), allow_none=True)
+    _check(q_weight, "q_weight", k.dtype, (d,), allow_none=True)
+    _check(k_weight, "k_weight", k.dtype, (d,), allow_none=True)
+    _check(inv_freq, "inv_freq", torch.float32, allow_none=True)
+    _check(cu_seqlens, "cu_seqlens", torch.int32, (R + 1,))
+    _check(kv_len, "kv_len", torch.int32, (R,))
+    _check(block_table, "block_table", torch.int32)
+    _check(k_cache, "k_cache", shape=(pages, hkv, page_size, d))
+    _check(v_cache, "v_cache", k_cache.dtype, (pages, hkv, page_size, d))
+    _check(dev_status, "dev_status", torch.int32, allow_none=True)
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    st = _L.dspark_kv_append(_ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride, _dtype_code(k), _ptr(q_weight),
+                             _ptr(k_weight), float(eps), _ptr(inv_freq), rot, _ptr(cu_seqlens), _ptr(kv_len),
+                             _ptr(block_table), R, rows, hq, hkv, d, page_size, max_blocks, pages, _ptr(k_cache),
+                             _ptr(v_cache), _ptr(q_out), _dtype_code(k_cache),
+                             DSPARK_ROPE_INTERLEAVED if interleaved else 0, _ptr(dev_status), _stream(stream))
+    _raise("dspark_kv_append", st)
+
+
+def dspark_attention_workspace_size(R, n_groups, max_rows, n_q_heads, n_kv_heads, head_dim) -> int:
+    return int(_L.dspark_attention_workspace_size(R, n_groups, max_rows, n_q_heads, n_kv_heads, head_dim))
+
+
+def _attention_args(q, k_cache, v_cache, block_table, kv_len, cu_seqlens, out, lse, ws, dev_status):
+    rows, hq, d = q.shape
+    R, max_blocks = block_table.shape
+    pages, hkv, page_size, _ = k_cache.shape
+    _check(q, "q", torch.bfloat16)
+    _check(k_cache, "k_cache", torch.bfloat16, (pages, hkv, page_size, d))
+    _check(v_cache, "v_cache", torch.bfloat16, (pages, hkv, page_size, d))
+    _check(block_table, "block_table", torch.int32)
+    _check(kv_len, "kv_len", torch.int32, (R,))
+    _check(cu_seqlens, "cu_seqlens", torch.int32, (R + 1,))
+    _check(out, "out", torch.bfloat16, (rows, hq, d))
+    _check(lse, "lse", torch.float32, (rows, hq), allow_none=True)
+    _check(ws, "ws", torch.uint8)
+    _check(dev_status, "dev_status", torch.int32, allow_none=True)
+    return (R, rows, hq, hkv, d, page_size, max_blocks, pages)
+
+
+def dspark_verify_attention(q, k_cache, v_cache, block_table, kv_len, cu_seqlens, scale, out, lse=None,
+                            full_block=False, ws=None, dev_status=None, stream=None):
+    sizes = _attention_args(q, k_cache, v_cache, block_table, kv_len, cu_seqlens, out, lse, ws, dev_status)
+    st = _L.dspark_verify_attention(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(kv_len),
+                                    _ptr(cu_seqlens), float(scale), *sizes, _ptr(out), _ptr(lse),
+                                    DSPARK_ATTN_FULL_BLOCK if full_block else 0, _ptr(ws), ws.numel(),
+                                    _ptr(dev_status), _stream(stream))
+    _raise("dspark_verify_attention", st)
+
+
+def dspark_prefix_attention(q, k_cache, v_cache, block_table, kv_len, cu_seqlens, group_start, shared_len, scale, out,
+                            lse=None, full_block=False, ws=None, dev_status=None, stream=None):
+    sizes = _attention_args(q, k_cache, v_cache, block_table, kv_len, cu_seqlens, out, lse, ws, dev_status)
+    n_groups = shared_len.numel()
+    _check(group_start, "group_start", torch.int32, (n_groups + 1,))
+    _check(shared_len, "shared_len", torch.int32)
+    st = _L.dspark_prefix_attention(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(kv_len),
+                                    _ptr(cu_seqlens), _ptr(group_start), _ptr(shared_len), n_groups, float(scale),
+                                    *sizes, _ptr(out), _ptr(lse), DSPARK_ATTN_FULL_BLOCK if full_block else 0,
+                                    _ptr(ws), ws.numel(), _ptr(dev_status), _stream(stream))
+    _raise("dspark_prefix_attention", st)
 
 
 def dspark_philox4x32_10(ctr, keys, out, stream=None):

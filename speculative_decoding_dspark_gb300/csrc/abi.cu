@@ -5,6 +5,7 @@
 // synchronises or throws; the only state is the pair of process-wide wait
 // settings (limit of the grid-wide waits, test injection), read at each call.
 #include <atomic>
+#include <cmath>
 #include <cstring>
 
 #include "kernels.cuh"
@@ -85,6 +86,43 @@ Residence residence(const void* ptr) {
     return Residence::kOther;
 }
 
+// What dspark_qk_norm_rope and dspark_kv_append ask of sizes, strides and alignment.
+int check_heads(const HeadsParams& p) {
+    if (!valid_dtype(p.in_dtype) || !valid_dtype(p.out_dtype)) return DSPARK_ERR_INVALID_ARG;
+    if (p.rows < 0 || p.hq < 0 || p.hkv <= 0 || p.d <= 0 || p.rot < 0 || p.rot > p.d || p.rot % 2) return DSPARK_ERR_INVALID_ARG;
+    if (!(p.eps >= 0.0f) || p.eps == INFINITY) return DSPARK_ERR_INVALID_ARG;
+    if (p.rot > 0 && !p.inv_freq) return DSPARK_ERR_INVALID_ARG;
+    const int64_t nq = (int64_t)p.hq * p.d, nkv = (int64_t)p.hkv * p.d;
+    if ((p.hq && (p.q_stride < nq || p.q_out_stride < nq)) || p.k_stride < nkv || (p.v && p.v_stride < nkv) ||
+        (p.k_out && p.k_out_stride < nkv))
+        return DSPARK_ERR_INVALID_ARG;
+    if (p.d % 8 || p.d > DSPARK_HEADS_MAX_D || p.rot % 16 || p.hq > (1 << 20) || p.hkv > (1 << 20)) return DSPARK_ERR_UNSUPPORTED;
+    const int in16 = p.in_dtype == DSPARK_F32 ? 4 : 8, out16 = p.out_dtype == DSPARK_F32 ? 4 : 8;  // elements in 16 bytes
+    if ((p.hq && (p.q_stride % in16 || p.q_out_stride % out16)) || p.k_stride % in16 || (p.v && p.v_stride % in16) ||
+        (p.k_out && p.k_out_stride % out16))
+        return DSPARK_ERR_UNSUPPORTED;
+    for (const void* x : {p.q, p.k, p.v, p.wq, p.wk, (const void*)p.q_out, (const void*)p.k_out,
+                          (const void*)p.k_cache, (const void*)p.v_cache})
+        if (!aligned16(x)) return DSPARK_ERR_UNSUPPORTED;
+    return DSPARK_OK;
+}
+
+int attention_call(AttnParams& p, size_t ws_bytes, unsigned flags, cudaStream_t stream) {
+    if (!p.k_cache || !p.v_cache || !p.block_table || !p.kv_len || !p.cu || (p.rows != 0 && (!p.q || !p.out)))
+        return DSPARK_ERR_INVALID_ARG;
+    if (p.R <= 0 || p.rows < 0 || p.hq <= 0 || p.hkv <= 0 || p.d <= 0 || p.page <= 0 || p.max_blocks <= 0 || p.pool_pages < 0)
+        return DSPARK_ERR_INVALID_ARG;
+    if (p.hq % p.hkv || !(fabsf(p.scale) <= 3.4e38f) || (flags & ~DSPARK_ATTN_FULL_BLOCK)) return DSPARK_ERR_INVALID_ARG;
+    if ((p.d != 64 && p.d != 128) || p.hq / p.hkv > 128) return DSPARK_ERR_UNSUPPORTED;
+    if (!aligned16(p.q) || !aligned16(p.k_cache) || !aligned16(p.v_cache) || !aligned16(p.out)) return DSPARK_ERR_UNSUPPORTED;
+    if (!p.ws || (reinterpret_cast<uintptr_t>(p.ws) % kAlign) != 0) return DSPARK_ERR_WORKSPACE;
+    const size_t need = attention_workspace(p.R, p.n_groups, p.rows, p.hq, p.hkv, p.d);
+    if (need == 0) return DSPARK_ERR_UNSUPPORTED;
+    if (ws_bytes < need) return DSPARK_ERR_WORKSPACE;
+    p.full_block = (flags & DSPARK_ATTN_FULL_BLOCK) != 0;
+    return p.rows == 0 ? DSPARK_OK : cuda_status(launch_attention(p, stream));
+}
+
 // Process-wide settings of the grid-wide waits (see dspark_set_wait_limit_ns).
 constexpr unsigned long long kDefaultWaitNs = 2000000000ull;
 std::atomic<unsigned long long> g_wait_ns{kDefaultWaitNs};
@@ -123,7 +161,7 @@ const char* dspark_status_string(int status) {
     }
 }
 
-int dspark_version(void) { return 10200; }
+int dspark_version(void) { return 10300; }
 
 int dspark_markov_draft_uses_tensor_cores(int u_dtype, int w_dtype, int R, int V, int rank,
                                           unsigned flags) {
@@ -413,6 +451,98 @@ int dspark_kv_commit(int32_t* kv_len, const int32_t* l, const int32_t* n_accepte
     if (R <= 0 || page_size <= 0 || max_blocks <= 0 || pool_pages < 0) return DSPARK_ERR_INVALID_ARG;
     return cuda_status(launch_kv_commit(kv_len, l, n_accepted, R, page_size, block_table, max_blocks, free_pages,
                                         free_top, pool_pages, dev_status, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int dspark_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int in_dtype,
+                        const void* q_weight, const void* k_weight, float eps, const int32_t* positions,
+                        const float* inv_freq, int rot_dim, int rows, int n_q_heads, int n_kv_heads,
+                        int head_dim, void* q_out, int64_t q_out_stride, void* k_out,
+                        int64_t k_out_stride, int out_dtype, unsigned flags, int32_t* dev_status,
+                        dspark_stream_t stream) {
+    if (rows != 0 && (!q || !k || !q_out || !k_out)) return DSPARK_ERR_INVALID_ARG;
+    if (n_q_heads <= 0 || (rot_dim > 0 && rows != 0 && !positions)) return DSPARK_ERR_INVALID_ARG;
+    if ((flags & ~DSPARK_ROPE_INTERLEAVED) != 0) return DSPARK_ERR_INVALID_ARG;
+    HeadsParams p{};
+    p.q = q; p.k = k; p.q_stride = q_stride; p.k_stride = k_stride; p.in_dtype = in_dtype; p.out_dtype = out_dtype;
+    p.wq = q_weight; p.wk = k_weight; p.eps = eps; p.inv_freq = inv_freq; p.rot = rot_dim;
+    p.pairs = (flags & DSPARK_ROPE_INTERLEAVED) != 0;
+    p.rows = rows; p.hq = n_q_heads; p.hkv = n_kv_heads; p.d = head_dim;
+    p.q_out = q_out; p.k_out = k_out; p.q_out_stride = q_out_stride; p.k_out_stride = k_out_stride;
+    p.positions = positions; p.dev_status = dev_status;
+    const int st = check_heads(p);
+    if (st != DSPARK_OK || rows == 0) return st;
+    return cuda_status(launch_heads(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int dspark_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                     int64_t v_stride, int in_dtype, const void* q_weight, const void* k_weight,
+                     float eps, const float* inv_freq, int rot_dim, const int32_t* cu_seqlens,
+                     const int32_t* kv_len, const int32_t* block_table, int R, int max_rows,
+                     int n_q_heads, int n_kv_heads, int head_dim, int page_size, int max_blocks,
+                     int pool_pages, void* k_cache, void* v_cache, void* q_out, int out_dtype,
+                     unsigned flags, int32_t* dev_status, dspark_stream_t stream) {
+    if (!cu_seqlens || !kv_len || !block_table || !k_cache || !v_cache) return DSPARK_ERR_INVALID_ARG;
+    if (n_q_heads < 0) return DSPARK_ERR_INVALID_ARG;
+    if (max_rows != 0 && (!k || !v || (n_q_heads > 0) != (q != nullptr) || (n_q_heads > 0) != (q_out != nullptr)))
+        return DSPARK_ERR_INVALID_ARG;
+    if (R <= 0 || page_size <= 0 || max_blocks <= 0 || pool_pages < 0) return DSPARK_ERR_INVALID_ARG;
+    if ((flags & ~DSPARK_ROPE_INTERLEAVED) != 0) return DSPARK_ERR_INVALID_ARG;
+    HeadsParams p{};
+    p.q = q; p.k = k; p.v = v; p.q_stride = q_stride; p.k_stride = k_stride; p.v_stride = v_stride;
+    p.in_dtype = in_dtype; p.out_dtype = out_dtype;
+    p.wq = q_weight; p.wk = k_weight; p.eps = eps; p.inv_freq = inv_freq; p.rot = rot_dim;
+    p.pairs = (flags & DSPARK_ROPE_INTERLEAVED) != 0;
+    p.rows = max_rows; p.hq = n_q_heads; p.hkv = n_kv_heads; p.d = head_dim;
+    p.q_out = q_out; p.q_out_stride = (int64_t)n_q_heads * head_dim;
+    p.cu = cu_seqlens; p.kv_len = kv_len; p.block_table = block_table; p.R = R; p.page = page_size;
+    p.max_blocks = max_blocks; p.pool_pages = pool_pages; p.k_cache = k_cache; p.v_cache = v_cache;
+    p.dev_status = dev_status;
+    const int st = check_heads(p);
+    if (st != DSPARK_OK || max_rows == 0) return st;
+    return cuda_status(launch_heads(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t dspark_attention_workspace_size(int R, int n_groups, int max_rows, int n_q_heads, int n_kv_heads,
+                                       int head_dim) {
+    if (R <= 0 || n_groups < 0 || max_rows < 0 || n_q_heads <= 0 || n_kv_heads <= 0 || n_q_heads % n_kv_heads ||
+        (head_dim != 64 && head_dim != 128))
+        return 0;
+    return attention_workspace(R, n_groups, max_rows, n_q_heads, n_kv_heads, head_dim);
+}
+
+int dspark_verify_attention(const void* q, const void* k_cache, const void* v_cache,
+                            const int32_t* block_table, const int32_t* kv_len, const int32_t* cu_seqlens,
+                            float scale, int R, int max_rows, int n_q_heads, int n_kv_heads,
+                            int head_dim, int page_size, int max_blocks, int pool_pages, void* out,
+                            float* lse, unsigned flags, void* ws, size_t ws_bytes, int32_t* dev_status,
+                            dspark_stream_t stream) {
+    AttnParams p{};
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.k_cache = static_cast<const __nv_bfloat16*>(k_cache); p.v_cache = static_cast<const __nv_bfloat16*>(v_cache);
+    p.block_table = block_table; p.kv_len = kv_len; p.cu = cu_seqlens; p.scale = scale;
+    p.R = R; p.rows = max_rows; p.hq = n_q_heads; p.hkv = n_kv_heads; p.d = head_dim;
+    p.page = page_size; p.max_blocks = max_blocks; p.pool_pages = pool_pages;
+    p.out = static_cast<__nv_bfloat16*>(out); p.lse = lse; p.dev_status = dev_status; p.ws = ws;
+    return attention_call(p, ws_bytes, flags, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int dspark_prefix_attention(const void* q, const void* k_cache, const void* v_cache,
+                            const int32_t* block_table, const int32_t* kv_len, const int32_t* cu_seqlens,
+                            const int32_t* group_start, const int32_t* shared_len, int n_groups,
+                            float scale, int R, int max_rows, int n_q_heads, int n_kv_heads,
+                            int head_dim, int page_size, int max_blocks, int pool_pages, void* out,
+                            float* lse, unsigned flags, void* ws, size_t ws_bytes, int32_t* dev_status,
+                            dspark_stream_t stream) {
+    if (!group_start || !shared_len || n_groups < 1) return DSPARK_ERR_INVALID_ARG;
+    AttnParams p{};
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.k_cache = static_cast<const __nv_bfloat16*>(k_cache); p.v_cache = static_cast<const __nv_bfloat16*>(v_cache);
+    p.block_table = block_table; p.kv_len = kv_len; p.cu = cu_seqlens; p.scale = scale;
+    p.group_start = group_start; p.shared_len = shared_len; p.n_groups = n_groups;
+    p.R = R; p.rows = max_rows; p.hq = n_q_heads; p.hkv = n_kv_heads; p.d = head_dim;
+    p.page = page_size; p.max_blocks = max_blocks; p.pool_pages = pool_pages;
+    p.out = static_cast<__nv_bfloat16*>(out); p.lse = lse; p.dev_status = dev_status; p.ws = ws;
+    return attention_call(p, ws_bytes, flags, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int dspark_philox4x32_10(const uint32_t* ctr, const uint64_t* keys, int n, uint32_t* out,

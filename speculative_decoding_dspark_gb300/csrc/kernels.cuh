@@ -185,6 +185,50 @@ cudaError_t launch_kv_commit(int32_t* kv_len, const int32_t* l, const int32_t* n
                              int max_blocks, int32_t* free_pages, int32_t* free_top, int pool_pages,
                              int32_t* dev_status, cudaStream_t stream);
 
+// ----------------------------------------------------------------------------
+// Query, key and value heads: norm, rotation, append to the paged cache
+// ----------------------------------------------------------------------------
+struct HeadsParams {
+    const void *q, *k, *v;  // v: append only (else NULL)
+    int64_t q_stride, k_stride, v_stride;  // elements between rows
+    int in_dtype, out_dtype;
+    const void *wq, *wk;    // [d] in_dtype, or NULL: no norm
+    float eps;
+    const float* inv_freq;
+    int rot, pairs;
+    int rows, hq, hkv, d;   // hq = 0: keys and values alone
+    void *q_out, *k_out;
+    int64_t q_out_stride, k_out_stride;
+    const int32_t* positions;
+    // append
+    const int32_t *cu, *kv_len, *block_table;
+    int R, page, max_blocks, pool_pages;
+    void *k_cache, *v_cache;
+    int32_t* dev_status;
+};
+
+cudaError_t launch_heads(const HeadsParams& p, cudaStream_t stream);
+
+// ----------------------------------------------------------------------------
+// Attention of the verify rows over the paged cache
+// ----------------------------------------------------------------------------
+struct AttnParams {
+    const __nv_bfloat16 *q, *k_cache, *v_cache;
+    const int32_t *block_table, *kv_len, *cu;
+    const int32_t *group_start, *shared_len;  // NULL: no shared pages
+    int n_groups;
+    float scale;
+    int full_block;
+    int R, rows, hq, hkv, d, page, max_blocks, pool_pages;
+    __nv_bfloat16* out;
+    float* lse;
+    int32_t* dev_status;
+    void* ws;
+};
+
+size_t attention_workspace(int R, int n_groups, int rows, int hq, int hkv, int d);
+cudaError_t launch_attention(const AttnParams& p, cudaStream_t stream);
+
 cudaError_t launch_commit(const int32_t* n_acc, const int32_t* l, int R, int gamma,
                           int32_t* commit_len, int32_t* cu_commit, int32_t* discard,
                           int32_t* total, int32_t* dev_status, cudaStream_t stream);
