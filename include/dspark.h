@@ -600,7 +600,7 @@ size_t dspark_attention_workspace_size(int R, int n_groups, int max_rows, int n_
  * Over the positions j the row sees, j <= kv_len[r] + i (with
  * DSPARK_ATTN_FULL_BLOCK: j < kv_len[r] + n, for a drafter whose block positions
  * see each other both ways):
- *   s_j = scale * q . K[j],  lse = log sum_j exp(s_j),  out = sum_j exp(s_j - lse) V[j]
+ *   s_j = scale * q . K[j] (scale >= 0),  lse = log sum_j exp(s_j),  out = sum_j exp(s_j - lse) V[j]
  * What lies in the pages past a request's last position, and what a row does not
  * see, has no influence on it, NaN and infinities among it.
  *
@@ -613,7 +613,8 @@ size_t dspark_attention_workspace_size(int R, int n_groups, int max_rows, int n_
  * outside [0, pool_pages) gets NaN rows and is reported (DSPARK_ERR_DEVICE_INPUT); rows from
  * cu_seqlens[R] on are not touched.  cu_seqlens that decreases, does not start at 0 or passes
  * max_rows makes all max_rows rows NaN.  Limits (DSPARK_ERR_UNSUPPORTED): head_dim 64 or 128,
- * at most 128 query heads to a key head, q, out and the caches 16-byte aligned.
+ * at most 128 query heads to a key head, pool_pages * n_kv_heads * page_size < 2^32 - 1,
+ * max_rows * n_q_heads < 2^31, q, out and the caches 16-byte aligned.
  */
 int dspark_verify_attention(const void* q, const void* k_cache, const void* v_cache,
                             const int32_t* block_table, const int32_t* kv_len, const int32_t* cu_seqlens,

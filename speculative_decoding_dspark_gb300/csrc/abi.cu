@@ -112,8 +112,10 @@ int attention_call(AttnParams& p, size_t ws_bytes, unsigned flags, cudaStream_t 
         return DSPARK_ERR_INVALID_ARG;
     if (p.R <= 0 || p.rows < 0 || p.hq <= 0 || p.hkv <= 0 || p.d <= 0 || p.page <= 0 || p.max_blocks <= 0 || p.pool_pages < 0)
         return DSPARK_ERR_INVALID_ARG;
-    if (p.hq % p.hkv || !(fabsf(p.scale) <= 3.4e38f) || (flags & ~DSPARK_ATTN_FULL_BLOCK)) return DSPARK_ERR_INVALID_ARG;
+    if (p.hq % p.hkv || !(p.scale >= 0.0f) || p.scale == INFINITY || (flags & ~DSPARK_ATTN_FULL_BLOCK)) return DSPARK_ERR_INVALID_ARG;
     if ((p.d != 64 && p.d != 128) || p.hq / p.hkv > 128) return DSPARK_ERR_UNSUPPORTED;
+    // cache rows are counted in 32 bits
+    if ((double)p.pool_pages * p.hkv * p.page >= 4294967295.0 || (long long)p.rows * p.hq >= (1LL << 31)) return DSPARK_ERR_UNSUPPORTED;
     if (!aligned16(p.q) || !aligned16(p.k_cache) || !aligned16(p.v_cache) || !aligned16(p.out)) return DSPARK_ERR_UNSUPPORTED;
     if (!p.ws || (reinterpret_cast<uintptr_t>(p.ws) % kAlign) != 0) return DSPARK_ERR_WORKSPACE;
     const size_t need = attention_workspace(p.R, p.n_groups, p.rows, p.hq, p.hkv, p.d);

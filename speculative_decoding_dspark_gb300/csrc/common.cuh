@@ -152,6 +152,22 @@ __device__ __forceinline__ T shfl_xor(T v, int m) {
     return __shfl_xor_sync(0xFFFFFFFFu, v, m);
 }
 
+// The request that owns `row`: the last r with cu[r] <= row, 32 candidates at a
+// time.  All lanes of the warp call it together.
+__device__ __forceinline__ int owner_of(const int32_t* cu, int R, int row) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, n = R;  // the answer is in [lo, lo + n)
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const int at = lo + lane * step;
+        const unsigned m = __ballot_sync(0xFFFFFFFFu, lane * step < n && cu[at] <= row);
+        const int last = m ? 31 - __clz(m) : 0;
+        n = min(step, n - last * step);
+        lo += last * step;
+    }
+    return lo;
+}
+
 // Global-time based bound for device spin waits (nanoseconds).
 __device__ __forceinline__ uint64_t global_ns() {
     uint64_t t;

@@ -60,22 +60,6 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
     *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(v);
 }
 
-// The request that owns `row`: the last r with cu[r] <= row, 32 candidates at a
-// time.  All lanes of the warp call it together.
-__device__ __forceinline__ int owner(const int32_t* cu, int R, int row) {
-    const int lane = threadIdx.x & 31;
-    int lo = 0, n = R;  // the answer is in [lo, lo + n)
-    while (n > 1) {
-        const int step = (n + 31) / 32;
-        const int at = lo + lane * step;
-        const unsigned m = __ballot_sync(0xFFFFFFFFu, lane * step < n && cu[at] <= row);
-        const int last = m ? 31 - __clz(m) : 0;
-        n = min(step, n - last * step);
-        lo += last * step;
-    }
-    return lo;
-}
-
 template <typename TIn, typename TOut, bool kPairs, bool kAppend>
 __global__ void __launch_bounds__(kHeadThreads) heads_kernel(const HeadsParams p, int rows_per_cta, int lanes) {
     extern __shared__ float2 turn_smem[];  // [rows_per_cta][rot / 2] cosine, sine
@@ -116,7 +100,7 @@ __global__ void __launch_bounds__(kHeadThreads) heads_kernel(const HeadsParams p
         long long pos = 0;
         RowPlace at{-1, 0, 0};
         if (kAppend) {
-            const int r = owner(p.cu, p.R, row);
+            const int r = owner_of(p.cu, p.R, row);
             const int lo = p.cu[r], hi = p.cu[r + 1], len = p.kv_len[r];
             if (row == 0 && lane == 0 && (p.cu[0] != 0 || p.cu[p.R] > p.rows || p.cu[p.R] < 0))
                 report(p.dev_status, DSPARK_ERR_DEVICE_INPUT);

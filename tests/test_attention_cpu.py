@@ -91,8 +91,8 @@ def test_heads_refusals_of_one_call(lib):
 @pytest.mark.parametrize("change,status", [
     (dict(q=None), INVALID), (dict(table=None), INVALID), (dict(out=None), INVALID), (dict(R=0), INVALID),
     (dict(rows=-1), INVALID), (dict(hq=9), INVALID), (dict(page=0), INVALID), (dict(blocks=0), INVALID),
-    (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID), (dict(flags=2), INVALID),
-    (dict(pool=-1), INVALID), (dict(d=96), UNSUPPORTED), (dict(hq=258), UNSUPPORTED), (dict(q=vp(4104)), UNSUPPORTED),
+    (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID), (dict(scale=-0.1), INVALID), (dict(flags=2), INVALID),
+    (dict(pool=-1), INVALID), (dict(d=96), UNSUPPORTED), (dict(hq=258), UNSUPPORTED), (dict(pool=1 << 30), UNSUPPORTED), (dict(rows=1 << 29), UNSUPPORTED), (dict(q=vp(4104)), UNSUPPORTED),
     (dict(v=vp(4098)), UNSUPPORTED), (dict(ws=None), WORKSPACE), (dict(ws=vp(4100)), WORKSPACE),
     (dict(ws_bytes=16), WORKSPACE), (dict(rows=0), 0),
 ])
