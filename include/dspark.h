@@ -543,7 +543,7 @@ int dspark_kv_commit(int32_t* kv_len, const int32_t* l, const int32_t* n_accepte
  *   q_out, k_out shaped as q and k, out_dtype, with row strides of their own.  They may be
  *                q and k themselves (same pointer, stride and type).
  * rows == 0 does nothing.  Limits (DSPARK_ERR_UNSUPPORTED): head_dim % 8 == 0 up to
- * DSPARK_HEADS_MAX_D, rot_dim % 16 == 0; every pointer but positions and inv_freq 16-byte
+ * DSPARK_HEADS_MAX_D, rot_dim % 16 == 0, at most 4096 heads of a kind; every pointer but positions and inv_freq 16-byte
  * aligned, every stride a multiple of 16 bytes.
  */
 int dspark_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int in_dtype,
@@ -613,7 +613,7 @@ size_t dspark_attention_workspace_size(int R, int n_groups, int max_rows, int n_
  * outside [0, pool_pages) gets NaN rows and is reported (DSPARK_ERR_DEVICE_INPUT); rows from
  * cu_seqlens[R] on are not touched.  cu_seqlens that decreases, does not start at 0 or passes
  * max_rows makes all max_rows rows NaN.  Limits (DSPARK_ERR_UNSUPPORTED): head_dim 64 or 128,
- * at most 128 query heads to a key head, pool_pages * n_kv_heads * page_size < 2^32 - 1,
+ * at most 128 query heads to a key head, pool_pages * n_kv_heads * page_size < 2^31 - 1,
  * max_rows * n_q_heads < 2^31, q, out and the caches 16-byte aligned.
  */
 int dspark_verify_attention(const void* q, const void* k_cache, const void* v_cache,

@@ -96,7 +96,7 @@ int check_heads(const HeadsParams& p) {
     if ((p.hq && (p.q_stride < nq || p.q_out_stride < nq)) || p.k_stride < nkv || (p.v && p.v_stride < nkv) ||
         (p.k_out && p.k_out_stride < nkv))
         return DSPARK_ERR_INVALID_ARG;
-    if (p.d % 8 || p.d > DSPARK_HEADS_MAX_D || p.rot % 16 || p.hq > (1 << 20) || p.hkv > (1 << 20)) return DSPARK_ERR_UNSUPPORTED;
+    if (p.d % 8 || p.d > DSPARK_HEADS_MAX_D || p.rot % 16 || p.hq > 4096 || p.hkv > 4096) return DSPARK_ERR_UNSUPPORTED;
     const int in16 = p.in_dtype == DSPARK_F32 ? 4 : 8, out16 = p.out_dtype == DSPARK_F32 ? 4 : 8;  // elements in 16 bytes
     if ((p.hq && (p.q_stride % in16 || p.q_out_stride % out16)) || p.k_stride % in16 || (p.v && p.v_stride % in16) ||
         (p.k_out && p.k_out_stride % out16))
@@ -114,8 +114,8 @@ int attention_call(AttnParams& p, size_t ws_bytes, unsigned flags, cudaStream_t 
         return DSPARK_ERR_INVALID_ARG;
     if (p.hq % p.hkv || !(p.scale >= 0.0f) || p.scale == INFINITY || (flags & ~DSPARK_ATTN_FULL_BLOCK)) return DSPARK_ERR_INVALID_ARG;
     if ((p.d != 64 && p.d != 128) || p.hq / p.hkv > 128) return DSPARK_ERR_UNSUPPORTED;
-    // cache rows are counted in 32 bits
-    if ((double)p.pool_pages * p.hkv * p.page >= 4294967295.0 || (long long)p.rows * p.hq >= (1LL << 31)) return DSPARK_ERR_UNSUPPORTED;
+    // rows of the cache are counted in 31 bits
+    if ((double)p.pool_pages * p.hkv * p.page >= 2147483647.0 || (long long)p.rows * p.hq >= (1LL << 31)) return DSPARK_ERR_UNSUPPORTED;
     if (!aligned16(p.q) || !aligned16(p.k_cache) || !aligned16(p.v_cache) || !aligned16(p.out)) return DSPARK_ERR_UNSUPPORTED;
     if (!p.ws || (reinterpret_cast<uintptr_t>(p.ws) % kAlign) != 0) return DSPARK_ERR_WORKSPACE;
     const size_t need = attention_workspace(p.R, p.n_groups, p.rows, p.hq, p.hkv, p.d);

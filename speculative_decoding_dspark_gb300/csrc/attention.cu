@@ -9,63 +9,90 @@
 // sum_j 2^{x_j - m} and sum_j 2^{x_j - m} V[j] with x = s log2(e); triples of
 // disjoint parts add up after scaling each by 2^{m - max m}.
 //
-// An item is 128 rows of one key head: the rows of a request (of a group, over
-// its shared pages) by query heads of that key head, so that a key read once
-// serves them all.  Its keys go by in blocks of 128:
+// An item is up to 256 rows of one key head: the rows of a request (of a group,
+// over its shared pages) by query heads of that key head, so that a key read
+// once serves them all.  Its keys go by in blocks of 128, and a step is one
+// block against one tile of 128 rows:
 //   S = Q K^T     tcgen05, 128 x 128, fp32 in tensor memory
 //   P = 2^(x - m) one thread a row: the row's maximum, 128 exponentials, the
 //                 sum; P goes back to tensor memory in bf16 over S
 //   O += P V      tcgen05 with P from tensor memory, 128 x d, fp32
+// Two tiles are in work at a time, so that the tensor cores have the one's
+// products while the other's exponentials are formed: of an item of more than
+// 128 rows its two halves over the same block, else the same rows over
+// alternating blocks, whose two triples are added at the end (both lie in the
+// same lanes of tensor memory).
+//
 // The reference m of a row moves only when the maximum has grown by more than
 // 2^8 (O is rescaled then): P stays below 2^8 and fp32 sums lose nothing.
 // P is the one rounding to fewer bits besides the output: 2^-8 of each weight
 // at most, and l adds the weights before it.
 //
+// One CTA per SM, sixteen warps: 0-3 and 4-7 form the exponentials of the two
+// tiles, 8-11 and 15 load, 12 issues the products, 13 walks along the items, 14
+// looks at blocks of values that not every row sees whole.  Keys and values come
+// through a ring of 160 KB, queries through two buffers, so that the next item's
+// first product does not wait for the last one's output.  Pages of a multiple of
+// 8 slots come by TMA, each lane of warp 15 having a box of up to 128 rows by 64
+// elements inside one page.  Other pages may end anywhere in a block: their rows
+// are gathered by 16-byte copies (warps 8-11, a row to a lane), which have about
+// 64 KB in flight per SM where TMA has the whole ring (949 MB of keys and values:
+// 200 us).  Four rows to a TMA gather would move 6.4 bytes a cycle (500 us).
+//
 // Splitting: the blocks of all items form one line, which is cut into equal
-// pieces, one per CTA (two CTAs per SM; each item costs a block more, for its
-// queries and output).  An item that is cut leaves (m, l, O) in the workspace
-// and a second kernel joins its pieces in their order.  The cut depends on the
-// lengths, which only the device knows: every CTA scans them itself.
+// pieces, one per CTA (each item costs a block more, for its queries and
+// output).  An item that is cut leaves its triples in the workspace and a second
+// kernel joins them in their order.  The cut depends on the lengths, which only
+// the device knows: every CTA scans them itself.
+#include <type_traits>
+
 #include "kernels.cuh"
 #include "tc_ptx.cuh"
 
 namespace dspark {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kTile = 128;   // rows of an item
+constexpr int kThreads = 512;
+constexpr int kLoaders = 128;
+constexpr int kTile = 128;   // rows of a tile
+constexpr int kRows = 256;   // rows of an item
 constexpr int kBlock = 128;  // keys of a block
-constexpr int kItemCost = 1;
-constexpr int kMaxCtas = 304;            // two per SM
-constexpr uint32_t kNoSlot = 0xFFFFFFFFu;
+constexpr int kItemCost = 4;  // blocks that an item costs besides its own: 1, 2, 4, 8 measured 269, 249, 251, 266 us for 128 ragged requests, 228, 209, 192, 192 behind a prefix
+constexpr int kMaxCtas = 152;            // one per SM
 constexpr float kGrowth = 8.0f;
-constexpr uint64_t kWaitNs = 2000000000ull;  // of a CTA on its own tensor-core operations
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // ---------------------------------------------------------------- the plan
-// Workspace of one launch: where each entry's (request's or group's) work
-// begins on the line, and the pieces of items that were cut.
+// A cut item, by the CTA that has its first blocks.
+struct Job {
+    int n_rows;         // of the item (0: this CTA began none that it did not finish)
+    int first, last;    // CTAs that have a piece
+    int row0, tile_row; // rows of q of the entry, and the item's first (row, query head) of it
+    int head;           // key head
+    int merge_prefix;   // the rows have a shared part too
+    int pad;
+};
+
+// Workspace of one launch.
 struct Plan {
-    int* bad;            // cu or group_start is not what it has to be
-    long long* start;    // [entries + 1]
-    float* part;         // [2 * ctas][kTile][d]  slot 2c: the item cut before CTA c's piece, 2c + 1: after it
-    float2* part_ml;     // [2 * ctas][kTile]
-    float* whole;        // groups only, [rows, hq, d]: items that were not cut
-    float2* whole_ml;    // [rows, hq]
+    Job* jobs;           // [ctas]
+    float* part;         // [2 * ctas][d / 4][kRows][4]  slot 2c: the item cut before CTA c's piece, 2c + 1: after it
+    float2* part_ml;     // [2 * ctas][kRows]
+    float* whole;        // groups only, [hkv][d / 4][rows * g][4]: the shared part's sums of every row
+    float2* whole_ml;    // [hkv][rows * g]
 };
 
 struct Entry {     // a request's own keys, or a group's shared ones
     int row0, n;   // its rows of q (0: nothing to do)
     int begin;     // first key
     int end;       // past the last key any of its rows sees
-    int len;       // causal: row i sees keys below len + i + 1
-    int causal;
+    int len;       // row i sees keys below len + i + 1 (-1: all rows see the same keys)
     int table;     // the block table's row
     int tiles, blocks;
     __device__ long long items(int hkv) const { return (long long)tiles * hkv; }
     __device__ long long cost(int hkv) const { return items(hkv) * (blocks + kItemCost); }
     // past the last key seen by row i of the entry
-    __device__ int limit(int i) const { return causal ? len + i + 1 : end; }
+    __device__ int limit(int i) const { return len < 0 ? end : len + i + 1; }
 };
 
 __device__ __forceinline__ int group_of(const AttnParams& p, int r) {
@@ -92,7 +119,6 @@ __device__ __forceinline__ bool request_ok(const AttnParams& p, int len, int n, 
 template <bool kGroups>
 __device__ __forceinline__ Entry entry_of(const AttnParams& p, int e) {
     Entry x;
-    x.causal = 0;
     x.begin = 0;
     if (kGroups) {
         const int r0 = p.group_start[e], r1 = p.group_start[e + 1];
@@ -100,7 +126,8 @@ __device__ __forceinline__ Entry entry_of(const AttnParams& p, int e) {
         x.table = r0;
         x.row0 = p.cu[r0];
         x.n = p.cu[r1] - x.row0;
-        x.len = x.end = s;
+        x.len = -1;
+        x.end = s;
         if (s <= 0 || s % p.page || (long long)s > (long long)p.max_blocks * p.page || s >= INT_MAX - kBlock) x.n = 0;
     } else {
         const int lo = p.cu[e], n = p.cu[e + 1] - lo, len = p.kv_len[e];
@@ -109,14 +136,13 @@ __device__ __forceinline__ Entry entry_of(const AttnParams& p, int e) {
         x.row0 = lo;
         x.n = request_ok(p, len, n, shared) ? n : 0;
         x.begin = shared;
-        x.len = len;
+        x.len = p.full_block ? -1 : len;
         x.end = len + n;
-        x.causal = !p.full_block;
     }
     if (x.n <= 0) {
         x.n = x.tiles = x.blocks = 0;
     } else {
-        x.tiles = (int)(((long long)x.n * (p.hq / p.hkv) + kTile - 1) / kTile);
+        x.tiles = (int)(((long long)x.n * (p.hq / p.hkv) + kRows - 1) / kRows);
         x.blocks = (x.end - x.begin + kBlock - 1) / kBlock;
     }
     return x;
@@ -124,18 +150,37 @@ __device__ __forceinline__ Entry entry_of(const AttnParams& p, int e) {
 
 // Blocks of tile t of an entry that some row of it sees.
 __device__ __forceinline__ int tile_blocks(const Entry& x, int t, int g) {
-    const long long last = ((long long)t * kTile + kTile - 1) / g;
-    const int i = last < x.n - 1 ? (int)last : x.n - 1;
+    const int last = (int)(((uint32_t)t * kRows + kRows - 1) / (uint32_t)g);
+    const int i = last < x.n - 1 ? last : x.n - 1;
     return (x.limit(i) - x.begin + kBlock - 1) / kBlock;
 }
 
-// Pieces the line is cut into: each has a unit at least.
-__device__ __forceinline__ int pieces(long long total, int ctas) { return total < ctas ? (int)total : ctas; }
-
-// The CTA whose piece of the line [total * c / ctas, total * (c + 1) / ctas) holds unit u.
-__device__ __forceinline__ int cta_of(long long u, long long total, int ctas) {
-    return (int)(((u + 1) * ctas - 1) / total);
+// a / b, which is short where both fit 32 bits.
+__device__ __forceinline__ long long divide(long long a, long long b) {
+    return (a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
 }
+
+// Units of the line to a CTA.
+__device__ __forceinline__ long long piece_length(long long total, int ctas) { return divide(total + ctas - 1, ctas); }
+
+// What a CTA does of one item: blocks [b0, b1) of it.
+struct Piece {
+    int steps;            // 0: there are no more
+    int pair;             // two tiles over each block
+    int b0, uncut;        // the piece is the whole item
+    int row0, tile_row;   // rows of q of the entry, and the item's first (row, query head) of it
+    int n_rows, head;     // rows of the item, key head
+    int begin, end, len;  // as in the entry
+    int table;
+    int low, high;        // past the last key that the item's first and last row see
+    int g0;               // steps of the pieces before
+    int last_cta;         // that has a piece of the item
+    int spoiled;          // a page is missing: the rows are NaN
+    int edge, look;       // first block, from b0 on, that some row does not see whole; that a box may overrun
+    int log_copies;       // the rows lie in a tile so many times
+    int n_q;              // query buffers used before
+    __device__ __forceinline__ int limit(int i) const { return len < 0 ? end : len + i + 1; }
+};
 
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
@@ -143,523 +188,1202 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
-// ---------------------------------------------------------------- the kernel
-template <int kD>
-struct Smem {
-    static constexpr int kHalf = kTile * 128;           // 128 rows of 64 elements, 128-byte swizzle
-    static constexpr int kOperand = kD / 64 * kHalf;    // Q, K or V
-    static constexpr int kTotal = 3 * kOperand + 1024;  // (the operands start on a 1024-byte boundary)
-};
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+// Two products and sums, or two sums, in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 y;
+    asm("{.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;}"
+        : "=f"(y.x), "=f"(y.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return y;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 y;
+    asm("{.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;}"
+        : "=f"(y.x), "=f"(y.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return y;
+}
 
-// 16-byte chunk c of row r of an operand tile.
+__device__ __forceinline__ void wait_prior_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Waits until the phase of `parity` completes, at most 2^20 suspensions of up to 20 us.
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 n;\n\tmov.b32 n, 1048576;\n"
+        "again:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+        "@p bra done;\n\t"
+        "sub.u32 n, n, 1;\n\t"
+        "setp.ne.u32 q, n, 0;\n\t"
+        "@q bra again;\n"
+        "done:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(tc::smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// The compiler is to know nothing of x: loops whose first rounds leave out a part
+// would else be written out for each of them, and all the warps' code has to stay
+// in the instruction cache (at 180 KB a third of the issue slots waited for it).
+__device__ __forceinline__ int opaque(int x) {
+    asm volatile("" : "+r"(x));
+    return x;
+}
+
+// ---------------------------------------------------------------- the kernel
+// 16-byte chunk c of row r of an operand.
 __device__ __forceinline__ uint32_t chunk_offset(int r, int c) {
     return (uint32_t)((c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
+constexpr int kPieces = 4;    // ahead of the products
+constexpr int kReaders = 14;  // warps that read them (with TMA one more)
+
+// kSteps: more than the loads can be ahead.
+template <int kSlots, int kSteps>
+struct Shared {
+    uint64_t full[kSlots], empty[kSlots];  // ring slots
+    uint64_t landed[kSlots];               // values that are looked at before they are full
+    uint64_t q_full[2], q_empty[2];
+    uint64_t s_full[2], p_full[2];         // per tile: scores formed, weights written
+    uint64_t o_done[2], o_free[2];         // a product with V is done; the output was read
+    uint64_t merge;                        // the second tile's sums are ready
+    uint64_t drain;
+    uint64_t piece_full[kPieces], piece_empty[kPieces];
+    Piece pieces[kPieces];
+    float2 ml[2][kTile];                   // each tile's m and l of its rows, for the other tile or its own copies
+    uint32_t odd[kSteps][4];               // by step: keys of a block whose values are not finite
+    volatile int abort_flag;
+    uint32_t tmem_base;
+    long long scan[kThreads / 32];
+    long long first_start;
+    int first_entry;
+    Entry first;
+};
+
+template <int kD>
+struct Layout {
+    static constexpr int kHalf = kTile * 128;           // 128 rows of 64 elements, 128-byte swizzle
+    static constexpr int kOperand = kD / 64 * kHalf;    // a tile of Q, a block of K or V
+    static constexpr int kSlots = 5 * 128 / kD;         // of the ring
+    static constexpr int kSteps = 8 * 128 / kD;
+    static constexpr int kTotal = (2 + kSlots) * kOperand + (int)sizeof(Shared<kSlots, kSteps>);
+    static_assert(kTotal <= 227 * 1024, "shared memory of a CTA");
+};
+
+// Arrives on `bar` when this thread's copies so far are done.
+__device__ __forceinline__ void cp_async_arrive_noinc(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
+}
+// `n` arrivals by one thread.
+__device__ __forceinline__ void arrive_n(uint64_t* bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(tc::smem_u32(bar)), "r"(n) : "memory");
+}
+
+struct Maps {
+    CUtensorMap k, v;  // [pages * hkv * page, d] in boxes of box_rows x 64
+    int box_rows;      // 0: rows are gathered one by one
+};
+
 template <int kD, bool kGroups>
-__global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttnParams p, const Plan plan, const int max_ctas,
-                                                               const int entries) {
+__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams p, const Plan plan, const Plan shared_plan,
+                                                               const int max_ctas, const int entries,
+                                                               const __grid_constant__ Maps maps) {
+    using L = Layout<kD>;
     constexpr int kChunks = kD / 8;
-    constexpr uint32_t kTmemO = kBlock;  // columns: S (and P over it) 0 .. 127, O 128 .. 128 + d
-    extern __shared__ unsigned char smem_raw[];
-    __shared__ uint64_t bar_s, bar_o;
-    __shared__ uint32_t tmem_base_smem;
-    __shared__ volatile int abort_flag;
-    __shared__ int bad_page[2];  // of this piece and the next
-    __shared__ uint32_t slots[2][kBlock];   // cache rows of the keys of two blocks
-    __shared__ uint32_t odd_keys[kBlock / 32];  // keys with a value that is not finite
-    __shared__ long long scan_sum[kThreads / 32];
-    __shared__ long long first_start;
-    __shared__ int first_entry;
+    constexpr int kSlots = L::kSlots;
+    constexpr uint32_t kTmemO = 2 * kBlock;  // columns: S of the tiles (P over it) 0 and 128, O 256 and 256 + 128
+    constexpr int kOddRing = L::kSteps;
+    extern __shared__ __align__(1024) unsigned char base[];
+    auto& sh = *reinterpret_cast<Shared<kSlots, kOddRing>*>(base + (2 + kSlots) * L::kOperand);
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
     const int g = p.hq / p.hkv;
-    unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    const uint32_t sQ = tc::smem_u32(base), sK = sQ + Smem<kD>::kOperand, sV = sK + Smem<kD>::kOperand;
+    const uint32_t sQ = tc::smem_u32(base), sRing = sQ + 2 * L::kOperand;
+    const __nv_bfloat16 kNan = __ushort_as_bfloat16(0x7FFF);
 
+    const uint32_t loaders = maps.box_rows > 0 ? 1 : kLoaders;  // arrivals that fill a slot
+    launch_dependents();
     // ---- the line of all items' blocks, and this CTA's piece of it
-    int bad = 0;
-    if (tid == 0) {
-        bad = p.cu[0] != 0 || p.cu[p.R] > p.rows;
-        if (p.n_groups) bad |= p.group_start[0] != 0 || p.group_start[p.n_groups] != p.R;
+    if (warp == 12) {
+        tc::tmem_alloc(&sh.tmem_base, 512);
+        tc::tmem_relinquish();
     }
-    for (int r = tid; r < p.R; r += kThreads) bad |= p.cu[r] > p.cu[r + 1];
-    for (int e = tid; e < p.n_groups; e += kThreads) bad |= p.group_start[e] > p.group_start[e + 1];
-    if (tid == 0) { abort_flag = 0; bad_page[0] = bad_page[1] = 0; first_entry = -1; }
-    bad = __syncthreads_or(bad);
-    if (blockIdx.x == 0 && tid == 0) *plan.bad = bad;
-    if (bad) return;  // (the joining kernel marks the rows)
+    if (tid == 0) {
+        sh.abort_flag = 0;
+        plan.jobs[blockIdx.x].n_rows = 0;
+#pragma unroll 1
+        for (int i = 0; i < kSlots; ++i) {
+            tc::mbar_init(&sh.full[i], loaders);
+            tc::mbar_init(&sh.landed[i], loaders);
+            tc::mbar_init(&sh.empty[i], 1);
+        }
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&sh.q_full[i], kLoaders);
+            tc::mbar_init(&sh.q_empty[i], 2);
+            tc::mbar_init(&sh.s_full[i], 1);
+            tc::mbar_init(&sh.p_full[i], 4);
+            tc::mbar_init(&sh.o_done[i], 1);
+            tc::mbar_init(&sh.o_free[i], 4);
+        }
+#pragma unroll 1
+        for (int i = 0; i < kPieces; ++i) {
+            tc::mbar_init(&sh.piece_full[i], 1);
+            tc::mbar_init(&sh.piece_empty[i], kReaders + (maps.box_rows > 0));
+        }
+        tc::mbar_init(&sh.merge, 4);
+        tc::mbar_init(&sh.drain, 1);
+        tc::fence_barrier_init();
+    }
     const int per = (entries + kThreads - 1) / kThreads;
     const int e0 = min(entries, tid * per), e1 = min(entries, e0 + per);
+    Entry first{};  // this thread's first
     long long mine = 0;
-    for (int e = e0; e < e1; ++e) mine += entry_of<kGroups>(p, e).cost(p.hkv);
+    int bad = 0;
+    if (kGroups) {
+#pragma unroll 1
+        for (int r = tid; r < p.R; r += kThreads) bad |= p.cu[r] > p.cu[r + 1];
+        bad |= p.group_start[0] != 0 || p.group_start[p.n_groups] != p.R;
+#pragma unroll 1
+        for (int e = e0; e < e1; ++e) {
+            const int r0 = p.group_start[e], r1 = p.group_start[e + 1];
+            bad |= r0 < 0 || r0 > r1 || r1 > p.R;
+        }
+    } else {
+#pragma unroll 1
+        for (int e = tid; e < p.n_groups; e += kThreads) bad |= p.group_start[e] > p.group_start[e + 1];
+        if (p.n_groups) bad |= p.group_start[0] != 0 || p.group_start[p.n_groups] != p.R;
+#pragma unroll 1
+        for (int e = e0; e < e1; ++e) bad |= p.cu[e] > p.cu[e + 1];
+    }
+    bad |= p.cu[0] != 0 || p.cu[p.R] > p.rows;
+    if (!bad) {
+#pragma unroll 1
+        for (int e = e0; e < e1; ++e) {
+            const Entry x = entry_of<kGroups>(p, e);
+            if (e == e0) first = x;
+            mine += x.cost(p.hkv);
+        }
+    }
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const long long up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
         if (lane >= o) incl += up;
     }
-    if (lane == 31) scan_sum[warp] = incl;
-    __syncthreads();
+    if (lane == 31) sh.scan[warp] = incl;
+    tc::tc_fence_before();
+    bad = __syncthreads_or(bad);
+    tc::tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sh.tmem_base, 0);
+    if (bad) {  // nothing can be said of any row
+        if (warp == 12) tc::tmem_dealloc(tmem, 512);
+        if (kGroups) return;
+        const long long n = (long long)p.rows * p.hq;
+#pragma unroll 1
+        for (long long i = (long long)blockIdx.x * kThreads + tid; i < n * kD; i += (long long)gridDim.x * kThreads) p.out[i] = kNan;
+        if (p.lse)
+#pragma unroll 1
+            for (long long i = (long long)blockIdx.x * kThreads + tid; i < n; i += (long long)gridDim.x * kThreads)
+                p.lse[i] = __int_as_float(0x7FC00000);
+        if (blockIdx.x == 0 && tid == 0) report(p.dev_status, DSPARK_ERR_DEVICE_INPUT);
+        return;
+    }
     long long before = incl - mine, total = 0;
+#pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += scan_sum[w];
-        total += scan_sum[w];
+        const long long x = sh.scan[w];
+        if (w < warp) before += x;
+        total += x;
     }
-    const int ctas = pieces(total, max_ctas);
-    long long x = total, x1 = total;
-    if (blockIdx.x < ctas) {
-        x = total * blockIdx.x / ctas;
-        x1 = total * (blockIdx.x + 1) / ctas;
-    }
-    if (blockIdx.x == 0) {
+    const long long length = piece_length(total, max_ctas);
+    const long long x0 = min(blockIdx.x * length, total), x1 = min(x0 + length, total);
+    if (x0 < x1 && x0 >= before && x0 < before + mine) {
         long long at = before;
+#pragma unroll 1
         for (int e = e0; e < e1; ++e) {
-            plan.start[e] = at;
-            at += entry_of<kGroups>(p, e).cost(p.hkv);
-        }
-        if (tid == 0) plan.start[entries] = total;
-    }
-    if (x >= before && x < before + mine) {
-        long long at = before;
-        for (int e = e0; e < e1; ++e) {
-            const long long c = entry_of<kGroups>(p, e).cost(p.hkv);
-            if (x < at + c) {
-                first_entry = e;
-                first_start = at;
+            const Entry x = e == e0 ? first : entry_of<kGroups>(p, e);
+            const long long c = x.cost(p.hkv);
+            if (x0 < at + c) {
+                sh.first_entry = e;
+                sh.first_start = at;
+                sh.first = x;
                 break;
             }
             at += c;
         }
     }
-    if (tid == 0) {
-        tc::mbar_init(&bar_s, 1);
-        tc::mbar_init(&bar_o, 1);
-        tc::fence_barrier_init();
-    }
     __syncthreads();
-    if (x >= x1) return;  // (less work than CTAs)
-    if (warp == 0) {
-        tc::tmem_alloc(&tmem_base_smem, 256);
-        tc::tmem_relinquish();
+    const float sl2 = fmaxf(p.scale * kLog2e, 1e-37f);  // (a masked score, -inf, weighs nothing at a scale of 0 too)
+    // Waits for the phase of that parity; false (and the CTA stops) when it does not come in some seconds.  (No
+    // function is called: the register split below leaves none for a call's frame.)
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        const bool ok = wait_bounded(bar, parity & 1);
+        if (!ok) sh.abort_flag = 1;
+        return ok;
+    };
+
+    // A warp's place in the sequence of pieces: piece `i` and step `u` of it.
+    struct Cursor {
+        int i = 0, u = 0, steps = 0, pair = 0, edge = 0;
+        const Piece* at = nullptr;
+        __device__ __forceinline__ int block() const { return pair ? u >> 1 : u; }     // from the piece's first on
+        __device__ __forceinline__ bool leads() const { return !(u & pair); }          // the step brings a block
+    };
+    // A place in the ring.
+    struct Ring {
+        uint32_t s = 0, phase = 0;
+        __device__ __forceinline__ void next() {
+            if (++s == kSlots) {
+                s = 0;
+                phase ^= 1;
+            }
+        }
+    };
+    auto open = [&](Cursor& c) {  // false: there are no more
+        const bool ok = wait(&sh.piece_full[c.i % kPieces], c.i / kPieces);
+        c.at = &sh.pieces[c.i % kPieces];
+        // (what a shuffle gives is the same for all lanes, and the compiler keeps it in uniform registers)
+        c.steps = __shfl_sync(0xFFFFFFFFu, ok ? c.at->steps : 0, 0);
+        c.pair = __shfl_sync(0xFFFFFFFFu, c.at->pair, 0);
+        c.edge = __shfl_sync(0xFFFFFFFFu, c.at->edge, 0);
+        c.u = 0;
+        return c.steps > 0;
+    };
+    auto stopped = [&]() { return __any_sync(0xFFFFFFFFu, sh.abort_flag); };
+    auto close = [&](Cursor& c) {  // done with the piece; on to the next
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sh.piece_empty[c.i % kPieces]);
+    };
+
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     }
-    tc::tc_fence_before();
-    __syncthreads();
-    tc::tc_fence_after();
-    const uint32_t tmem = tmem_base_smem;
-    const uint32_t my_tmem = tmem + ((uint32_t)(warp * 32) << 16);
-    uint32_t phase_s = 0, phase_o = 0;
-    int turn = 0;
-    const float sl2 = p.scale * kLog2e;
 
-    int e = first_entry;
-    long long e_start = first_start;
-    Entry en = entry_of<kGroups>(p, e);
-    while (x < x1) {
-        while (x >= e_start + en.cost(p.hkv)) {  // (entries without work cost nothing)
-            e_start += en.cost(p.hkv);
-            en = entry_of<kGroups>(p, ++e);
-        }
-        const long long item_cost = en.blocks + kItemCost;
-        const int item = (int)((x - e_start) / item_cost);
-        const long long s0 = e_start + item * item_cost;
-        const int h = item / en.tiles, t = item - h * en.tiles;
-        const int n_blocks = tile_blocks(en, t, g);
-        const int b0 = (int)max(x - s0 - kItemCost, 0LL);
-        const int b1 = (int)min(min(x1, s0 + item_cost) - s0 - kItemCost, (long long)n_blocks);
-        x = s0 + item_cost;
-        if (b0 >= b1) continue;
-
-        // ---- one piece: blocks [b0, b1) of tile t of key head h
-        const long long r_tile = (long long)t * kTile;
-        const int n_rows = (int)min((long long)en.n * g - r_tile, (long long)kTile);
-        const bool live = tid < n_rows;
-        const bool warp_live = warp * 32 < n_rows;
-        const int my_i = live ? (int)((r_tile + tid) / g) : 0;
-        const long long my_row = (long long)(en.row0 + my_i) * p.hq + h * g + (live ? (int)((r_tile + tid) - (long long)my_i * g) : 0);
-        const int my_limit = live ? en.limit(my_i) : en.limit(0);
-        const int low_limit = en.limit((int)(r_tile / g));  // of the tile's first row
-        const int high_limit = en.limit((int)((r_tile + n_rows - 1) / g));
-
-        // the cache row of key `tid` of block b
-        auto slot_of = [&](int b) -> uint32_t {
-            const int pos = en.begin + b * kBlock + tid;
-            if (b >= b1 || pos >= high_limit) return kNoSlot;
-            const int pb = pos / p.page;
-            const int id = p.block_table[(long long)en.table * p.max_blocks + pb];
-            if (id < 0 || id >= p.pool_pages) {
-                bad_page[turn] = 1;
-                return kNoSlot;
-            }
-            return ((uint32_t)id * p.hkv + h) * p.page + (pos - pb * p.page);
-        };
-        auto load_block = [&](uint32_t dst, const __nv_bfloat16* cache, const uint32_t* from) {
-#pragma unroll 4
-            for (int i = 0; i < kBlock * kChunks / kThreads; ++i) {
-                const int idx = i * kThreads + tid, r = idx / kChunks, c = idx % kChunks;
-                const uint32_t s = from[r];
-                tc::cp_async_16(dst + chunk_offset(r, c), cache + (size_t)(s == kNoSlot ? 0 : s) * kD + c * 8,
-                                s == kNoSlot ? 0 : 16);
-            }
-        };
-
-        slots[b0 & 1][tid] = slot_of(b0);
-        slots[(b0 + 1) & 1][tid] = slot_of(b0 + 1);
-        for (int idx = tid; idx < n_rows * kChunks; idx += kThreads) {
-            const int r = idx / kChunks, c = idx % kChunks;
-            const int i = (int)((r_tile + r) / g);
-            const size_t row = (size_t)(en.row0 + i) * p.hq + h * g + ((r_tile + r) - (long long)i * g);
-            tc::cp_async_16(sQ + chunk_offset(r, c), p.q + row * kD + c * 8, 16);
-        }
-        __syncthreads();
-        load_block(sK, p.k_cache, slots[b0 & 1]);
-        tc::cp_async_commit();
-
-        float m = -INFINITY, l = 0.0f;  // m in raw scores
-        for (int b = b0; b < b1; ++b) {
-            const int key0 = en.begin + b * kBlock;
-            // K of this block has arrived; every thread is done with the last S
-            tc::cp_async_wait<0>();
-            tc::fence_proxy_async_smem();
-            tc::tc_fence_before();
-            __syncthreads();
-            if (warp == 0) {
-                tc::tc_fence_after();
-                constexpr uint32_t idesc = tc::idesc_bf16_f32(kTile, kBlock);
-                const uint64_t qd = tc::smem_desc_sw128(sQ), kd = tc::smem_desc_sw128(sK);
-#pragma unroll
-                for (int k = 0; k < kD / 16; ++k) {
-                    const uint64_t step = (uint64_t)((k >> 2) * (Smem<kD>::kHalf >> 4) + (k & 3) * 2);
-                    tc::umma_bf16_elect(tmem, qd + step, kd + step, idesc, k != 0);
-                }
-                tc::umma_commit_elect(&bar_s);
-            }
-            // V's buffer is free once the last block's product is done
-            if (b > b0) {
-                tc::mbar_wait(&bar_o, phase_o, &abort_flag, kWaitNs);
-                phase_o ^= 1;
-            }
-            load_block(sV, p.v_cache, slots[b & 1]);
-            tc::cp_async_commit();
-            tc::mbar_wait(&bar_s, phase_s, &abort_flag, kWaitNs);
-            phase_s ^= 1;
-            tc::tc_fence_after();
-            if (b + 1 < b1) load_block(sK, p.k_cache, slots[(b + 1) & 1]);
-            tc::cp_async_commit();
-            const uint32_t next_slot = slot_of(b + 2);
-
+    if (warp < 8) {
+        // ================================================================ exponentials
+        const int X = warp >> 2, t128 = tid & (kTile - 1);
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + lanes + X * kBlock, tO = tmem + lanes + kTmemO + X * kBlock;
+        const uint32_t tO2 = tmem + lanes + kTmemO + (X ^ 1) * kBlock;
+        // The warp's arrival (32 of them on one barrier take some 4 cycles each: 2000 cycles of a step).
+        auto arrive = [&](uint64_t* bar) {
             __syncwarp();
-            if (warp_live) {
-                float s[kBlock];
-                tc::tmem_ld_32x32b_x32<0>(my_tmem, s);
-                tc::tmem_ld_32x32b_x32<32>(my_tmem + 32, s);
-                tc::tmem_ld_32x32b_x32<64>(my_tmem + 64, s);
-                tc::tmem_ld_32x32b_x32<96>(my_tmem + 96, s);
-                tc::tmem_ld_wait();
-                const int seen = my_limit - key0;  // keys of the block this row sees
-                const bool whole = __all_sync(0xFFFFFFFFu, seen >= kBlock);
-                if (!whole) {
-#pragma unroll
-                    for (int j = 0; j < kBlock; ++j) s[j] = j < seen ? s[j] : -INFINITY;
-                }
-                float top[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-                for (int j = 4; j < kBlock; ++j) top[j & 3] = fmaxf(top[j & 3], s[j]);
-                const float mb = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                // move the reference when the maximum has grown by more than 2^kGrowth
-                const bool move = mb > m && !((mb - m) * sl2 <= kGrowth);
-                if (__any_sync(0xFFFFFFFFu, move)) {
-                    const float f = !move ? 1.0f : m == -INFINITY ? 0.0f : exp2_approx((m - mb) * sl2);
-                    if (move) m = mb;
-                    l *= f;
-                    if (b > b0) {
+            if (lane == 0) tc::mbar_arrive(bar);
+        };
+        auto tile_sync = [&]() {
+            __syncwarp();  // (the barrier counts warps: their lanes have to come together)
+            asm volatile("bar.sync %0, 128;" ::"r"(1 + X) : "memory");
+        };
+        int n_step = 0;     // steps of this tile so far
+        int n_done = 0;     // of them, the ones whose product is waited for
+        int n_merge = 0;
+        bool prior_done = false;
+        Cursor at;
+        for (; open(at) && !stopped(); close(at), ++at.i) {
+            const Piece& w = *at.at;
+            const int g0 = w.g0, steps = at.steps;
+            const int u0 = X ^ (g0 & 1);
+            if (u0 >= steps) continue;  // (one step, the other tile's)
+            const int sub = at.pair ? u0 : 0;
+            // Up to 32 rows lie in the tile four times, each copy takes a quarter of a block's keys: all four warps
+            // form exponentials then, and each 32 of a row instead of 128.
+            const int log_copies = w.log_copies, log_rows = 7 - log_copies;
+            const int n_rows = min(w.n_rows - sub * kTile, kTile), t_row = t128 & ((1 << log_rows) - 1);
+            const int col0 = (t128 >> log_rows) << log_rows;  // this copy's first key of a block
+            const bool live = t_row < n_rows, warp_live = (t_row & ~31) < n_rows;
+            const int my_r = w.tile_row + (live ? sub * kTile + t_row : 0), my_i = my_r / g;
+            const int my_limit = w.limit(my_i);
+            const int first_key = w.begin + w.b0 * kBlock;
+            float m = -INFINITY, l = 0.0f;  // m in raw scores
 #pragma unroll 1
-                        for (int c = 0; c < kD; c += 16) {
-                            float o[16];
-                            uint32_t u[16];
-                            tc::tmem_ld_32x32b_x16<0>(my_tmem + kTmemO + c, o);
-                            tc::tmem_ld_wait();
+            for (int u = u0; u < steps; u += 2) {
+                const int key0 = first_key + (at.pair ? u >> 1 : u) * kBlock;
+                // N scores of this row from column col0 on: maximum, weights, their sum
+                auto weigh = [&](auto n_) {
+                    constexpr int N = decltype(n_)::value;
+                    float s[N];
+                    tc::tmem_ld_32x32b_x32<0>(tS + col0, s);
+                    if constexpr (N == kBlock) {
+                        tc::tmem_ld_32x32b_x32<32>(tS + 32, s);
+                        tc::tmem_ld_32x32b_x32<64>(tS + 64, s);
+                        tc::tmem_ld_32x32b_x32<96>(tS + 96, s);
+                    }
+                    tc::tmem_ld_wait();
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(o[j] * f);
-                            tc::tmem_st_32x32b_x16<0>(my_tmem + kTmemO + c, u);
+                    for (int j = 0; j < N; j += 8) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) top[i] = max3(top[i], s[j + 2 * i], s[j + 2 * i + 1]);
+                    }
+                    const float mb = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                    // move the reference when the maximum has grown by more than 2^kGrowth
+                    const bool move = mb > m && !((mb - m) * sl2 <= kGrowth);
+                    if (__any_sync(0xFFFFFFFFu, move)) {
+                        const float f = !move ? 1.0f : m == -INFINITY ? 0.0f : exp2_approx((m - mb) * sl2);
+                        if (move) m = mb;
+                        l *= f;
+                        if (u > u0) {
+#pragma unroll 1
+                            for (int c = 0; c < kD; c += 16) {
+                                float o[16];
+                                uint32_t v[16];
+                                tc::tmem_ld_32x32b_x16<0>(tO + c, o);
+                                tc::tmem_ld_wait();
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(o[j] * f);
+                                tc::tmem_st_32x32b_x16<0>(tO + c, v);
+                            }
                         }
                     }
-                }
-                const float ref = m == -INFINITY ? 0.0f : m * sl2;
-                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    const float ref = m == -INFINITY ? 0.0f : -m * sl2;
+                    float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-                for (int c = 0; c < kBlock; c += 32) {
-                    uint32_t u[16];
+                    for (int c = 0; c < N; c += 32) {
+                        uint32_t v[16];
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        float a = exp2_approx(fmaf(s[c + j], sl2, -ref)), d = exp2_approx(fmaf(s[c + j + 1], sl2, -ref));
-                        if (!whole) {
-                            a = c + j < seen ? a : 0.0f;
-                            d = c + j + 1 < seen ? d : 0.0f;
+                        for (int j = 0; j < 32; j += 2) {
+                            const float2 x = fma2(make_float2(s[c + j], s[c + j + 1]), make_float2(sl2, sl2), make_float2(ref, ref));
+                            const float2 y = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+                            sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], y);
+                            const __nv_bfloat162 both = __floats2bfloat162_rn(y.x, y.y);
+                            v[j >> 1] = *reinterpret_cast<const uint32_t*>(&both);
                         }
-                        sum[(j >> 1) & 1] += a;
-                        sum[2 + ((j >> 1) & 1)] += d;
-                        const __nv_bfloat162 w = __floats2bfloat162_rn(a, d);
-                        u[j >> 1] = *reinterpret_cast<const uint32_t*>(&w);
+                        tc::tmem_st_32x32b_x16<0>(tS + (col0 + c) / 2, v);
                     }
-                    tc::tmem_st_32x32b_x16<0>(my_tmem + c / 2, u);
-                }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                tc::tmem_st_wait();
-            }
-            // V of this block has arrived (the next K may be on its way)
-            tc::cp_async_wait<1>();
-            int odd = 0;
-            if (low_limit < high_limit && key0 + kBlock > low_limit) {
-                // some row does not see all of these keys: a value that is not finite must not reach
-                // it through a zero weight.  Such keys are taken out here and added by hand below.
-                if (tid < kBlock / 32) odd_keys[tid] = 0;
-                __syncthreads();
-                const int key = tid;
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                    if constexpr (N < kBlock) {  // the other copies' keys weigh nothing here
+                        const uint32_t zero[16] = {};
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(base + 2 * Smem<kD>::kOperand + chunk_offset(key, c));
-                    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        odd |= (v[j] & 0x7F80u) == 0x7F80u || (v[j] & 0x7F800000u) == 0x7F800000u;
-                }
-                if (odd) {
-                    atomicOr(&odd_keys[key >> 5], 1u << (key & 31));
-#pragma unroll
-                    for (int c = 0; c < kChunks; ++c)
-                        *reinterpret_cast<uint4*>(base + 2 * Smem<kD>::kOperand + chunk_offset(key, c)) = make_uint4(0, 0, 0, 0);
-                }
-                odd = __syncthreads_or(odd);
-            }
-            tc::fence_proxy_async_smem();
-            tc::tc_fence_before();
-            __syncthreads();
-            if (warp == 0) {
-                tc::tc_fence_after();
-                constexpr uint32_t idesc = tc::idesc_bf16_f32(kTile, kD) | tc::kIdescBTransposed;
-                const uint64_t vd = tc::smem_desc_sw128_mn(sV, Smem<kD>::kHalf);
-#pragma unroll
-                for (int k = 0; k < kBlock / 16; ++k)
-                    tc::umma_bf16_ta_elect(tmem + kTmemO, tmem + 8 * k, vd + (uint64_t)(k * (2048 >> 4)), idesc,
-                                           b != b0 || k != 0);
-                tc::umma_commit_elect(&bar_o);
-            }
-            if (odd) {
-                tc::mbar_wait(&bar_o, phase_o, &abort_flag, kWaitNs);  // (waited for again: the phase stays)
+                        for (int c = 0; c < kBlock; c += 32)
+                            if (c < col0 || c >= col0 + N) tc::tmem_st_32x32b_x16<0>(tS + c / 2, zero);
+                    }
+                    tc::tmem_st_wait();
+                };
+                // (the scores are formed after the last product with V of this tile: that one is done too)
+                wait(&sh.s_full[X], n_step);
                 tc::tc_fence_after();
                 __syncwarp();
                 if (warp_live) {
-                    for (int key = 0; key < kBlock; ++key) {
-                        if (!(odd_keys[key >> 5] >> (key & 31) & 1)) continue;
-                        const uint32_t pair = tc::tmem_ld_32x32b_x1(my_tmem + key / 2);
-                        tc::tmem_ld_wait();
-                        const float w = __uint_as_float(key & 1 ? pair & 0xFFFF0000u : pair << 16);
-                        const __nv_bfloat16* v = p.v_cache + (size_t)slots[b & 1][key] * kD;
-                        for (int c = 0; c < kD; c += 16) {
-                            float o[16];
-                            uint32_t u[16];
-                            tc::tmem_ld_32x32b_x16<0>(my_tmem + kTmemO + c, o);
+                    const int seen = my_limit - key0;  // keys of the block this row sees
+                    if (!__all_sync(0xFFFFFFFFu, seen >= kBlock)) {
+#pragma unroll 1
+                        for (int c = col0; c < col0 + (1 << log_rows); c += 16) {
+                            float x[16];
+                            uint32_t v[16];
+                            tc::tmem_ld_32x32b_x16<0>(tS + c, x);
                             tc::tmem_ld_wait();
 #pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                u[j] = __float_as_uint(key0 + key < my_limit ? fmaf(w, __bfloat162float(v[c + j]), o[j]) : o[j]);
-                            tc::tmem_st_32x32b_x16<0>(my_tmem + kTmemO + c, u);
+                            for (int j = 0; j < 16; ++j) v[j] = j < seen - c ? __float_as_uint(x[j]) : 0xFF800000u;
+                            tc::tmem_st_32x32b_x16<0>(tS + c, v);
                         }
+                        tc::tmem_st_wait();
                     }
-                    tc::tmem_st_wait();
+                    if (log_copies) weigh(std::integral_constant<int, 32>{});
+                    else weigh(std::integral_constant<int, kBlock>{});
                 }
                 tc::tc_fence_before();
-            }
-            if (odd) __syncthreads();  // (the slots were read)
-            slots[b & 1][tid] = next_slot;
-        }
-        tc::mbar_wait(&bar_o, phase_o, &abort_flag, kWaitNs);
-        phase_o ^= 1;
-        tc::tc_fence_after();
-        __syncthreads();  // (bad_page, slots)
-        if (tid == 0) bad_page[turn ^ 1] = 0;
-
-        // ---- the piece's triple
-        const bool spoiled = bad_page[turn] != 0 || abort_flag != 0;
-        if (spoiled && tid == 0) report(p.dev_status, abort_flag ? DSPARK_ERR_TIMEOUT : DSPARK_ERR_DEVICE_INPUT);
-        if (spoiled) l = __int_as_float(0x7FC00000);
-        const bool uncut = b0 == 0 && b1 == n_blocks;
-        if (warp_live) {
-            const float m2 = m == -INFINITY ? -INFINITY : m * sl2;
-            const int slot = 2 * blockIdx.x + (b0 == 0);
-            const bool final = !kGroups && uncut && p.n_groups == 0;
-            float* to = uncut ? plan.whole + my_row * kD : plan.part + ((size_t)slot * kTile + tid) * kD;
-            const float inv = 1.0f / l;
+                arrive(&sh.p_full[X]);
+                ++n_step;
+                if ((at.pair ? u >> 1 : u) >= at.edge) {
+                    // Some row does not see all of these keys.  Values that are not finite were taken out of the
+                    // block, so that they reach no row through a zero weight; here the rows that do see them get them.
+                    wait(&sh.o_done[X], n_done);
+                    if (u + 2 < steps) ++n_done;
+                    tc::tc_fence_after();
+                    __syncwarp();
+                    const uint32_t* odd = sh.odd[(g0 + (at.pair ? u & ~1 : u)) % kOddRing];
+                    if (warp_live && (odd[0] | odd[1] | odd[2] | odd[3])) {
 #pragma unroll 1
-            for (int c = 0; c < kD; c += 32) {
-                float o[32];
-                tc::tmem_ld_32x32b_x32<0>(my_tmem + kTmemO + c, o);
-                tc::tmem_ld_wait();
-                if (live && final) {
+                        for (int key = col0; key < col0 + (1 << log_rows); ++key) {
+                            if (!(odd[key >> 5] >> (key & 31) & 1)) continue;
+                            const int pos = key0 + key, pb = pos / p.page;
+                            const int id = p.block_table[(long long)w.table * p.max_blocks + pb];
+                            const __nv_bfloat16* v = p.v_cache + (((size_t)id * p.hkv + w.head) * p.page + (pos - pb * p.page)) * kD;
+                            const uint32_t both = tc::tmem_ld_32x32b_x1(tS + key / 2);
+                            tc::tmem_ld_wait();
+                            const float weight = __uint_as_float(key & 1 ? both & 0xFFFF0000u : both << 16);
+#pragma unroll 1
+                            for (int c = 0; c < kD; c += 16) {
+                                float o[16];
+                                uint32_t q[16];
+                                tc::tmem_ld_32x32b_x16<0>(tO + c, o);
+                                tc::tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
-                        __nv_bfloat162 w[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            w[i] = __floats2bfloat162_rn(o[j + 2 * i] * inv, o[j + 2 * i + 1] * inv);
-                        *reinterpret_cast<uint4*>(p.out + my_row * kD + c + j) = *reinterpret_cast<const uint4*>(w);
+                                for (int j = 0; j < 16; ++j)
+                                    q[j] = __float_as_uint(pos < my_limit ? fmaf(weight, __bfloat162float(v[c + j]), o[j]) : o[j]);
+                                tc::tmem_st_32x32b_x16<0>(tO + c, q);
+                            }
+                            tc::tmem_st_wait();
+                        }
                     }
-                } else if (live) {
-#pragma unroll
-                    for (int j = 0; j < 32; j += 4)
-                        *reinterpret_cast<float4*>(to + c + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                    tc::tc_fence_before();
                 }
-                __syncwarp();
             }
-            if (live) {
-                if (!final) (uncut ? plan.whole_ml[my_row] : plan.part_ml[(size_t)slot * kTile + tid]) = make_float2(m2, l);
-                else if (p.lse) p.lse[my_row] = (m2 + log2f(l)) * kLn2;
+            // ---- the triple of this tile's rows
+            wait(&sh.o_done[X], n_done);
+            ++n_done;
+            tc::tc_fence_after();
+            __syncwarp();
+            const bool two = !at.pair && steps > 1;  // the other tile has a part of the same rows
+            if (two && u0 == 1) {
+                sh.ml[X][t128] = make_float2(m, l);
+                tc::tc_fence_before();
+                arrive(&sh.merge);
+                ++n_merge;
+                continue;
+            }
+            // adds another part's (m, l) to (m0, l0): their common reference, and both scales.  (A sum that is not a
+            // number stays one, whatever its scale.)
+            auto add = [](float& m0, float& l0, float m1, float l1, float& f0, float& f1) {
+                const float top = fmaxf(m0, m1);
+                f0 = m0 == -INFINITY ? 0.0f : exp2_approx(m0 - top);
+                f1 = m1 == -INFINITY ? 0.0f : exp2_approx(m1 - top);
+                l0 = (m0 == -INFINITY ? l0 : l0 * f0) + (m1 == -INFINITY ? l1 : l1 * f1);
+                m0 = top;
+            };
+            m = m == -INFINITY ? -INFINITY : m * sl2;  // base-2 from here on
+            float f1 = 1.0f, f2 = 0.0f, f3 = 0.0f;     // scales of this tile's, the other tile's, the shared part's sums
+            if (two) {
+                wait(&sh.merge, n_merge);
+                tc::tc_fence_after();
+                __syncwarp();
+                ++n_merge;
+                const float2 other = sh.ml[X ^ 1][t128];
+                add(m, l, other.x == -INFINITY ? -INFINITY : other.x * sl2, other.y, f1, f2);
+            }
+            if (log_copies) {
+                sh.ml[X][t128] = make_float2(m, l);
+                tile_sync();
+                const float own = m;
+                m = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < 1 << log_copies; ++c) m = fmaxf(m, sh.ml[X][(c << log_rows) + t_row].x);
+                l = 0.0f;
+#pragma unroll 1
+                for (int c = 0; c < 1 << log_copies; ++c) {
+                    const float2 ml = sh.ml[X][(c << log_rows) + t_row];
+                    l += ml.x == -INFINITY ? ml.y : ml.y * exp2_approx(ml.x - m);
+                }
+                const float f = own == -INFINITY ? 0.0f : exp2_approx(own - m);
+                f1 *= f;
+                f2 *= f;
+                tile_sync();  // (the places are used again)
+            }
+            if (w.spoiled) l = __int_as_float(0x7FC00000);
+            const bool uncut = w.uncut != 0;
+            const bool final = !kGroups && uncut;
+            const size_t slot = (size_t)(2 * blockIdx.x + (w.b0 == 0)) * kRows;  // its first row
+            // partial sums lie by four columns, then rows, so that a warp's stores are contiguous
+            const size_t lin_step = (size_t)p.rows * g, lin0 = (size_t)w.row0 * g + w.tile_row + sub * kTile;
+            const bool prefix = final && p.n_groups > 0 && w.begin > 0;
+            if (prefix) {
+                if (!prior_done) wait_prior_grid();
+                prior_done = true;
+                const float2 ml = shared_plan.whole_ml[(size_t)w.head * lin_step + lin0 + (live ? t_row : 0)];
+                float fa;
+                add(m, l, ml.x, ml.y, fa, f3);
+                f1 *= fa;
+                f2 *= fa;
+            }
+            if (final) {
+                const float inv = 1.0f / l;
+                f1 *= inv;
+                f2 *= inv;
+                f3 *= inv;
+            }
+            const float4* const shared_part = reinterpret_cast<const float4*>(shared_plan.whole + (size_t)w.head * lin_step * kD);
+            float4* const to = reinterpret_cast<float4*>(uncut ? plan.whole + (size_t)w.head * lin_step * kD : plan.part + slot * kD);
+            const size_t to0 = uncut ? lin0 : sub * kTile, to_step = uncut ? lin_step : kRows;
+            auto row_of_out = [&](int r) {  // of this tile's row r
+                const int i = (w.tile_row + sub * kTile + r) / g;
+                return (size_t)(w.row0 + i) * p.hq + w.head * g + (w.tile_row + sub * kTile + r - i * g);
+            };
+            {
+                // The sums go through the tile's query buffer, half of the columns at a time: there the copies' meet,
+                // and rows are written out side by side.
+                float4* const stage = reinterpret_cast<float4*>(base + ((w.n_q + sub) & 1) * L::kOperand);  // [c / 4][128 lanes]
+                if (final) sh.ml[X][t128] = make_float2(f3, __int_as_float(live ? (int)row_of_out(t_row) : 0));
+#pragma unroll 1
+                for (int c0 = 0; c0 < kD; c0 += kD / 2) {
+#pragma unroll 1
+                    for (int c = 0; c < kD / 2; c += 16) {
+                        float o[16], o2[16];
+                        tc::tmem_ld_32x32b_x16<0>(tO + c0 + c, o);
+                        if (two) tc::tmem_ld_32x32b_x16<0>(tO2 + c0 + c, o2);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) o[j] = two ? o[j] * f1 + o2[j] * f2 : o[j] * f1;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int q = c / 4 + j;
+                            stage[q * kTile + (t128 ^ (q & 15))] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                        }
+                    }
+                    tile_sync();
+                    constexpr int kQuads = kD / 8;  // of four columns, in this half
+                    if (final) {  // a row's columns side by side
+                        const int q = t128 % kQuads;
+#pragma unroll 1
+                        for (int r = t128 / kQuads; r < n_rows; r += kTile / kQuads) {
+                            const float2 f = sh.ml[X][r];
+                            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            if (prefix) x = shared_part[(size_t)(c0 / 4 + q) * lin_step + lin0 + r];
+                            float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+                            for (int c = r; c < kTile; c += 1 << log_rows) {
+                                const float4 v = stage[q * kTile + (c ^ (q & 15))];
+                                y.x += v.x; y.y += v.y; y.z += v.z; y.w += v.w;
+                            }
+                            const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x + x.x * f.x, y.y + x.y * f.x);
+                            const __nv_bfloat162 hi = __floats2bfloat162_rn(y.z + x.z * f.x, y.w + x.w * f.x);
+                            *reinterpret_cast<uint2*>(p.out + (size_t)__float_as_int(f.y) * kD + c0 + 4 * q) =
+                                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+                        }
+                    } else {  // a column's rows
+                        const int r = t_row;
+#pragma unroll 1
+                        for (int q = t128 >> log_rows; q < kQuads && live; q += 1 << log_copies) {
+                            float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+                            for (int c = r; c < kTile; c += 1 << log_rows) {
+                                const float4 v = stage[q * kTile + (c ^ (q & 15))];
+                                y.x += v.x; y.y += v.y; y.z += v.z; y.w += v.w;
+                            }
+                            to[(size_t)(c0 / 4 + q) * to_step + to0 + r] = y;
+                        }
+                    }
+                    tile_sync();
+                }
+            }
+            if (live && t128 == t_row) {
+                if (!final) (uncut ? plan.whole_ml + (size_t)w.head * lin_step : plan.part_ml + slot)[to0 + t_row] = make_float2(m, l);
+                else if (p.lse) p.lse[row_of_out(t_row)] = (m + log2f(l)) * kLn2;
+            }
+            tc::tc_fence_before();
+            arrive(&sh.o_free[X]);
+            if (two) arrive(&sh.o_free[X ^ 1]);
+            tile_sync();
+            if (t128 == 0) {
+                tc::mbar_arrive(&sh.q_empty[(w.n_q + sub) & 1]);
+                if (!uncut && w.b0 == 0 && sub == 0) {
+                    Job j;
+                    j.n_rows = w.n_rows;
+                    j.first = blockIdx.x;
+                    j.last = w.last_cta;
+                    j.row0 = w.row0;
+                    j.tile_row = w.tile_row;
+                    j.head = w.head;
+                    j.merge_prefix = !kGroups && p.n_groups > 0 && w.begin > 0;
+                    j.pad = 0;
+                    plan.jobs[blockIdx.x] = j;
+                }
             }
         }
-        tc::tc_fence_before();
-        __syncthreads();
-        tc::tc_fence_after();
-        turn ^= 1;
+    } else if (warp < 12) {
+        // ================================================================ loads
+        constexpr int kNone = -1, kMissing = -2;
+        const int t128 = tid - 256, part = warp - 8;
+        uint32_t n_q = 0;
+        auto first_key = [](const Cursor& c) { return c.at->begin + (c.at->b0 + c.block()) * kBlock; };
+        // the cache row of this lane's key of the cursor's block
+        auto row_of = [&](const Cursor& c) -> int {
+            const Piece& w = *c.at;
+            const int pos = first_key(c) + part * 32 + lane;
+            if (pos >= w.high) return kNone;
+            const int pb = pos / p.page;
+            const int id = __ldg(p.block_table + (long long)w.table * p.max_blocks + pb);
+            if (id < 0 || id >= p.pool_pages) return kMissing;
+            return (id * p.hkv + w.head) * p.page + (pos - pb * p.page);
+        };
+        // This lane's row and those of its warp (row < 0: zeros) to their places of an operand.
+        auto copy = [&](uint32_t dst, const __nv_bfloat16* rows, int row) {
+            constexpr int kPerPass = 32 / kChunks;  // rows that 32 chunks make up
+            const int c = lane % kChunks;
+            const char* const from = reinterpret_cast<const char*>(rows) + c * 16;
+            dst += part * 32 * 128;
+#pragma unroll 4
+            for (int i = 0; i < kChunks; ++i) {
+                const int r = i * kPerPass + lane / kChunks, from_row = __shfl_sync(0xFFFFFFFFu, row, r);
+                tc::cp_async_16(dst + chunk_offset(r, c), from + (size_t)max(from_row, 0) * (kD * 2), from_row < 0 ? 0 : 16);
+            }
+        };
+        auto load_q = [&](const Piece& w, int sub) {
+            const int q = n_q & 1;
+            const int t_row = t128 & ((kTile >> w.log_copies) - 1), at = w.tile_row + sub * kTile + t_row, qi = at / g;
+            const int row = sub * kTile + t_row < w.n_rows ? (w.row0 + qi) * p.hq + w.head * g + (at - qi * g) : kNone;
+            if (n_q >= 2) wait(&sh.q_empty[q], (n_q >> 1) - 1);
+            copy(sQ + q * L::kOperand, p.q, row);
+            cp_async_arrive_noinc(&sh.q_full[q]);
+            ++n_q;
+        };
+        Cursor k;
+        bool more = open(k);
+        if (maps.box_rows > 0) {  // queries alone
+#pragma unroll 1
+            while (more && !stopped()) {
+#pragma unroll 1
+                for (k.u = 0; k.u <= k.pair; ++k.u) load_q(*k.at, k.u);
+                close(k);
+                ++k.i;
+                more = open(k);
+            }
+        } else {
+            // Keys two steps ahead of the values, as the products take them.  A block's rows are looked up once, a
+            // step before its keys are loaded, and kept until its values are.
+            Cursor v;
+            open(v);
+            int next = 0, kept0 = 0, kept1 = 0, n_kept = 0;
+            Ring ring;
+            uint32_t filled = 0;
+            if (more) next = row_of(k);
+            // (a tile's queries go before its own first keys: a buffer may come free only after the step between)
+            bool queries = more;
+#pragma unroll 1
+            for (int i = opaque(-4); v.steps > 0 && !stopped();) {  // values of a step, keys of the step after the next
+                const bool is_k = i & 1;
+                if (is_k ? !more : i < 0) {
+                    ++i;
+                    continue;
+                }
+                if (is_k && queries) {
+                    load_q(*k.at, k.u);
+                    queries = false;
+                    continue;
+                }
+                ++i;
+                const Cursor& c = is_k ? k : v;
+                if (c.leads()) {
+                    const int row = is_k ? next : kept0;
+                    if (is_k) {
+                        if (next == kMissing) {
+                            sh.pieces[k.i % kPieces].spoiled = 1;
+                            report(p.dev_status, DSPARK_ERR_DEVICE_INPUT);
+                        }
+                        (n_kept == 0 ? kept0 : kept1) = next;
+                        ++n_kept;
+                    } else {
+                        kept0 = kept1;
+                        --n_kept;
+                    }
+                    uint64_t* const bar = !is_k && c.block() >= c.at->look ? &sh.landed[ring.s] : &sh.full[ring.s];
+                    if (filled == kSlots) wait(&sh.empty[ring.s], ring.phase ^ 1);
+                    else ++filled;
+                    copy(sRing + ring.s * L::kOperand, is_k ? p.k_cache : p.v_cache, row);
+                    if (__any_sync(0xFFFFFFFFu, row == kMissing)) {  // (what the warp noted of it goes before the arrival)
+                        asm volatile("cp.async.wait_all;" ::: "memory");
+                        tc::mbar_arrive(bar);
+                    } else {
+                        cp_async_arrive_noinc(bar);
+                    }
+                    ring.next();
+                }
+                if (is_k) {
+                    if (++k.u == k.steps) {
+                        ++k.i;
+                        more = open(k);
+                    }
+                    queries = k.u <= k.pair;
+                    if (more && k.leads()) next = row_of(k);
+                } else if (++v.u == v.steps) {
+                    close(v);
+                    ++v.i;
+                    open(v);
+                }
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp == 14) {
+        // ================================================================ values that not every row may see
+        // The slots go by as in the loading warp.  In a block that some row does not see whole, values that are
+        // not finite must not reach that row through a zero weight: their keys are taken out of the block and
+        // noted for the warps that add them by hand.
+        Ring ring;
+        uint32_t gv = 0, parity = 0;
+        Cursor k, v;
+        bool more = open(k);
+        open(v);
+#pragma unroll 1
+        for (int i = opaque(-2); v.steps > 0 && !stopped(); ++i) {
+            if (i >= 0 && v.leads()) {
+                const Piece& w = *v.at;
+                if (v.block() >= w.look) {
+                    const uint32_t s = ring.s;
+                    const int key0 = w.begin + (w.b0 + v.block()) * kBlock;
+                    const bool edge = v.block() >= v.edge, past = key0 + kBlock > w.high && maps.box_rows > 0;
+                    wait(&sh.landed[s], parity >> s);
+                    parity ^= 1u << s;
+                    unsigned char* const at = base + (2 + s) * L::kOperand;
+                    if (lane < 4) sh.odd[gv % kOddRing][lane] = 0;
+                    __syncwarp();
+                    const int from = max(w.low - key0, 0), to = min(w.high - key0, kBlock);
+                    if (past)  // a box holds what lies past the last key
+#pragma unroll 1
+                        for (int i = to * kChunks + lane; i < (to + maps.box_rows - 1) / maps.box_rows * maps.box_rows * kChunks; i += 32)
+                            *reinterpret_cast<uint4*>(at + chunk_offset(i / kChunks, i % kChunks)) = make_uint4(0, 0, 0, 0);
+                    if (edge)
+#pragma unroll 1
+                    for (int i = from * kChunks + lane; i < to * kChunks; i += 32) {
+                        const int r = i / kChunks;
+                        const uint4 q = *reinterpret_cast<const uint4*>(at + chunk_offset(r, i % kChunks));
+                        const uint32_t x[4] = {q.x, q.y, q.z, q.w};
+                        int odd = 0;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            odd |= (x[j] & 0x7F80u) == 0x7F80u || (x[j] & 0x7F800000u) == 0x7F800000u;
+                        if (odd) atomicOr(&sh.odd[gv % kOddRing][r >> 5], 1u << (r & 31));
+                    }
+                    __syncwarp();
+#pragma unroll 1
+                    for (int r = from; edge && r < to; ++r) {
+                        if (!(sh.odd[gv % kOddRing][r >> 5] >> (r & 31) & 1)) continue;
+                        if (lane < kChunks) *reinterpret_cast<uint4*>(at + chunk_offset(r, lane)) = make_uint4(0, 0, 0, 0);
+                    }
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) arrive_n(&sh.full[s], loaders);
+                }
+                ring.next();
+            }
+            if (more) {
+                if (k.leads()) ring.next();
+                if (++k.u == k.steps) {
+                    ++k.i;
+                    more = open(k);
+                }
+            }
+            if (i >= 0) {
+                ++gv;
+                if (++v.u == v.steps) {
+                    close(v);
+                    ++v.i;
+                    open(v);
+                }
+            }
+        }
+    } else if (warp == 12) {
+        // ================================================================ products
+        constexpr uint32_t idesc_s = tc::idesc_bf16_f32(kTile, kBlock);
+        constexpr uint32_t idesc_o = tc::idesc_bf16_f32(kTile, kD) | tc::kIdescBTransposed;
+        const bool copied = maps.box_rows == 0;  // (not by the async proxy)
+        Ring ring;
+        uint32_t n_q = 0, k_slot = 0, v_slot = 0;
+        int gk = 0, gv = 0;                 // steps of the two walks
+        uint32_t used[2] = {0, 0};          // items that used each tile's output
+        Cursor k, v;
+        bool more = open(k);
+        open(v);
+#pragma unroll 1
+        for (int i = opaque(-2);; ++i) {  // values of a step, then scores of the step after the next
+            if (i >= 0) {
+                const int X = gv & 1, sub = v.u & v.pair;
+                wait(&sh.p_full[X], gv >> 1);
+                if (sub == 0) {
+                    v_slot = ring.s;
+                    wait(&sh.full[v_slot], ring.phase);
+                    ring.next();
+                }
+                if (v.u < 2) {
+                    if (used[X]) wait(&sh.o_free[X], used[X] - 1);
+                    ++used[X];
+                }
+                if (copied) tc::fence_proxy_async_smem();
+                tc::tc_fence_after();
+                __syncwarp();
+                const uint64_t vd = tc::smem_desc_sw128_mn(sRing + v_slot * L::kOperand, L::kHalf);
+#pragma unroll
+                for (int j = 0; j < kBlock / 16; ++j)
+                    tc::umma_bf16_ta_elect(tmem + kTmemO + X * kBlock, tmem + X * kBlock + 8 * j,
+                                           vd + (uint64_t)(j * (2048 >> 4)), idesc_o, v.u >= 2 || j != 0);
+                if (sub == v.pair) tc::umma_commit_elect(&sh.empty[v_slot]);
+                if (v.u + 2 >= v.steps || v.block() >= v.edge) tc::umma_commit_elect(&sh.o_done[X]);
+                ++gv;
+                if (++v.u == v.steps) {
+                    close(v);
+                    ++v.i;
+                    open(v);
+                }
+            }
+            if (v.steps == 0 || stopped()) break;
+            if (!more) continue;
+            const int X = gk & 1, sub = k.u & k.pair;
+            const uint32_t q = n_q + sub;
+            if (k.u <= k.pair) wait(&sh.q_full[q & 1], q >> 1);
+            if (sub == 0) {
+                k_slot = ring.s;
+                wait(&sh.full[k_slot], ring.phase);
+                ring.next();
+            }
+            if (copied || k.u <= k.pair) tc::fence_proxy_async_smem();
+            tc::tc_fence_after();
+            __syncwarp();
+            const uint64_t qd = tc::smem_desc_sw128(sQ + (q & 1) * L::kOperand);
+            const uint64_t kd = tc::smem_desc_sw128(sRing + k_slot * L::kOperand);
+#pragma unroll
+            for (int j = 0; j < kD / 16; ++j) {
+                const uint64_t at = (uint64_t)((j >> 2) * (L::kHalf >> 4) + (j & 3) * 2);
+                tc::umma_bf16_elect(tmem + X * kBlock, qd + at, kd + at, idesc_s, j != 0);
+            }
+            tc::umma_commit_elect(&sh.s_full[X]);
+            if (sub == k.pair) tc::umma_commit_elect(&sh.empty[k_slot]);
+            if (k.u + k.pair + 1 >= k.steps) tc::umma_commit_elect(&sh.q_empty[q & 1]);
+            ++gk;
+            if (++k.u == k.steps) {
+                n_q += 1 + k.pair;
+                ++k.i;
+                more = open(k);
+            }
+        }
+        __syncwarp();
+        tc::umma_commit_elect(&sh.drain);
+        wait_bounded(&sh.drain, 0);  // (whatever made the CTA stop, its products are done before tensor memory is given back)
+    } else if (warp == 15 && maps.box_rows > 0) {
+        // ================================================================ loads by TMA
+        // A lane has one box of a block, its first key and 64 of its columns.
+        const int none = p.pool_pages * p.hkv * p.page;  // past the matrices: zeros
+        const int boxes = kBlock / maps.box_rows, box_key = lane % boxes * maps.box_rows, half = lane / boxes;
+        const int pages_on = kBlock / p.page, slots_on = kBlock - pages_on * p.page;  // from a block to the next
+        const uint32_t dst = half * L::kHalf + box_key * 128;
+        Ring ring;
+        uint32_t filled = 0;
+        // this lane's box of the next block of keys: its position, page and slot of it, and the page's id
+        int pos = 0, page = 0, slot = 0, id = 0;
+        const int32_t* table = nullptr;
+        int high = 0, head = 0;
+        Cursor k, v;
+        bool more;
+        auto open_k = [&]() {
+            more = open(k);
+            if (!more) return;
+            const Piece& w = *k.at;
+            pos = w.begin + w.b0 * kBlock + box_key;
+            page = pos / p.page;
+            slot = pos - page * p.page;
+            table = p.block_table + (long long)w.table * p.max_blocks;
+            high = w.high;
+            head = w.head;
+            if (pos < high) id = __ldg(table + page);
+        };
+        open_k();
+        open(v);
+        int kept0 = 0, kept1 = 0, n_kept = 0;
+#pragma unroll 1
+        for (int i = opaque(-4); v.steps > 0 && !stopped(); ++i) {  // values of a step, keys of the step after the next
+            const bool is_k = i & 1;
+            if (is_k ? !more : i < 0) continue;
+            const Cursor& c = is_k ? k : v;
+            if (c.leads()) {
+                int row = kept0;
+                uint64_t* bar = &sh.full[ring.s];
+                if (is_k) {
+                    row = none;
+                    if (pos < high) {
+                        if (id >= 0 && id < p.pool_pages) {
+                            row = (id * p.hkv + head) * p.page + slot;
+                        } else {
+                            sh.pieces[k.i % kPieces].spoiled = 1;
+                            report(p.dev_status, DSPARK_ERR_DEVICE_INPUT);
+                        }
+                    }
+                    (n_kept == 0 ? kept0 : kept1) = row;
+                    ++n_kept;
+                    // on to the next block: its page's id is there when it is wanted
+                    pos += kBlock;
+                    page += pages_on;
+                    slot += slots_on;
+                    if (slot >= p.page) {
+                        slot -= p.page;
+                        ++page;
+                    }
+                    if (pos < high) id = __ldg(table + page);
+                } else {
+                    kept0 = kept1;
+                    --n_kept;
+                    if (c.block() >= c.at->look) bar = &sh.landed[ring.s];
+                }
+                if (filled == kSlots) wait(&sh.empty[ring.s], ring.phase ^ 1);
+                else ++filled;
+                __syncwarp();  // (what a lane noted of a missing page goes before the arrival)
+                if (lane == 0) tc::mbar_arrive_expect_tx(bar, L::kOperand);
+                __syncwarp();
+                if (half < kD / 64)
+                    tc::tma_load_2d(base + (2 + ring.s) * L::kOperand + dst, is_k ? &maps.k : &maps.v, bar, half * 64, row);
+                ring.next();
+            }
+            if (is_k) {
+                if (++k.u == k.steps) {
+                    ++k.i;
+                    open_k();
+                }
+            } else if (++v.u == v.steps) {
+                close(v);
+                ++v.i;
+                open(v);
+            }
+        }
+    } else if (warp == 13) {
+        // ================================================================ the pieces, one after the other
+        int i = 0;
+        auto post = [&](const Piece& x) {
+            if (i >= kPieces) wait(&sh.piece_empty[i % kPieces], i / kPieces - 1);
+            if (lane == 0) {
+                sh.pieces[i % kPieces] = x;
+                tc::mbar_arrive(&sh.piece_full[i % kPieces]);
+            }
+            __syncwarp();
+            ++i;
+        };
+        Piece x;
+        x.g0 = x.spoiled = x.n_q = 0;
+        if (x0 < x1) {
+            int e = sh.first_entry;
+            Entry en = sh.first;
+            const int item = (int)divide(x0 - sh.first_start, en.blocks + kItemCost);
+            int h = item / en.tiles, t = item - h * en.tiles;
+            long long start = sh.first_start + (long long)item * (en.blocks + kItemCost);  // the item's first unit
+#pragma unroll 1
+            while (start < x1 && !stopped()) {
+                const int n_blocks = tile_blocks(en, t, g);
+                const long long first = start + kItemCost;
+                const int b0 = x0 > first ? (int)(x0 - first) : 0;
+                const int b1 = x1 - first < n_blocks ? (int)max(x1 - first, 0LL) : n_blocks;
+                if (b0 < b1) {
+                    x.b0 = b0;
+                    x.uncut = b0 == 0 && b1 == n_blocks;
+                    x.row0 = en.row0;
+                    x.tile_row = t * kRows;
+                    x.n_rows = min(en.n * g - t * kRows, kRows);
+                    x.head = h;
+                    x.begin = en.begin;
+                    x.end = en.end;
+                    x.len = en.len;
+                    x.table = en.table;
+                    x.low = en.limit(x.tile_row / g);
+                    x.high = en.limit((x.tile_row + x.n_rows - 1) / g);
+                    x.edge = x.low < x.high ? max((x.low - x.begin) / kBlock - b0, 0) : INT_MAX;
+                    x.look = maps.box_rows > 0 && (x.high - x.begin) % kBlock ? min(x.edge, (x.high - x.begin) / kBlock - b0) : x.edge;
+                    x.pair = x.n_rows > kTile;
+                    x.steps = (b1 - b0) << x.pair;
+                    x.log_copies = x.n_rows <= 32 ? 2 : 0;
+                    x.last_cta = b0 == 0 && !x.uncut ? (int)divide(first + n_blocks - 1, length) : 0;
+                    post(x);
+                    x.g0 += x.steps;
+                    x.n_q += 1 + x.pair;
+                }
+                start += en.blocks + kItemCost;
+                if (++t == en.tiles) {
+                    t = 0;
+                    if (++h == p.hkv) {
+                        h = 0;
+                        if (start < x1)
+                            do en = entry_of<kGroups>(p, ++e); while (en.tiles == 0);
+                    }
+                }
+            }
+        }
+        x.steps = 0;
+        post(x);
+        if (!kGroups && p.n_groups > 0) wait_prior_grid();  // (so that whoever waits for this grid waits for those too)
+        if (!kGroups) {  // requests that cannot be right
+#pragma unroll 1
+            for (int r = blockIdx.x; r < p.R; r += gridDim.x) {
+                const int n = p.cu[r + 1] - p.cu[r];
+                if (n == 0 || entry_of<false>(p, r).n > 0) continue;
+                const long long from = (long long)p.cu[r] * p.hq, to = (long long)p.cu[r + 1] * p.hq;
+#pragma unroll 1
+                for (long long j = from * kD + lane; j < to * kD; j += 32) p.out[j] = kNan;
+                if (p.lse)
+#pragma unroll 1
+                    for (long long j = from + lane; j < to; j += 32) p.lse[j] = __int_as_float(0x7FC00000);
+                if (lane == 0) report(p.dev_status, DSPARK_ERR_DEVICE_INPUT);
+            }
+        }
     }
+    __syncwarp();
     __syncthreads();
-    if (warp == 0) tc::tmem_dealloc(tmem, 256);
+    if (tid == 0 && sh.abort_flag) report(p.dev_status, DSPARK_ERR_TIMEOUT);
+    if (warp == 12) tc::tmem_dealloc(tmem, 512);
 }
 
 // ---------------------------------------------------------------- joining the pieces
-constexpr int kJoinThreads = 256;
+constexpr int kJoinCols = 16;  // of a CTA
 
-struct Joined {
-    float m, l;
-    float o[4];
-};
-
-// Adds the pieces of the row's item over one entry's keys, in their order.  Lane i holds d / 32 elements.
+// CTA (c, i): columns [16 i, 16 i + 16) of the item that CTA c of the attention
+// kernel began and did not finish, a thread to a row; the pieces are added in
+// their order, the shared part first.
 template <int kD, bool kGroups>
-__device__ __forceinline__ void join_entry(const AttnParams& p, const Plan& plan, int max_ctas, int entries, int e, int row,
-                                           int head, Joined& a) {
-    constexpr int kPer = kD / 32;
-    const int lane = threadIdx.x & 31, g = p.hq / p.hkv;
-    const Entry x = entry_of<kGroups>(p, e);
-    if (x.n == 0) return;
-    const int h = head / g;
-    const long long at = (long long)(row - x.row0) * g + (head - h * g);
-    const int t = (int)(at / kTile), r = (int)(at % kTile);
-    const long long s0 = plan.start[e] + ((long long)h * x.tiles + t) * (x.blocks + kItemCost) + kItemCost;
-    const int n_blocks = tile_blocks(x, t, g);
-    const long long total = plan.start[entries];
-    const int ctas = pieces(total, max_ctas);
-    const int c0 = cta_of(s0, total, ctas), c1 = cta_of(s0 + n_blocks - 1, total, ctas);
-    for (int c = c0; c <= c1; ++c) {
-        const long long item = (long long)row * p.hq + head;
-        const long long slot = (long long)(2 * c + (c == c0)) * kTile + r;
-        const float2 ml = c0 == c1 ? plan.whole_ml[item] : plan.part_ml[slot];
-        const float* from = (c0 == c1 ? plan.whole + item * kD : plan.part + slot * kD) + lane * kPer;
-        float o[4];
-        if (kPer == 4) *reinterpret_cast<float4*>(o) = *reinterpret_cast<const float4*>(from);
-        else *reinterpret_cast<float2*>(o) = *reinterpret_cast<const float2*>(from);
-        const float top = fmaxf(a.m, ml.x);
-        const float fa = a.m == -INFINITY ? 0.0f : exp2f(a.m - top);
-        const float fb = ml.x == -INFINITY && ml.y == 0.0f ? 0.0f : exp2f(ml.x - top);
-        a.m = top;
-        a.l = a.l * fa + ml.y * fb;
+__global__ void __launch_bounds__(kRows) join_kernel(const AttnParams p, const Plan plan, const Plan shared_plan) {
+    constexpr int kQuads = kJoinCols / 4;
+    launch_dependents();
+    wait_prior_grid();
+    const Job job = plan.jobs[blockIdx.x];
+    const int r = threadIdx.x, g = p.hq / p.hkv;
+    if (r >= job.n_rows) return;
+    const int col = blockIdx.y * kQuads;  // in fours
+    const int lin = job.row0 * g + job.tile_row + r;
+    const size_t lin_step = (size_t)p.rows * g, lin_ml = (size_t)job.head * p.rows * g + lin;
+    const size_t lin_at = ((size_t)job.head * (kD / 4) + col) * lin_step + lin;
+    float m = -INFINITY, l = 0.0f;
+    float4 o[kQuads];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) a.o[i] = a.o[i] * fa + o[i] * fb;
-    }
-}
-
-// One warp per (row, query head): rows whose item was cut, or that have a
-// shared part, get their sums; rows of requests that cannot be right get NaN.
-template <int kD>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnParams p, const Plan plan, const Plan shared_plan,
-                                                           const int max_ctas) {
-    constexpr int kPer = kD / 32;
-    const int lane = threadIdx.x & 31;
-    const long long item = (long long)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
-    if (item >= (long long)p.rows * p.hq) return;
-    const int row = (int)(item / p.hq), head = (int)(item % p.hq), g = p.hq / p.hkv;
-    bool ok = *plan.bad == 0;
-    if (!ok && item == 0 && lane == 0) report(p.dev_status, DSPARK_ERR_DEVICE_INPUT);
-    Joined a{-INFINITY, 0.0f, {0.0f, 0.0f, 0.0f, 0.0f}};
-    if (ok) {
-        if (row >= p.cu[p.R]) return;
-        const int r = owner_of(p.cu, p.R, row);
-        const Entry x = entry_of<false>(p, r);
-        if (x.n == 0) {  // a length, or its group, is bad
-            ok = false;
-            if (lane == 0) report(p.dev_status, DSPARK_ERR_DEVICE_INPUT);
-        } else {
-            if (p.n_groups == 0) {
-                const long long at = (long long)(row - x.row0) * g + head % g;
-                const int t = (int)(at / kTile);
-                const long long s0 = plan.start[r] + ((long long)(head / g) * x.tiles + t) * (x.blocks + kItemCost) + kItemCost;
-                const long long total = plan.start[p.R];
-                const int ctas = pieces(total, max_ctas);
-                if (cta_of(s0, total, ctas) == cta_of(s0 + tile_blocks(x, t, g) - 1, total, ctas)) return;  // not cut
-            } else {
-                join_entry<kD, true>(p, shared_plan, max_ctas, p.n_groups, group_of(p, r), row, head, a);
-            }
-            join_entry<kD, false>(p, plan, max_ctas, p.R, r, row, head, a);
+    for (int q = 0; q < kQuads; ++q) o[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int c = job.first - job.merge_prefix; c <= job.last; ++c) {
+        const bool shared = c < job.first;
+        const size_t slot = (size_t)(2 * c + (c == job.first)) * kRows;
+        const float2 ml = shared ? shared_plan.whole_ml[lin_ml] : plan.part_ml[slot + r];
+        const float4* from = shared ? reinterpret_cast<const float4*>(shared_plan.whole) + lin_at
+                                    : reinterpret_cast<const float4*>(plan.part + slot * kD) + col * kRows + r;
+        const size_t step = shared ? lin_step : kRows;
+        const float top = fmaxf(m, ml.x);
+        const float fa = m == -INFINITY ? 0.0f : exp2_approx(m - top), fb = ml.x == -INFINITY ? 0.0f : exp2_approx(ml.x - top);
+        l = (m == -INFINITY ? l : l * fa) + (ml.x == -INFINITY ? ml.y : ml.y * fb);
+        m = top;
+#pragma unroll
+        for (int q = 0; q < kQuads; ++q) {
+            const float4 v = from[q * step];
+            o[q].x = o[q].x * fa + v.x * fb; o[q].y = o[q].y * fa + v.y * fb;
+            o[q].z = o[q].z * fa + v.z * fb; o[q].w = o[q].w * fa + v.w * fb;
         }
     }
-    const float inv = ok ? 1.0f / a.l : __int_as_float(0x7FC00000);
-    __nv_bfloat16 w[kPer];
+    if (kGroups) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) w[i] = __float2bfloat16(ok ? a.o[i] * inv : inv);
-    if (kPer == 4) *reinterpret_cast<uint2*>(p.out + item * kD + lane * kPer) = *reinterpret_cast<const uint2*>(w);
-    else *reinterpret_cast<uint32_t*>(p.out + item * kD + lane * kPer) = *reinterpret_cast<const uint32_t*>(w);
-    if (p.lse && lane == 0) p.lse[item] = ok ? (a.m + log2f(a.l)) * kLn2 : inv;
+        for (int q = 0; q < kQuads; ++q) reinterpret_cast<float4*>(plan.whole)[lin_at + q * lin_step] = o[q];
+        if (col == 0) plan.whole_ml[lin_ml] = make_float2(m, l);
+    } else {
+        const int i = (job.tile_row + r) / g;
+        const size_t item = (size_t)(job.row0 + i) * p.hq + job.head * g + (job.tile_row + r - i * g);
+        const float inv = 1.0f / l;
+        alignas(16) __nv_bfloat162 w[2 * kQuads];
+#pragma unroll
+        for (int q = 0; q < kQuads; ++q) {
+            w[2 * q] = __floats2bfloat162_rn(o[q].x * inv, o[q].y * inv);
+            w[2 * q + 1] = __floats2bfloat162_rn(o[q].z * inv, o[q].w * inv);
+        }
+        uint4* to = reinterpret_cast<uint4*>(p.out + item * kD + col * 4);
+#pragma unroll
+        for (int q = 0; q < kQuads / 2; ++q) to[q] = reinterpret_cast<const uint4*>(w)[q];
+        if (p.lse && col == 0) p.lse[item] = (m + log2f(l)) * kLn2;
+    }
 }
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
 // One launch's plan in the workspace at `off` (which moves on).
-Plan plan_at(void* ws, size_t& off, int entries, long long items, int d, bool whole) {
+Plan plan_at(void* ws, size_t& off, long long items, int d, bool whole) {
     unsigned char* b = static_cast<unsigned char*>(ws);
     Plan p;
-    p.bad = reinterpret_cast<int*>(b + off); off += 256;
-    p.start = reinterpret_cast<long long*>(b + off); off += up(sizeof(long long) * ((size_t)entries + 1));
-    p.part = reinterpret_cast<float*>(b + off); off += sizeof(float) * 2 * kMaxCtas * kTile * (size_t)d;
-    p.part_ml = reinterpret_cast<float2*>(b + off); off += sizeof(float2) * 2 * kMaxCtas * kTile;
+    p.jobs = reinterpret_cast<Job*>(b + off); off += up(sizeof(Job) * kMaxCtas);
+    p.part = reinterpret_cast<float*>(b + off); off += sizeof(float) * 2 * kMaxCtas * kRows * (size_t)d;
+    p.part_ml = reinterpret_cast<float2*>(b + off); off += sizeof(float2) * 2 * kMaxCtas * kRows;
     p.whole = reinterpret_cast<float*>(b + off); off += whole ? up(sizeof(float) * (size_t)items * d) : 0;
     p.whole_ml = reinterpret_cast<float2*>(b + off); off += whole ? up(sizeof(float2) * (size_t)items) : 0;
     return p;
 }
 
+// A launch that may start while the kernel before it in the stream runs (which
+// it waits for itself).
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encoder() {
+    static const EncodeTiled fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                        q == cudaDriverEntryPointSuccess;
+        return ok ? reinterpret_cast<EncodeTiled>(f) : nullptr;
+    }();
+    return fn;
+}
+
+// A [rows, d] matrix of bf16 in boxes of box_rows x 64.
+bool encode_boxes(CUtensorMap* m, const void* base, long long rows, int d, int box_rows) {
+    const EncodeTiled enc = encoder();
+    const cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)d * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+    const cuuint32_t es[2] = {1, 1};
+    return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int kD>
 cudaError_t launch_d(const AttnParams& p, cudaStream_t stream) {
+    Maps maps{};
+    int box_rows = 128;  // the largest power of two that every page is a multiple of
+    while (p.page % box_rows) box_rows /= 2;
+    if (box_rows >= 8 && p.pool_pages > 0) {
+        const long long rows = (long long)p.pool_pages * p.hkv * p.page;
+        if (!encode_boxes(&maps.k, p.k_cache, rows, kD, box_rows) || !encode_boxes(&maps.v, p.v_cache, rows, kD, box_rows))
+            return cudaErrorInvalidValue;
+        maps.box_rows = box_rows;
+    }
     int dev = 0, n_sm = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
     if ((err = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return err;
-    const int ctas = 2 * n_sm < kMaxCtas ? 2 * n_sm : kMaxCtas;
+    const int ctas = n_sm < kMaxCtas ? n_sm : kMaxCtas;
     const long long items = (long long)p.rows * p.hq;
     size_t off = 0;
-    const Plan plan = plan_at(p.ws, off, p.R, items, kD, p.n_groups > 0);
+    const Plan plan = plan_at(p.ws, off, items, kD, false);
     Plan shared_plan = plan;
-    const int smem = Smem<kD>::kTotal;
-    if (p.n_groups > 0) {
-        shared_plan = plan_at(p.ws, off, p.n_groups, items, kD, true);
-        if ((err = cudaFuncSetAttribute(attention_kernel<kD, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
-            return err;
-        attention_kernel<kD, true><<<ctas, kThreads, smem, stream>>>(p, shared_plan, ctas, p.n_groups);
-        if ((err = cudaGetLastError()) != cudaSuccess) return err;
-    }
+    const int smem = Layout<kD>::kTotal;
+    const dim3 join_grid(ctas, kD / kJoinCols);
     if ((err = cudaFuncSetAttribute(attention_kernel<kD, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
         return err;
-    attention_kernel<kD, false><<<ctas, kThreads, smem, stream>>>(p, plan, ctas, p.R);
-    if ((err = cudaGetLastError()) != cudaSuccess) return err;
-    const unsigned grid = (unsigned)((items + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
-    join_kernel<kD><<<grid, kJoinThreads, 0, stream>>>(p, plan, shared_plan, ctas);
-    return cudaGetLastError();
+    if (p.n_groups > 0) {
+        shared_plan = plan_at(p.ws, off, items, kD, true);
+        if ((err = cudaFuncSetAttribute(attention_kernel<kD, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
+            return err;
+        attention_kernel<kD, true><<<ctas, kThreads, smem, stream>>>(p, shared_plan, shared_plan, ctas, p.n_groups, maps);
+        if ((err = cudaGetLastError()) != cudaSuccess) return err;
+        if ((err = launch_after(join_kernel<kD, true>, join_grid, kRows, 0, stream, p, shared_plan, shared_plan)) != cudaSuccess)
+            return err;
+        if ((err = launch_after(attention_kernel<kD, false>, dim3(ctas), kThreads, smem, stream, p, plan, shared_plan, ctas, p.R, maps)) != cudaSuccess)
+            return err;
+    } else {
+        attention_kernel<kD, false><<<ctas, kThreads, smem, stream>>>(p, plan, plan, ctas, p.R, maps);
+        if ((err = cudaGetLastError()) != cudaSuccess) return err;
+    }
+    return launch_after(join_kernel<kD, false>, join_grid, kRows, 0, stream, p, plan, shared_plan);
 }
 
 }  // namespace
 
-size_t attention_workspace(int R, int n_groups, int rows, int hq, int, int d) {
+size_t attention_workspace(int, int n_groups, int rows, int hq, int, int d) {
     size_t off = 0;
-    plan_at(nullptr, off, R, (long long)rows * hq, d, n_groups > 0);
-    if (n_groups > 0) plan_at(nullptr, off, n_groups, (long long)rows * hq, d, true);
+    plan_at(nullptr, off, (long long)rows * hq, d, false);
+    if (n_groups > 0) plan_at(nullptr, off, (long long)rows * hq, d, true);
     return off;
 }
 
