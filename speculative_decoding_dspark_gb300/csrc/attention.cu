@@ -29,13 +29,13 @@
 // at most, and l adds the weights before it.
 //
 // One CTA per SM, sixteen warps: 0-3 and 4-7 form the exponentials of the two
-// tiles, 8-11 and 15 load, 12 issues the products, 13 walks along the items, 14
+// tiles, 8-11 load keys and values, 15 queries, 12 issues the products, 13 walks along the items, 14
 // looks at blocks of values that not every row sees whole.  Keys and values come
 // through a ring of 160 KB, queries through two buffers, so that the next item's
 // first product does not wait for the last one's output.  Pages of a multiple of
-// 8 slots come by TMA, each lane of warp 15 having a box of up to 128 rows by 64
-// elements inside one page.  Other pages may end anywhere in a block: their rows
-// are gathered by 16-byte copies (warps 8-11, a row to a lane), which have about
+// 8 slots come by TMA, each lane of a loading warp having a box of up to 128 rows
+// by 64 elements inside one page.  Other pages may end anywhere in a block: their rows
+// are gathered by 16-byte copies (a row to a lane, the queries' too), which have about
 // 64 KB in flight per SM where TMA has the whole ring (949 MB of keys and values:
 // 200 us).  Four rows to a TMA gather would move 6.4 bytes a cycle (500 us).
 //
@@ -146,13 +146,6 @@ __device__ __forceinline__ Entry entry_of(const AttnParams& p, int e) {
         x.blocks = (x.end - x.begin + kBlock - 1) / kBlock;
     }
     return x;
-}
-
-// Blocks of tile t of an entry that some row of it sees.
-__device__ __forceinline__ int tile_blocks(const Entry& x, int t, int g) {
-    const int last = (int)(((uint32_t)t * kRows + kRows - 1) / (uint32_t)g);
-    const int i = last < x.n - 1 ? last : x.n - 1;
-    return (x.limit(i) - x.begin + kBlock - 1) / kBlock;
 }
 
 // a / b, which is short where both fit 32 bits.
@@ -329,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         }
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&sh.q_full[i], kLoaders);
+            tc::mbar_init(&sh.q_full[i], maps.box_rows > 0 ? 32 : kLoaders);
             tc::mbar_init(&sh.q_empty[i], 2);
             tc::mbar_init(&sh.s_full[i], 1);
             tc::mbar_init(&sh.p_full[i], 4);
@@ -724,6 +717,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                         tc::tmem_ld_32x32b_x16<0>(tO + c0 + c, o);
                         if (two) tc::tmem_ld_32x32b_x16<0>(tO2 + c0 + c, o2);
                         tc::tmem_ld_wait();
+                        if (c0 + c + 16 == kD) {  // the next item's products may have the place
+                            tc::tc_fence_before();
+                            arrive(&sh.o_free[X]);
+                            if (two) arrive(&sh.o_free[X ^ 1]);
+                        }
 #pragma unroll
                         for (int j = 0; j < 16; ++j) o[j] = two ? o[j] * f1 + o2[j] * f2 : o[j] * f1;
 #pragma unroll
@@ -734,19 +732,25 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                     }
                     tile_sync();
                     constexpr int kQuads = kD / 8;  // of four columns, in this half
+                    auto sum_of = [&](int q, int r) {  // over the copies
+                        float4 y = stage[q * kTile + (r ^ (q & 15))];
+                        if (log_copies) {
+#pragma unroll
+                            for (int c = 32; c < kTile; c += 32) {
+                                const float4 v = stage[q * kTile + ((c + r) ^ (q & 15))];
+                                y.x += v.x; y.y += v.y; y.z += v.z; y.w += v.w;
+                            }
+                        }
+                        return y;
+                    };
                     if (final) {  // a row's columns side by side
                         const int q = t128 % kQuads;
-#pragma unroll 1
+#pragma unroll 2
                         for (int r = t128 / kQuads; r < n_rows; r += kTile / kQuads) {
                             const float2 f = sh.ml[X][r];
                             float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                             if (prefix) x = shared_part[(size_t)(c0 / 4 + q) * lin_step + lin0 + r];
-                            float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 1
-                            for (int c = r; c < kTile; c += 1 << log_rows) {
-                                const float4 v = stage[q * kTile + (c ^ (q & 15))];
-                                y.x += v.x; y.y += v.y; y.z += v.z; y.w += v.w;
-                            }
+                            const float4 y = sum_of(q, r);
                             const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x + x.x * f.x, y.y + x.y * f.x);
                             const __nv_bfloat162 hi = __floats2bfloat162_rn(y.z + x.z * f.x, y.w + x.w * f.x);
                             *reinterpret_cast<uint2*>(p.out + (size_t)__float_as_int(f.y) * kD + c0 + 4 * q) =
@@ -756,12 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                         const int r = t_row;
 #pragma unroll 1
                         for (int q = t128 >> log_rows; q < kQuads && live; q += 1 << log_copies) {
-                            float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 1
-                            for (int c = r; c < kTile; c += 1 << log_rows) {
-                                const float4 v = stage[q * kTile + (c ^ (q & 15))];
-                                y.x += v.x; y.y += v.y; y.z += v.z; y.w += v.w;
-                            }
+                            const float4 y = sum_of(q, r);
                             to[(size_t)(c0 / 4 + q) * to_step + to0 + r] = y;
                         }
                     }
@@ -772,10 +771,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                 if (!final) (uncut ? plan.whole_ml + (size_t)w.head * lin_step : plan.part_ml + slot)[to0 + t_row] = make_float2(m, l);
                 else if (p.lse) p.lse[row_of_out(t_row)] = (m + log2f(l)) * kLn2;
             }
-            tc::tc_fence_before();
-            arrive(&sh.o_free[X]);
-            if (two) arrive(&sh.o_free[X ^ 1]);
-            tile_sync();
             if (t128 == 0) {
                 tc::mbar_arrive(&sh.q_empty[(w.n_q + sub) & 1]);
                 if (!uncut && w.b0 == 0 && sub == 0) {
@@ -792,10 +787,100 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                 }
             }
         }
-    } else if (warp < 12) {
-        // ================================================================ loads
+    } else if (warp < 12 && maps.box_rows > 0) {
+        // ================================================================ loads by TMA
+        // A lane has one box of a block, its first key and 64 of its columns; the four warps take the slots in turn
+        // (a slot takes a warp about 1500 cycles, of pages of 16).  Each waits for every slot to be empty, its own or
+        // not: a warp that skipped a slot's phase could take the one before it for it.
+        const int none = p.pool_pages * p.hkv * p.page;  // past the matrices: zeros
+        const int boxes = kBlock / maps.box_rows, box_key = lane % boxes * maps.box_rows, half = lane / boxes;
+        const int pages_on = kBlock / p.page, slots_on = kBlock - pages_on * p.page;  // from a block to the next
+        const uint32_t dst = half * L::kHalf + box_key * 128;
+        Ring ring;
+        uint32_t filled = 0, turn = warp & 3;  // slots until this warp's next
+        // this lane's box of the next block of keys: its position, page and slot of it, and the page's id
+        int pos = 0, page = 0, slot = 0, id = 0;
+        const int32_t* table = nullptr;
+        int high = 0, head = 0;
+        Cursor k, v;
+        bool more;
+        auto open_k = [&]() {
+            more = open(k);
+            if (!more) return;
+            const Piece& w = *k.at;
+            pos = w.begin + w.b0 * kBlock + box_key;
+            page = pos / p.page;
+            slot = pos - page * p.page;
+            table = p.block_table + (long long)w.table * p.max_blocks;
+            high = w.high;
+            head = w.head;
+            if (pos < high) id = __ldg(table + page);
+        };
+        open_k();
+        open(v);
+        int kept0 = 0, kept1 = 0, n_kept = 0;
+#pragma unroll 1
+        for (int i = opaque(-4); v.steps > 0 && !stopped(); ++i) {  // values of a step, keys of the step after the next
+            const bool is_k = i & 1;
+            if (is_k ? !more : i < 0) continue;
+            const Cursor& c = is_k ? k : v;
+            if (c.leads()) {
+                int row = kept0;
+                uint64_t* bar = &sh.full[ring.s];
+                if (is_k) {
+                    row = none;
+                    if (pos < high) {
+                        if (id >= 0 && id < p.pool_pages) {
+                            row = (id * p.hkv + head) * p.page + slot;
+                        } else {
+                            sh.pieces[k.i % kPieces].spoiled = 1;
+                            report(p.dev_status, DSPARK_ERR_DEVICE_INPUT);
+                        }
+                    }
+                    (n_kept == 0 ? kept0 : kept1) = row;
+                    ++n_kept;
+                    // on to the next block: its page's id is there when it is wanted
+                    pos += kBlock;
+                    page += pages_on;
+                    slot += slots_on;
+                    if (slot >= p.page) {
+                        slot -= p.page;
+                        ++page;
+                    }
+                    if (pos < high) id = __ldg(table + page);
+                } else {
+                    kept0 = kept1;
+                    --n_kept;
+                    if (c.block() >= c.at->look) bar = &sh.landed[ring.s];
+                }
+                if (filled == kSlots) wait(&sh.empty[ring.s], ring.phase ^ 1);
+                else ++filled;
+                if (turn == 0) {
+                    __syncwarp();  // (what a lane noted of a missing page goes before the arrival)
+                    if (lane == 0) tc::mbar_arrive_expect_tx(bar, L::kOperand);
+                    __syncwarp();
+                    if (half < kD / 64)
+                        tc::tma_load_2d(base + (2 + ring.s) * L::kOperand + dst, is_k ? &maps.k : &maps.v, bar, half * 64, row);
+                }
+                turn = (turn - 1) & 3;
+                ring.next();
+            }
+            if (is_k) {
+                if (++k.u == k.steps) {
+                    ++k.i;
+                    open_k();
+                }
+            } else if (++v.u == v.steps) {
+                close(v);
+                ++v.i;
+                open(v);
+            }
+        }
+    } else if (warp < 12 || warp == 15) {
+        // ================================================================ rows copied one by one
+        // (with TMA: of the queries alone, by warp 15)
         constexpr int kNone = -1, kMissing = -2;
-        const int t128 = tid - 256, part = warp - 8;
+        const int part = warp & 3;
         uint32_t n_q = 0;
         auto first_key = [](const Cursor& c) { return c.at->begin + (c.at->b0 + c.block()) * kBlock; };
         // the cache row of this lane's key of the cursor's block
@@ -809,7 +894,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
             return (id * p.hkv + w.head) * p.page + (pos - pb * p.page);
         };
         // This lane's row and those of its warp (row < 0: zeros) to their places of an operand.
-        auto copy = [&](uint32_t dst, const __nv_bfloat16* rows, int row) {
+        auto copy = [&](uint32_t dst, int part, const __nv_bfloat16* rows, int row) {
             constexpr int kPerPass = 32 / kChunks;  // rows that 32 chunks make up
             const int c = lane % kChunks;
             const char* const from = reinterpret_cast<const char*>(rows) + c * 16;
@@ -820,12 +905,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                 tc::cp_async_16(dst + chunk_offset(r, c), from + (size_t)max(from_row, 0) * (kD * 2), from_row < 0 ? 0 : 16);
             }
         };
-        auto load_q = [&](const Piece& w, int sub) {
+        // parts [p0, p1) of a tile's queries
+        auto load_q = [&](const Piece& w, int sub, int p0, int p1) {
             const int q = n_q & 1;
-            const int t_row = t128 & ((kTile >> w.log_copies) - 1), at = w.tile_row + sub * kTile + t_row, qi = at / g;
-            const int row = sub * kTile + t_row < w.n_rows ? (w.row0 + qi) * p.hq + w.head * g + (at - qi * g) : kNone;
             if (n_q >= 2) wait(&sh.q_empty[q], (n_q >> 1) - 1);
-            copy(sQ + q * L::kOperand, p.q, row);
+#pragma unroll 1
+            for (int i = p0; i < p1; ++i) {
+                const int t_row = (32 * i + lane) & ((kTile >> w.log_copies) - 1), at = w.tile_row + sub * kTile + t_row, qi = at / g;
+                copy(sQ + q * L::kOperand, i, p.q,
+                     sub * kTile + t_row < w.n_rows ? (w.row0 + qi) * p.hq + w.head * g + (at - qi * g) : kNone);
+            }
             cp_async_arrive_noinc(&sh.q_full[q]);
             ++n_q;
         };
@@ -835,12 +924,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
 #pragma unroll 1
             while (more && !stopped()) {
 #pragma unroll 1
-                for (k.u = 0; k.u <= k.pair; ++k.u) load_q(*k.at, k.u);
+                for (k.u = 0; k.u <= k.pair; ++k.u) load_q(*k.at, k.u, 0, 4);
                 close(k);
                 ++k.i;
                 more = open(k);
             }
-        } else {
+        } else if (warp < 12) {
             // Keys two steps ahead of the values, as the products take them.  A block's rows are looked up once, a
             // step before its keys are loaded, and kept until its values are.
             Cursor v;
@@ -859,7 +948,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                     continue;
                 }
                 if (is_k && queries) {
-                    load_q(*k.at, k.u);
+                    load_q(*k.at, k.u, part, part + 1);
                     queries = false;
                     continue;
                 }
@@ -881,7 +970,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                     uint64_t* const bar = !is_k && c.block() >= c.at->look ? &sh.landed[ring.s] : &sh.full[ring.s];
                     if (filled == kSlots) wait(&sh.empty[ring.s], ring.phase ^ 1);
                     else ++filled;
-                    copy(sRing + ring.s * L::kOperand, is_k ? p.k_cache : p.v_cache, row);
+                    copy(sRing + ring.s * L::kOperand, part, is_k ? p.k_cache : p.v_cache, row);
                     if (__any_sync(0xFFFFFFFFu, row == kMissing)) {  // (what the warp noted of it goes before the arrival)
                         asm volatile("cp.async.wait_all;" ::: "memory");
                         tc::mbar_arrive(bar);
@@ -1049,90 +1138,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         __syncwarp();
         tc::umma_commit_elect(&sh.drain);
         wait_bounded(&sh.drain, 0);  // (whatever made the CTA stop, its products are done before tensor memory is given back)
-    } else if (warp == 15 && maps.box_rows > 0) {
-        // ================================================================ loads by TMA
-        // A lane has one box of a block, its first key and 64 of its columns.
-        const int none = p.pool_pages * p.hkv * p.page;  // past the matrices: zeros
-        const int boxes = kBlock / maps.box_rows, box_key = lane % boxes * maps.box_rows, half = lane / boxes;
-        const int pages_on = kBlock / p.page, slots_on = kBlock - pages_on * p.page;  // from a block to the next
-        const uint32_t dst = half * L::kHalf + box_key * 128;
-        Ring ring;
-        uint32_t filled = 0;
-        // this lane's box of the next block of keys: its position, page and slot of it, and the page's id
-        int pos = 0, page = 0, slot = 0, id = 0;
-        const int32_t* table = nullptr;
-        int high = 0, head = 0;
-        Cursor k, v;
-        bool more;
-        auto open_k = [&]() {
-            more = open(k);
-            if (!more) return;
-            const Piece& w = *k.at;
-            pos = w.begin + w.b0 * kBlock + box_key;
-            page = pos / p.page;
-            slot = pos - page * p.page;
-            table = p.block_table + (long long)w.table * p.max_blocks;
-            high = w.high;
-            head = w.head;
-            if (pos < high) id = __ldg(table + page);
-        };
-        open_k();
-        open(v);
-        int kept0 = 0, kept1 = 0, n_kept = 0;
-#pragma unroll 1
-        for (int i = opaque(-4); v.steps > 0 && !stopped(); ++i) {  // values of a step, keys of the step after the next
-            const bool is_k = i & 1;
-            if (is_k ? !more : i < 0) continue;
-            const Cursor& c = is_k ? k : v;
-            if (c.leads()) {
-                int row = kept0;
-                uint64_t* bar = &sh.full[ring.s];
-                if (is_k) {
-                    row = none;
-                    if (pos < high) {
-                        if (id >= 0 && id < p.pool_pages) {
-                            row = (id * p.hkv + head) * p.page + slot;
-                        } else {
-                            sh.pieces[k.i % kPieces].spoiled = 1;
-                            report(p.dev_status, DSPARK_ERR_DEVICE_INPUT);
-                        }
-                    }
-                    (n_kept == 0 ? kept0 : kept1) = row;
-                    ++n_kept;
-                    // on to the next block: its page's id is there when it is wanted
-                    pos += kBlock;
-                    page += pages_on;
-                    slot += slots_on;
-                    if (slot >= p.page) {
-                        slot -= p.page;
-                        ++page;
-                    }
-                    if (pos < high) id = __ldg(table + page);
-                } else {
-                    kept0 = kept1;
-                    --n_kept;
-                    if (c.block() >= c.at->look) bar = &sh.landed[ring.s];
-                }
-                if (filled == kSlots) wait(&sh.empty[ring.s], ring.phase ^ 1);
-                else ++filled;
-                __syncwarp();  // (what a lane noted of a missing page goes before the arrival)
-                if (lane == 0) tc::mbar_arrive_expect_tx(bar, L::kOperand);
-                __syncwarp();
-                if (half < kD / 64)
-                    tc::tma_load_2d(base + (2 + ring.s) * L::kOperand + dst, is_k ? &maps.k : &maps.v, bar, half * 64, row);
-                ring.next();
-            }
-            if (is_k) {
-                if (++k.u == k.steps) {
-                    ++k.i;
-                    open_k();
-                }
-            } else if (++v.u == v.steps) {
-                close(v);
-                ++v.i;
-                open(v);
-            }
-        }
     } else if (warp == 13) {
         // ================================================================ the pieces, one after the other
         int i = 0;
@@ -1155,7 +1160,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
             long long start = sh.first_start + (long long)item * (en.blocks + kItemCost);  // the item's first unit
 #pragma unroll 1
             while (start < x1 && !stopped()) {
-                const int n_blocks = tile_blocks(en, t, g);
+                const int tile_row = t * kRows, n_rows = min(en.n * g - tile_row, kRows);
+                const int high = en.limit((tile_row + n_rows - 1) / g), n_blocks = (high - en.begin + kBlock - 1) / kBlock;
                 const long long first = start + kItemCost;
                 const int b0 = x0 > first ? (int)(x0 - first) : 0;
                 const int b1 = x1 - first < n_blocks ? (int)max(x1 - first, 0LL) : n_blocks;
@@ -1163,21 +1169,23 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                     x.b0 = b0;
                     x.uncut = b0 == 0 && b1 == n_blocks;
                     x.row0 = en.row0;
-                    x.tile_row = t * kRows;
-                    x.n_rows = min(en.n * g - t * kRows, kRows);
+                    x.tile_row = tile_row;
+                    x.n_rows = n_rows;
                     x.head = h;
                     x.begin = en.begin;
                     x.end = en.end;
                     x.len = en.len;
                     x.table = en.table;
-                    x.low = en.limit(x.tile_row / g);
-                    x.high = en.limit((x.tile_row + x.n_rows - 1) / g);
-                    x.edge = x.low < x.high ? max((x.low - x.begin) / kBlock - b0, 0) : INT_MAX;
-                    x.look = maps.box_rows > 0 && (x.high - x.begin) % kBlock ? min(x.edge, (x.high - x.begin) / kBlock - b0) : x.edge;
-                    x.pair = x.n_rows > kTile;
+                    x.low = en.limit(t ? tile_row / g : 0);
+                    x.high = high;
+                    x.edge = x.low < high ? max((x.low - en.begin) / kBlock - b0, 0) : INT_MAX;
+                    x.look = maps.box_rows > 0 && (high - en.begin) % kBlock ? min(x.edge, n_blocks - 1 - b0) : x.edge;
+                    x.pair = n_rows > kTile;
                     x.steps = (b1 - b0) << x.pair;
-                    x.log_copies = x.n_rows <= 32 ? 2 : 0;
-                    x.last_cta = b0 == 0 && !x.uncut ? (int)divide(first + n_blocks - 1, length) : 0;
+                    x.log_copies = n_rows <= 32 ? 2 : 0;
+                    x.last_cta = 0;
+                    if (b0 == 0 && !x.uncut)  // (the last CTA with a piece: every one has `length` units)
+                        x.last_cta = blockIdx.x + 1 + (int)divide(first + n_blocks - 1 - x1, length);
                     post(x);
                     x.g0 += x.steps;
                     x.n_q += 1 + x.pair;
