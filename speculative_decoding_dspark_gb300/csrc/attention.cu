@@ -258,9 +258,6 @@ struct Shared {
     volatile int abort_flag;
     uint32_t tmem_base;
     long long scan[kThreads / 32];
-    long long first_start;
-    int first_entry;
-    Entry first;
 };
 
 template <int kD>
@@ -311,70 +308,62 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         tc::tmem_alloc(&sh.tmem_base, 512);
         tc::tmem_relinquish();
     }
-    if (tid == 0) {
-        sh.abort_flag = 0;
-        plan.jobs[blockIdx.x].n_rows = 0;
-#pragma unroll 1
-        for (int i = 0; i < kSlots; ++i) {
-            tc::mbar_init(&sh.full[i], loaders);
-            tc::mbar_init(&sh.landed[i], loaders);
-            tc::mbar_init(&sh.empty[i], 1);
+    if (warp == 13) {
+        if (lane < kSlots) {
+            tc::mbar_init(&sh.full[lane], loaders);
+            tc::mbar_init(&sh.landed[lane], loaders);
+            tc::mbar_init(&sh.empty[lane], 1);
         }
-#pragma unroll 1
-        for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&sh.q_full[i], maps.box_rows > 0 ? 32 : kLoaders);
-            tc::mbar_init(&sh.q_empty[i], 2);
-            tc::mbar_init(&sh.s_full[i], 1);
-            tc::mbar_init(&sh.p_full[i], 4);
-            tc::mbar_init(&sh.o_done[i], 1);
-            tc::mbar_init(&sh.o_free[i], 4);
+        if (lane < 2) {
+            tc::mbar_init(&sh.q_full[lane], maps.box_rows > 0 ? 32 : kLoaders);
+            tc::mbar_init(&sh.q_empty[lane], 2);
+            tc::mbar_init(&sh.s_full[lane], 1);
+            tc::mbar_init(&sh.p_full[lane], 4);
+            tc::mbar_init(&sh.o_done[lane], 1);
+            tc::mbar_init(&sh.o_free[lane], 4);
         }
-#pragma unroll 1
-        for (int i = 0; i < kPieces; ++i) {
-            tc::mbar_init(&sh.piece_full[i], 1);
-            tc::mbar_init(&sh.piece_empty[i], kReaders + (maps.box_rows > 0));
+        if (lane < kPieces) {
+            tc::mbar_init(&sh.piece_full[lane], 1);
+            tc::mbar_init(&sh.piece_empty[lane], kReaders + (maps.box_rows > 0));
         }
-        tc::mbar_init(&sh.merge, 4);
-        tc::mbar_init(&sh.drain, 1);
+        if (lane == 0) {
+            tc::mbar_init(&sh.merge, 4);
+            tc::mbar_init(&sh.drain, 1);
+            sh.abort_flag = 0;
+            plan.jobs[blockIdx.x].n_rows = 0;
+        }
         tc::fence_barrier_init();
     }
+    // every thread has `per` entries
     const int per = (entries + kThreads - 1) / kThreads;
-    const int e0 = min(entries, tid * per), e1 = min(entries, e0 + per);
-    Entry first{};  // this thread's first
+    auto cost_of = [&](int t) {
+        long long c = 0;
+#pragma unroll 1
+        for (int e = t * per; e < min(entries, (t + 1) * per); ++e) c += entry_of<kGroups>(p, e).cost(p.hkv);
+        return c;
+    };
+    auto scanned = [&](long long c) {  // over the warp, each lane's included
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long up = __shfl_up_sync(0xFFFFFFFFu, c, o);
+            if (lane >= o) c += up;
+        }
+        return c;
+    };
+    int bad = p.cu[0] != 0 || p.cu[p.R] > p.rows;
+    if (p.n_groups) bad |= p.group_start[0] != 0 || p.group_start[p.n_groups] != p.R;
+#pragma unroll 1
+    for (int r = tid; r < p.R; r += kThreads) bad |= p.cu[r] > p.cu[r + 1];
+#pragma unroll 1
+    for (int e = tid; e < p.n_groups; e += kThreads) {
+        const int r0 = p.group_start[e], r1 = p.group_start[e + 1];
+        bad |= r0 < 0 || r0 > r1 || r1 > p.R;
+    }
+    // (a group's entry is formed from its requests' rows: only when these are within cu)
     long long mine = 0;
-    int bad = 0;
-    if (kGroups) {
-#pragma unroll 1
-        for (int r = tid; r < p.R; r += kThreads) bad |= p.cu[r] > p.cu[r + 1];
-        bad |= p.group_start[0] != 0 || p.group_start[p.n_groups] != p.R;
-#pragma unroll 1
-        for (int e = e0; e < e1; ++e) {
-            const int r0 = p.group_start[e], r1 = p.group_start[e + 1];
-            bad |= r0 < 0 || r0 > r1 || r1 > p.R;
-        }
-    } else {
-#pragma unroll 1
-        for (int e = tid; e < p.n_groups; e += kThreads) bad |= p.group_start[e] > p.group_start[e + 1];
-        if (p.n_groups) bad |= p.group_start[0] != 0 || p.group_start[p.n_groups] != p.R;
-#pragma unroll 1
-        for (int e = e0; e < e1; ++e) bad |= p.cu[e] > p.cu[e + 1];
-    }
-    bad |= p.cu[0] != 0 || p.cu[p.R] > p.rows;
-    if (!bad) {
-#pragma unroll 1
-        for (int e = e0; e < e1; ++e) {
-            const Entry x = entry_of<kGroups>(p, e);
-            if (e == e0) first = x;
-            mine += x.cost(p.hkv);
-        }
-    }
-    long long incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        if (lane >= o) incl += up;
-    }
-    if (lane == 31) sh.scan[warp] = incl;
+    if (!kGroups || !bad) mine = cost_of(tid);
+    mine = scanned(mine);
+    if (lane == 31) sh.scan[warp] = mine;
     tc::tc_fence_before();
     bad = __syncthreads_or(bad);
     tc::tc_fence_after();
@@ -392,31 +381,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         if (blockIdx.x == 0 && tid == 0) report(p.dev_status, DSPARK_ERR_DEVICE_INPUT);
         return;
     }
-    long long before = incl - mine, total = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        const long long x = sh.scan[w];
-        if (w < warp) before += x;
-        total += x;
-    }
-    const long long length = piece_length(total, max_ctas);
-    const long long x0 = min(blockIdx.x * length, total), x1 = min(x0 + length, total);
-    if (x0 < x1 && x0 >= before && x0 < before + mine) {
-        long long at = before;
-#pragma unroll 1
-        for (int e = e0; e < e1; ++e) {
-            const Entry x = e == e0 ? first : entry_of<kGroups>(p, e);
-            const long long c = x.cost(p.hkv);
-            if (x0 < at + c) {
-                sh.first_entry = e;
-                sh.first_start = at;
-                sh.first = x;
-                break;
-            }
-            at += c;
-        }
-    }
-    __syncthreads();
     const float sl2 = fmaxf(p.scale * kLog2e, 1e-37f);  // (a masked score, -inf, weighs nothing at a scale of 0 too)
     // Waits for the phase of that parity; false (and the CTA stops) when it does not come in some seconds.  (No
     // function is called: the register split below leaves none for a call's frame.)
@@ -789,15 +753,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         }
     } else if (warp < 12 && maps.box_rows > 0) {
         // ================================================================ loads by TMA
-        // A lane has one box of a block, its first key and 64 of its columns; the four warps take the slots in turn
-        // (a slot takes a warp about 1500 cycles, of pages of 16).  Each waits for every slot to be empty, its own or
-        // not: a warp that skipped a slot's phase could take the one before it for it.
+        // A lane has one box of a block, its first key and 64 of its columns; each of the four warps has slots of its
+        // own (one takes it about 1500 cycles, of pages of 16).  All uses of a slot are one warp's: its wait for the
+        // slot to be empty again is then never for another phase of the same parity.
         const int none = p.pool_pages * p.hkv * p.page;  // past the matrices: zeros
         const int boxes = kBlock / maps.box_rows, box_key = lane % boxes * maps.box_rows, half = lane / boxes;
         const int pages_on = kBlock / p.page, slots_on = kBlock - pages_on * p.page;  // from a block to the next
         const uint32_t dst = half * L::kHalf + box_key * 128;
         Ring ring;
-        uint32_t filled = 0, turn = warp & 3;  // slots until this warp's next
+        uint32_t filled = 0;
         // this lane's box of the next block of keys: its position, page and slot of it, and the page's id
         int pos = 0, page = 0, slot = 0, id = 0;
         const int32_t* table = nullptr;
@@ -853,16 +817,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                     --n_kept;
                     if (c.block() >= c.at->look) bar = &sh.landed[ring.s];
                 }
-                if (filled == kSlots) wait(&sh.empty[ring.s], ring.phase ^ 1);
-                else ++filled;
-                if (turn == 0) {
+                if ((int)(ring.s & 3) == (warp & 3)) {
+                    if (filled == kSlots) wait(&sh.empty[ring.s], ring.phase ^ 1);
                     __syncwarp();  // (what a lane noted of a missing page goes before the arrival)
                     if (lane == 0) tc::mbar_arrive_expect_tx(bar, L::kOperand);
                     __syncwarp();
                     if (half < kD / 64)
                         tc::tma_load_2d(base + (2 + ring.s) * L::kOperand + dst, is_k ? &maps.k : &maps.v, bar, half * 64, row);
                 }
-                turn = (turn - 1) & 3;
+                if (filled < kSlots) ++filled;
                 ring.next();
             }
             if (is_k) {
@@ -1150,14 +1113,33 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
             __syncwarp();
             ++i;
         };
+        // this CTA's piece of the line, and the entry that it begins in: its warp, its thread, itself
+        long long total = 0, at = 0;
+        const long long sums = lane < kThreads / 32 ? sh.scan[lane] : 0, upto = scanned(sums);
+        total = __shfl_sync(0xFFFFFFFFu, upto, 31);
+        const long long length = piece_length(total, max_ctas);
+        const long long x0 = min(blockIdx.x * length, total), x1 = min(x0 + length, total);
+        int e = 0;
+        Entry en{};
+        if (x0 < x1) {
+            const int w = __ffs(__ballot_sync(0xFFFFFFFFu, x0 < upto)) - 1;
+            at = __shfl_sync(0xFFFFFFFFu, upto - sums, w);
+            const long long cost = cost_of(32 * w + lane), end = at + scanned(cost);
+            const int l = __ffs(__ballot_sync(0xFFFFFFFFu, x0 < end)) - 1;
+            at = __shfl_sync(0xFFFFFFFFu, end - cost, l);
+#pragma unroll 1
+            for (e = (32 * w + l) * per;; ++e) {
+                en = entry_of<kGroups>(p, e);
+                if (x0 < at + en.cost(p.hkv)) break;
+                at += en.cost(p.hkv);
+            }
+        }
         Piece x;
         x.g0 = x.spoiled = x.n_q = 0;
         if (x0 < x1) {
-            int e = sh.first_entry;
-            Entry en = sh.first;
-            const int item = (int)divide(x0 - sh.first_start, en.blocks + kItemCost);
+            const int item = (int)divide(x0 - at, en.blocks + kItemCost);
             int h = item / en.tiles, t = item - h * en.tiles;
-            long long start = sh.first_start + (long long)item * (en.blocks + kItemCost);  // the item's first unit
+            long long start = at + (long long)item * (en.blocks + kItemCost);  // the item's first unit
 #pragma unroll 1
             while (start < x1 && !stopped()) {
                 const int tile_row = t * kRows, n_rows = min(en.n * g - tile_row, kRows);
