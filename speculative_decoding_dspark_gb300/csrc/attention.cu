@@ -424,9 +424,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
     };
 
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     }
 
     if (warp < 8) {
@@ -612,6 +612,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                 m0 = top;
             };
             m = m == -INFINITY ? -INFINITY : m * sl2;  // base-2 from here on
+            const size_t lin_step = (size_t)p.rows * g, lin0 = (size_t)w.row0 * g + w.tile_row + sub * kTile;
+            const bool prefix = !kGroups && w.uncut && p.n_groups > 0 && w.begin > 0;
+            float2 shared_ml = make_float2(-INFINITY, 0.0f);
+            if (prefix) {  // (asked for early: it is needed after the copies' sums)
+                if (!prior_done) wait_prior_grid();
+                prior_done = true;
+                shared_ml = shared_plan.whole_ml[(size_t)w.head * lin_step + lin0 + (live ? t_row : 0)];
+            }
             float f1 = 1.0f, f2 = 0.0f, f3 = 0.0f;     // scales of this tile's, the other tile's, the shared part's sums
             if (two) {
                 wait(&sh.merge, n_merge);
@@ -644,14 +652,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
             const bool final = !kGroups && uncut;
             const size_t slot = (size_t)(2 * blockIdx.x + (w.b0 == 0)) * kRows;  // its first row
             // partial sums lie by four columns, then rows, so that a warp's stores are contiguous
-            const size_t lin_step = (size_t)p.rows * g, lin0 = (size_t)w.row0 * g + w.tile_row + sub * kTile;
-            const bool prefix = final && p.n_groups > 0 && w.begin > 0;
             if (prefix) {
-                if (!prior_done) wait_prior_grid();
-                prior_done = true;
-                const float2 ml = shared_plan.whole_ml[(size_t)w.head * lin_step + lin0 + (live ? t_row : 0)];
                 float fa;
-                add(m, l, ml.x, ml.y, fa, f3);
+                add(m, l, shared_ml.x, shared_ml.y, fa, f3);
                 f1 *= fa;
                 f2 *= fa;
             }
@@ -673,8 +676,20 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                 // and rows are written out side by side.
                 float4* const stage = reinterpret_cast<float4*>(base + ((w.n_q + sub) & 1) * L::kOperand);  // [c / 4][128 lanes]
                 if (final) sh.ml[X][t128] = make_float2(f3, __int_as_float(live ? (int)row_of_out(t_row) : 0));
+                // Of the output a thread has four columns of every kApart-th row, kBatch rows at a time.
+                constexpr int kQuads = kD / 8, kApart = kTile / kQuads, kBatch = 32 / kApart;
+                const int my_q = t128 % kQuads, my_r0 = t128 / kQuads;
+                float4 pre[kBatch];  // the shared part's sums of a batch
+                auto fetch = [&](int c0, int r0) {
+                    if (!prefix) return;
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i)
+                        if (r0 + i * kApart < n_rows)
+                            pre[i] = shared_part[(size_t)(c0 / 4 + my_q) * lin_step + lin0 + r0 + i * kApart];
+                };
 #pragma unroll 1
                 for (int c0 = 0; c0 < kD; c0 += kD / 2) {
+                    fetch(c0, my_r0);  // (there by the time the sums are in their places)
 #pragma unroll 1
                     for (int c = 0; c < kD / 2; c += 16) {
                         float o[16], o2[16];
@@ -695,7 +710,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                         }
                     }
                     tile_sync();
-                    constexpr int kQuads = kD / 8;  // of four columns, in this half
                     auto sum_of = [&](int q, int r) {  // over the copies
                         float4 y = stage[q * kTile + (r ^ (q & 15))];
                         if (log_copies) {
@@ -708,17 +722,24 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                         return y;
                     };
                     if (final) {  // a row's columns side by side
-                        const int q = t128 % kQuads;
-#pragma unroll 2
-                        for (int r = t128 / kQuads; r < n_rows; r += kTile / kQuads) {
-                            const float2 f = sh.ml[X][r];
-                            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                            if (prefix) x = shared_part[(size_t)(c0 / 4 + q) * lin_step + lin0 + r];
-                            const float4 y = sum_of(q, r);
-                            const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x + x.x * f.x, y.y + x.y * f.x);
-                            const __nv_bfloat162 hi = __floats2bfloat162_rn(y.z + x.z * f.x, y.w + x.w * f.x);
-                            *reinterpret_cast<uint2*>(p.out + (size_t)__float_as_int(f.y) * kD + c0 + 4 * q) =
-                                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+#pragma unroll 1
+                        for (int r0 = my_r0; r0 < n_rows; r0 += kBatch * kApart) {
+                            if (r0 != my_r0) fetch(c0, r0);
+#pragma unroll
+                            for (int i = 0; i < kBatch; ++i) {
+                                const int r = r0 + i * kApart;
+                                if (r < n_rows) {
+                                    const float2 f = sh.ml[X][r];
+                                    float4 y = sum_of(my_q, r);
+                                    if (prefix) {
+                                        y.x += pre[i].x * f.x; y.y += pre[i].y * f.x;
+                                        y.z += pre[i].z * f.x; y.w += pre[i].w * f.x;
+                                    }
+                                    const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x, y.y), hi = __floats2bfloat162_rn(y.z, y.w);
+                                    *reinterpret_cast<uint2*>(p.out + (size_t)__float_as_int(f.y) * kD + c0 + 4 * my_q) =
+                                        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+                                }
+                            }
                         }
                     } else {  // a column's rows
                         const int r = t_row;
