@@ -140,13 +140,13 @@ def dspark_version() -> int:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())  # of torch.cuda.current_stream()
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _dtype_code(t):
@@ -158,6 +158,9 @@ def _dtype_code(t):
 
 
 def _check(t, name, dtype=None, shape=None, allow_none=False, allow_pinned=False):
+    if (t is not None and t.is_cuda and (dtype is None or t.dtype is dtype) and (shape is None or t.shape == shape)
+            and t.is_contiguous()):
+        return
     if t is None:
         if allow_none:
             return
