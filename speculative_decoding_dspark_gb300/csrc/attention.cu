@@ -57,8 +57,11 @@ constexpr int kLoaders = 128;
 constexpr int kTile = 128;   // rows of a tile
 constexpr int kRows = 256;   // rows of an item
 constexpr int kBlock = 128;  // keys of a block
-constexpr int kItemCost = 4;  // blocks that an item costs besides its own: 1, 2, 4, 8 measured 269, 249, 251, 266 us for 128 ragged requests, 228, 209, 192, 192 behind a prefix
+// Blocks that an item costs besides its own (its queries, its output).  1, 2, 4, 8: 228, 209, 192, 192 us for short
+// ragged requests behind shared prefixes, 269, 249, 251, 266 us for 128 long ones (both before later steps).
+constexpr int kItemCost = 4;
 constexpr int kMaxCtas = 152;            // one per SM
+constexpr int kMaxKeys = INT_MAX - 4 * kBlock;  // (loads look up to two blocks past the last key)
 constexpr float kGrowth = 8.0f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -113,7 +116,7 @@ __device__ __forceinline__ int shared_of(const AttnParams& p, int r) {
 
 __device__ __forceinline__ bool request_ok(const AttnParams& p, int len, int n, int shared) {
     return len >= 0 && shared >= 0 && shared <= len && (long long)len + n <= (long long)p.max_blocks * p.page &&
-           (long long)len + n < (1LL << 31) - kBlock;
+           (long long)len + n <= kMaxKeys;
 }
 
 template <bool kGroups>
@@ -128,7 +131,7 @@ __device__ __forceinline__ Entry entry_of(const AttnParams& p, int e) {
         x.n = p.cu[r1] - x.row0;
         x.len = -1;
         x.end = s;
-        if (s <= 0 || s % p.page || (long long)s > (long long)p.max_blocks * p.page || s >= INT_MAX - kBlock) x.n = 0;
+        if (s <= 0 || s % p.page || (long long)s > (long long)p.max_blocks * p.page || s > kMaxKeys) x.n = 0;
     } else {
         const int lo = p.cu[e], n = p.cu[e + 1] - lo, len = p.kv_len[e];
         const int shared = shared_of(p, e);
@@ -186,9 +189,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
     return y;
 }
-__device__ __forceinline__ void wait_prior_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // Waits until the phase of `parity` completes, at most 2^20 suspensions of up to 20 us.
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
@@ -286,7 +286,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
     const __nv_bfloat16 kNan = __ushort_as_bfloat16(0x7FFF);
 
     const uint32_t loaders = maps.box_rows > 0 ? 1 : kLoaders;  // arrivals that fill a slot
-    launch_dependents();
     // ---- the line of all items' blocks, and this CTA's piece of it
     if (warp == 12) {
         tc::tmem_alloc(&sh.tmem_base, 512);
@@ -314,10 +313,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
             tc::mbar_init(&sh.merge, 4);
             tc::mbar_init(&sh.drain, 1);
             sh.abort_flag = 0;
-            plan.jobs[blockIdx.x].n_rows = 0;
         }
         tc::fence_barrier_init();
     }
+    // (Nothing before this depends on what earlier kernels wrote.  Behind the shared parts' launch the rest does not
+    // either, but for the shared parts themselves.)
+    if (kGroups || p.n_groups == 0) wait_prior_grid();
+    launch_dependents();
+    if (tid == 0) plan.jobs[blockIdx.x].n_rows = 0;
     // every thread has `per` entries
     const int per = (entries + kThreads - 1) / kThreads;
     auto cost_of = [&](int t) {
@@ -355,6 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
     if (bad) {  // nothing can be said of any row
         if (warp == 12) tc::tmem_dealloc(tmem, 512);
         if (kGroups) return;
+        wait_prior_grid();  // (so that whoever waits for this grid waits for the shared parts' too)
         const long long n = (long long)p.rows * p.hq;
 #pragma unroll 1
         for (long long i = (long long)blockIdx.x * kThreads + tid; i < n * kD; i += (long long)gridDim.x * kThreads) p.out[i] = kNan;
@@ -990,9 +994,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
 #pragma unroll 1
                         for (int i = to * kChunks + lane; i < (to + maps.box_rows - 1) / maps.box_rows * maps.box_rows * kChunks; i += 32)
                             *reinterpret_cast<uint4*>(at + chunk_offset(i / kChunks, i % kChunks)) = make_uint4(0, 0, 0, 0);
-                    if (edge)
 #pragma unroll 1
-                    for (int i = from * kChunks + lane; i < to * kChunks; i += 32) {
+                    for (int i = from * kChunks + lane; edge && i < to * kChunks; i += 32) {
                         const int r = i / kChunks;
                         const uint4 q = *reinterpret_cast<const uint4*>(at + chunk_offset(r, i % kChunks));
                         const uint32_t x[4] = {q.x, q.y, q.z, q.w};
@@ -1208,7 +1211,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
     }
     __syncwarp();
     __syncthreads();
-    if (tid == 0 && sh.abort_flag) report(p.dev_status, DSPARK_ERR_TIMEOUT);
+    if (sh.abort_flag) {
+        if (tid == 0) report(p.dev_status, DSPARK_ERR_TIMEOUT);
+        for (const uint64_t t0 = global_ns(); global_ns() - t0 < 1000000;) {}  // (copies in flight land before the CTA ends)
+    }
     if (warp == 12) tc::tmem_dealloc(tmem, 512);
 }
 
@@ -1288,23 +1294,6 @@ Plan plan_at(void* ws, size_t& off, long long items, int d, bool whole) {
     return p;
 }
 
-// A launch that may start while the kernel before it in the stream runs (which
-// it waits for itself).
-template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
-}
-
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -1360,16 +1349,13 @@ cudaError_t launch_d(const AttnParams& p, cudaStream_t stream) {
         shared_plan = plan_at(p.ws, off, items, kD, true);
         if ((err = cudaFuncSetAttribute(attention_kernel<kD, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
             return err;
-        attention_kernel<kD, true><<<ctas, kThreads, smem, stream>>>(p, shared_plan, shared_plan, ctas, p.n_groups, maps);
-        if ((err = cudaGetLastError()) != cudaSuccess) return err;
+        if ((err = launch_after(attention_kernel<kD, true>, dim3(ctas), kThreads, smem, stream, p, shared_plan, shared_plan, ctas, p.n_groups, maps)) != cudaSuccess)
+            return err;
         if ((err = launch_after(join_kernel<kD, true>, join_grid, kRows, 0, stream, p, shared_plan, shared_plan)) != cudaSuccess)
             return err;
-        if ((err = launch_after(attention_kernel<kD, false>, dim3(ctas), kThreads, smem, stream, p, plan, shared_plan, ctas, p.R, maps)) != cudaSuccess)
-            return err;
-    } else {
-        attention_kernel<kD, false><<<ctas, kThreads, smem, stream>>>(p, plan, plan, ctas, p.R, maps);
-        if ((err = cudaGetLastError()) != cudaSuccess) return err;
     }
+    if ((err = launch_after(attention_kernel<kD, false>, dim3(ctas), kThreads, smem, stream, p, plan, shared_plan, ctas, p.R, maps)) != cudaSuccess)
+        return err;
     return launch_after(join_kernel<kD, false>, join_grid, kRows, 0, stream, p, plan, shared_plan);
 }
 

@@ -191,6 +191,12 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     return y;
 }
 
+// Waits until the kernels before this one in the stream are done, their writes
+// visible; lets the next one start (it waits likewise).  For kernels launched by
+// launch_after.
+__device__ __forceinline__ void wait_prior_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Global-time based bound for device spin waits (nanoseconds).
 __device__ __forceinline__ uint64_t global_ns() {
     uint64_t t;
