@@ -578,12 +578,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                 }
             }
             // ---- the triple of this tile's rows
+            // The other tile may have a part of the same rows: the one with the last step waits the least for it, and
+            // the next item begins with the other.
+            const bool two = !at.pair && steps > 1, last = at.pair || ((steps - 1 - u0) & 1) == 0;
+            // (without copies the query buffer is not needed below)
+            if (last && !log_copies && t128 == 0) tc::mbar_arrive(&sh.q_empty[(w.n_q + sub) & 1]);
             wait(&sh.o_done[X], n_done);
             ++n_done;
             tc::tc_fence_after();
             __syncwarp();
-            const bool two = !at.pair && steps > 1;  // the other tile has a part of the same rows
-            if (two && u0 == 1) {
+            if (two && !last) {
                 sh.ml[X][t128] = make_float2(m, l);
                 tc::tc_fence_before();
                 arrive(&sh.merge);
@@ -659,38 +663,72 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                 const int i = (w.tile_row + sub * kTile + r) / g;
                 return (size_t)(w.row0 + i) * p.hq + w.head * g + (w.tile_row + sub * kTile + r - i * g);
             };
-            {
-                // The sums go through the tile's query buffer, half of the columns at a time: there the copies' meet,
-                // and rows are written out side by side.
-                float4* const stage = reinterpret_cast<float4*>(base + ((w.n_q + sub) & 1) * L::kOperand);  // [c / 4][128 lanes]
-                if (final) sh.ml[X][t128] = make_float2(f3, __int_as_float(live ? (int)row_of_out(t_row) : 0));
-                // Of the output a thread has four columns of every kApart-th row, kBatch rows at a time.
-                constexpr int kQuads = kD / 8, kApart = kTile / kQuads, kBatch = 32 / kApart;
-                const int my_q = t128 % kQuads, my_r0 = t128 / kQuads;
-                float4 pre[kBatch];  // the shared part's sums of a batch
-                auto fetch = [&](int c0, int r0) {
-                    if (!prefix) return;
+            auto sums = [&](int c, float (&o)[16]) {  // 16 columns of this lane's row, of both tiles
+                float o2[16];
+                tc::tmem_ld_32x32b_x16<0>(tO + c, o);
+                if (two) tc::tmem_ld_32x32b_x16<0>(tO2 + c, o2);
+                tc::tmem_ld_wait();
+                if (c + 16 == kD) {  // the next item's products may have the place
+                    tc::tc_fence_before();
+                    arrive(&sh.o_free[X]);
+                    if (two) arrive(&sh.o_free[X ^ 1]);
+                }
 #pragma unroll
-                    for (int i = 0; i < kBatch; ++i)
-                        if (r0 + i * kApart < n_rows)
-                            pre[i] = shared_part[(size_t)(c0 / 4 + my_q) * lin_step + lin0 + r0 + i * kApart];
-                };
+                for (int j = 0; j < 16; ++j) o[j] = two ? o[j] * f1 + o2[j] * f2 : o[j] * f1;
+            };
+            auto pack = [](float4 y) {
+                const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x, y.y), hi = __floats2bfloat162_rn(y.z, y.w);
+                return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+            };
+            if (!log_copies) {
+                // A row to a lane: a column of a warp's sums lies in one piece, and of the output each lane writes whole
+                // sectors.
+                __nv_bfloat16* const out = p.out + (final && live ? row_of_out(t_row) : 0) * kD;
+#pragma unroll 1
+                for (int c = 0; c < kD; c += 16) {
+                    float o[16];
+                    float4 next[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        next[j] = !prefix || !live ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : shared_part[(size_t)(c / 4 + j) * lin_step + lin0 + t_row];
+                    sums(c, o);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        o[4 * j] += next[j].x * f3; o[4 * j + 1] += next[j].y * f3;
+                        o[4 * j + 2] += next[j].z * f3; o[4 * j + 3] += next[j].w * f3;
+                    }
+                    if (live) {
+                        uint2 b[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float4 y = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                            b[j] = pack(y);
+                            if (!final) to[(size_t)(c / 4 + j) * to_step + to0 + t_row] = y;
+                        }
+                        if (final) {
+                            reinterpret_cast<uint4*>(out + c)[0] = make_uint4(b[0].x, b[0].y, b[1].x, b[1].y);
+                            reinterpret_cast<uint4*>(out + c)[1] = make_uint4(b[2].x, b[2].y, b[3].x, b[3].y);
+                        }
+                    }
+                }
+            } else {
+                // The copies' sums meet in the item's query buffer, half of the columns at a time.
+                float4* const stage = reinterpret_cast<float4*>(base + (w.n_q & 1) * L::kOperand);  // [c / 4][128 lanes]
+                if (final) sh.ml[X][t128] = make_float2(f3, __int_as_float(live ? (int)row_of_out(t_row) : 0));
+                constexpr int kQuads = kD / 8, kApart = kTile / kQuads, kBatch = 32 / kApart;
+                const int my_q = opaque(t128) % kQuads, my_r0 = opaque(t128) / kQuads;  // of the output: four columns of every kApart-th row
+                float4 pre[kBatch];                                     // the shared part's sums of them
 #pragma unroll 1
                 for (int c0 = 0; c0 < kD; c0 += kD / 2) {
-                    fetch(c0, my_r0);  // (there by the time the sums are in their places)
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i)  // (there by the time the sums are in their places)
+                        pre[i] = !prefix || my_r0 + i * kApart >= n_rows
+                                     ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                                     : shared_part[(size_t)(c0 / 4 + my_q) * lin_step + lin0 + my_r0 + i * kApart];
 #pragma unroll 1
                     for (int c = 0; c < kD / 2; c += 16) {
-                        float o[16], o2[16];
-                        tc::tmem_ld_32x32b_x16<0>(tO + c0 + c, o);
-                        if (two) tc::tmem_ld_32x32b_x16<0>(tO2 + c0 + c, o2);
-                        tc::tmem_ld_wait();
-                        if (c0 + c + 16 == kD) {  // the next item's products may have the place
-                            tc::tc_fence_before();
-                            arrive(&sh.o_free[X]);
-                            if (two) arrive(&sh.o_free[X ^ 1]);
-                        }
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) o[j] = two ? o[j] * f1 + o2[j] * f2 : o[j] * f1;
+                        float o[16];
+                        sums(c0 + c, o);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const int q = c / 4 + j;
@@ -700,64 +738,49 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                     tile_sync();
                     auto sum_of = [&](int q, int r) {  // over the copies
                         float4 y = stage[q * kTile + (r ^ (q & 15))];
-                        if (log_copies) {
 #pragma unroll
-                            for (int c = 32; c < kTile; c += 32) {
-                                const float4 v = stage[q * kTile + ((c + r) ^ (q & 15))];
-                                y.x += v.x; y.y += v.y; y.z += v.z; y.w += v.w;
-                            }
+                        for (int c = 32; c < kTile; c += 32) {
+                            const float4 v = stage[q * kTile + ((c + r) ^ (q & 15))];
+                            y.x += v.x; y.y += v.y; y.z += v.z; y.w += v.w;
                         }
                         return y;
                     };
                     if (final) {  // a row's columns side by side
-#pragma unroll 1
-                        for (int r0 = my_r0; r0 < n_rows; r0 += kBatch * kApart) {
-                            if (r0 != my_r0) fetch(c0, r0);
 #pragma unroll
-                            for (int i = 0; i < kBatch; ++i) {
-                                const int r = r0 + i * kApart;
-                                if (r < n_rows) {
-                                    const float2 f = sh.ml[X][r];
-                                    float4 y = sum_of(my_q, r);
-                                    if (prefix) {
-                                        y.x += pre[i].x * f.x; y.y += pre[i].y * f.x;
-                                        y.z += pre[i].z * f.x; y.w += pre[i].w * f.x;
-                                    }
-                                    const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x, y.y), hi = __floats2bfloat162_rn(y.z, y.w);
-                                    *reinterpret_cast<uint2*>(p.out + (size_t)__float_as_int(f.y) * kD + c0 + 4 * my_q) =
-                                        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-                                }
+                        for (int i = 0; i < kBatch; ++i) {
+                            const int r = my_r0 + i * kApart;
+                            if (r < n_rows) {
+                                const float2 f = sh.ml[X][r];
+                                float4 y = sum_of(my_q, r);
+                                y.x += pre[i].x * f.x; y.y += pre[i].y * f.x;
+                                y.z += pre[i].z * f.x; y.w += pre[i].w * f.x;
+                                *reinterpret_cast<uint2*>(p.out + (size_t)__float_as_int(f.y) * kD + c0 + 4 * my_q) = pack(y);
                             }
                         }
                     } else {  // a column's rows
-                        const int r = t_row;
 #pragma unroll 1
-                        for (int q = t128 >> log_rows; q < kQuads && live; q += 1 << log_copies) {
-                            const float4 y = sum_of(q, r);
-                            to[(size_t)(c0 / 4 + q) * to_step + to0 + r] = y;
-                        }
+                        for (int q = t128 >> log_rows; q < kQuads && live; q += 1 << log_copies)
+                            to[(size_t)(c0 / 4 + q) * to_step + to0 + t_row] = sum_of(q, t_row);
                     }
                     tile_sync();
                 }
+                if (t128 == 0) tc::mbar_arrive(&sh.q_empty[w.n_q & 1]);
             }
             if (live && t128 == t_row) {
                 if (!final) (uncut ? plan.whole_ml + (size_t)w.head * lin_step : plan.part_ml + slot)[to0 + t_row] = make_float2(m, l);
                 else if (p.lse) p.lse[row_of_out(t_row)] = (m + log2f(l)) * kLn2;
             }
-            if (t128 == 0) {
-                tc::mbar_arrive(&sh.q_empty[(w.n_q + sub) & 1]);
-                if (!uncut && w.b0 == 0 && sub == 0) {
-                    Job j;
-                    j.n_rows = w.n_rows;
-                    j.first = blockIdx.x;
-                    j.last = w.last_cta;
-                    j.row0 = w.row0;
-                    j.tile_row = w.tile_row;
-                    j.head = w.head;
-                    j.merge_prefix = !kGroups && p.n_groups > 0 && w.begin > 0;
-                    j.pad = 0;
-                    plan.jobs[blockIdx.x] = j;
-                }
+            if (t128 == 0 && !uncut && w.b0 == 0 && sub == 0) {
+                Job j;
+                j.n_rows = w.n_rows;
+                j.first = blockIdx.x;
+                j.last = w.last_cta;
+                j.row0 = w.row0;
+                j.tile_row = w.tile_row;
+                j.head = w.head;
+                j.merge_prefix = !kGroups && p.n_groups > 0 && w.begin > 0;
+                j.pad = 0;
+                plan.jobs[blockIdx.x] = j;
             }
         }
     } else if (warp < 12 && maps.box_rows > 0) {
@@ -1045,6 +1068,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         Cursor k, v;
         bool more = open(k);
         open(v);
+        int owed = 0;  // scores that may be formed
 #pragma unroll 1
         for (int i = opaque(-2);; ++i) {  // values of a step, then scores of the step after the next
             if (i >= 0) {
@@ -1077,33 +1101,38 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                 }
             }
             if (v.steps == 0 || stopped()) break;
-            if (!more) continue;
-            const int X = gk & 1, sub = k.u & k.pair;
-            const uint32_t q = n_q + sub;
-            if (k.u <= k.pair) wait(&sh.q_full[q & 1], q >> 1);
-            if (sub == 0) {
-                k_slot = ring.s;
-                wait(&sh.full[k_slot], ring.phase);
-                ring.next();
-            }
-            if (copied || k.u <= k.pair) tc::fence_proxy_async_smem();
-            tc::tc_fence_after();
-            __syncwarp();
-            const uint64_t qd = tc::smem_desc_sw128(sQ + (q & 1) * L::kOperand);
-            const uint64_t kd = tc::smem_desc_sw128(sRing + k_slot * L::kOperand);
+            // (a pair's last product goes before the next item's scores, whose queries may wait for the pair's first half)
+            ++owed;
+            if (k.u == 0 && (v.u & v.pair)) continue;
+#pragma unroll 1
+            for (; owed > 0 && more; --owed) {
+                const int X = gk & 1, sub = k.u & k.pair;
+                const uint32_t q = n_q + sub;
+                if (k.u <= k.pair) wait(&sh.q_full[q & 1], q >> 1);
+                if (sub == 0) {
+                    k_slot = ring.s;
+                    wait(&sh.full[k_slot], ring.phase);
+                    ring.next();
+                }
+                if (copied || k.u <= k.pair) tc::fence_proxy_async_smem();
+                tc::tc_fence_after();
+                __syncwarp();
+                const uint64_t qd = tc::smem_desc_sw128(sQ + (q & 1) * L::kOperand);
+                const uint64_t kd = tc::smem_desc_sw128(sRing + k_slot * L::kOperand);
 #pragma unroll
-            for (int j = 0; j < kD / 16; ++j) {
-                const uint64_t at = (uint64_t)((j >> 2) * (L::kHalf >> 4) + (j & 3) * 2);
-                tc::umma_bf16_elect(tmem + X * kBlock, qd + at, kd + at, idesc_s, j != 0);
-            }
-            tc::umma_commit_elect(&sh.s_full[X]);
-            if (sub == k.pair) tc::umma_commit_elect(&sh.empty[k_slot]);
-            if (k.u + k.pair + 1 >= k.steps) tc::umma_commit_elect(&sh.q_empty[q & 1]);
-            ++gk;
-            if (++k.u == k.steps) {
-                n_q += 1 + k.pair;
-                ++k.i;
-                more = open(k);
+                for (int j = 0; j < kD / 16; ++j) {
+                    const uint64_t at = (uint64_t)((j >> 2) * (L::kHalf >> 4) + (j & 3) * 2);
+                    tc::umma_bf16_elect(tmem + X * kBlock, qd + at, kd + at, idesc_s, j != 0);
+                }
+                tc::umma_commit_elect(&sh.s_full[X]);
+                if (sub == k.pair) tc::umma_commit_elect(&sh.empty[k_slot]);
+                if (k.u + k.pair + 1 >= k.steps) tc::umma_commit_elect(&sh.q_empty[q & 1]);
+                ++gk;
+                if (++k.u == k.steps) {
+                    n_q += 1 + k.pair;
+                    ++k.i;
+                    more = open(k);
+                }
             }
         }
         __syncwarp();
