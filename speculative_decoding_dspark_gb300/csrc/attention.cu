@@ -351,6 +351,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
     if (!kGroups || !bad) mine = cost_of(tid);
     mine = scanned(mine);
     if (lane == 31) sh.scan[warp] = mine;
+    long long* const scans = reinterpret_cast<long long*>(base + 2 * L::kOperand);  // each thread's, over its warp (in the ring)
+    scans[tid] = mine;
+    tc::fence_proxy_async_smem();
     tc::tc_fence_before();
     bad = __syncthreads_or(bad);
     tc::tc_fence_after();
@@ -1150,72 +1153,60 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
             __syncwarp();
             ++i;
         };
-        // this CTA's piece of the line, and the entry that it begins in: its warp, its thread, itself
-        long long total = 0, at = 0;
+        // this CTA's piece of the line, and the thread whose entries it begins in
         const long long sums = lane < kThreads / 32 ? sh.scan[lane] : 0, upto = scanned(sums);
-        total = __shfl_sync(0xFFFFFFFFu, upto, 31);
-        const long long length = piece_length(total, max_ctas);
+        const long long total = __shfl_sync(0xFFFFFFFFu, upto, 31), length = piece_length(total, max_ctas);
         const long long x0 = min(blockIdx.x * length, total), x1 = min(x0 + length, total);
-        int e = 0;
-        Entry en{};
-        if (x0 < x1) {
-            const int w = __ffs(__ballot_sync(0xFFFFFFFFu, x0 < upto)) - 1;
-            at = __shfl_sync(0xFFFFFFFFu, upto - sums, w);
-            const long long cost = cost_of(32 * w + lane), end = at + scanned(cost);
-            const int l = __ffs(__ballot_sync(0xFFFFFFFFu, x0 < end)) - 1;
-            at = __shfl_sync(0xFFFFFFFFu, end - cost, l);
-#pragma unroll 1
-            for (e = (32 * w + l) * per;; ++e) {
-                en = entry_of<kGroups>(p, e);
-                if (x0 < at + en.cost(p.hkv)) break;
-                at += en.cost(p.hkv);
-            }
-        }
         Piece x;
         x.g0 = x.spoiled = x.n_q = 0;
         if (x0 < x1) {
-            const int item = (int)divide(x0 - at, en.blocks + kItemCost);
-            int h = item / en.tiles, t = item - h * en.tiles;
-            long long start = at + (long long)item * (en.blocks + kItemCost);  // the item's first unit
+            const int w = __ffs(__ballot_sync(0xFFFFFFFFu, x0 < upto)) - 1;
+            const long long before = __shfl_sync(0xFFFFFFFFu, upto - sums, w), end = before + scans[32 * w + lane];
+            const int l = __ffs(__ballot_sync(0xFFFFFFFFu, x0 < end)) - 1;
+            long long start = l ? __shfl_sync(0xFFFFFFFFu, end, max(l - 1, 0)) : before;  // the item's first unit
+            __syncwarp();
 #pragma unroll 1
-            while (start < x1 && !stopped()) {
-                const int tile_row = t * kRows, n_rows = min(en.n * g - tile_row, kRows);
-                const int high = en.limit((tile_row + n_rows - 1) / g), n_blocks = (high - en.begin + kBlock - 1) / kBlock;
-                const long long first = start + kItemCost;
-                const int b0 = x0 > first ? (int)(x0 - first) : 0;
-                const int b1 = x1 - first < n_blocks ? (int)max(x1 - first, 0LL) : n_blocks;
-                if (b0 < b1) {
-                    x.b0 = b0;
-                    x.uncut = b0 == 0 && b1 == n_blocks;
-                    x.row0 = en.row0;
-                    x.tile_row = tile_row;
-                    x.n_rows = n_rows;
-                    x.head = h;
-                    x.begin = en.begin;
-                    x.end = en.end;
-                    x.len = en.len;
-                    x.table = en.table;
-                    x.low = en.limit(t ? tile_row / g : 0);
-                    x.high = high;
-                    x.edge = x.low < high ? max((x.low - en.begin) / kBlock - b0, 0) : INT_MAX;
-                    x.look = maps.box_rows > 0 && (high - en.begin) % kBlock ? min(x.edge, n_blocks - 1 - b0) : x.edge;
-                    x.pair = n_rows > kTile;
-                    x.steps = (b1 - b0) << x.pair;
-                    x.log_copies = n_rows <= 32 ? 2 : 0;
-                    x.last_cta = 0;
-                    if (b0 == 0 && !x.uncut)  // (the last CTA with a piece: every one has `length` units)
-                        x.last_cta = blockIdx.x + 1 + (int)divide(first + n_blocks - 1 - x1, length);
-                    post(x);
-                    x.g0 += x.steps;
-                    x.n_q += 1 + x.pair;
-                }
-                start += en.blocks + kItemCost;
-                if (++t == en.tiles) {
-                    t = 0;
-                    if (++h == p.hkv) {
-                        h = 0;
-                        if (start < x1)
-                            do en = entry_of<kGroups>(p, ++e); while (en.tiles == 0);
+            for (int e = (32 * w + l) * per; start < x1 && e < entries && !stopped(); ++e) {
+                const Entry en = entry_of<kGroups>(p, e);
+                const int units = en.blocks + kItemCost;
+                const int items = en.tiles * p.hkv, skip = (int)min(divide(max(x0 - start, 0LL), units), (long long)items);
+                start += (long long)skip * units;
+                int h = skip / max(en.tiles, 1), t = skip - h * en.tiles;
+#pragma unroll 1
+                for (int item = skip; item < items && start < x1; ++item, start += units) {
+                    const int tile_row = t * kRows, n_rows = min(en.n * g - tile_row, kRows);
+                    const int high = en.limit((tile_row + n_rows - 1) / g), n_blocks = (high - en.begin + kBlock - 1) / kBlock;
+                    const long long first = start + kItemCost;
+                    const int b0 = x0 > first ? (int)(x0 - first) : 0;
+                    const int b1 = x1 - first < n_blocks ? (int)max(x1 - first, 0LL) : n_blocks;
+                    if (b0 < b1) {
+                        x.b0 = b0;
+                        x.uncut = b0 == 0 && b1 == n_blocks;
+                        x.row0 = en.row0;
+                        x.tile_row = tile_row;
+                        x.n_rows = n_rows;
+                        x.head = h;
+                        x.begin = en.begin;
+                        x.end = en.end;
+                        x.len = en.len;
+                        x.table = en.table;
+                        x.low = en.limit(t ? tile_row / g : 0);
+                        x.high = high;
+                        x.edge = x.low < high ? max((x.low - en.begin) / kBlock - b0, 0) : INT_MAX;
+                        x.look = maps.box_rows > 0 && (high - en.begin) % kBlock ? min(x.edge, n_blocks - 1 - b0) : x.edge;
+                        x.pair = n_rows > kTile;
+                        x.steps = (b1 - b0) << x.pair;
+                        x.log_copies = n_rows <= 32 ? 2 : 0;
+                        x.last_cta = 0;
+                        if (b0 == 0 && !x.uncut)  // (the last CTA with a piece: every one has `length` units)
+                            x.last_cta = blockIdx.x + 1 + (int)divide(first + n_blocks - 1 - x1, length);
+                        post(x);
+                        x.g0 += x.steps;
+                        x.n_q += 1 + x.pair;
+                    }
+                    if (++t == en.tiles) {
+                        t = 0;
+                        ++h;
                     }
                 }
             }
