@@ -29,21 +29,37 @@
 // at most, and l adds the weights before it.
 //
 // One CTA per SM, sixteen warps: 0-3 and 4-7 form the exponentials of the two
-// tiles, 8-11 load keys and values, 15 queries, 12 issues the products, 13 walks along the items, 14
-// looks at blocks of values that not every row sees whole.  Keys and values come
+// tiles and write the sums out, 8-11 load keys and values, 15 queries, 12 issues
+// the products, 13 finds the CTA's pieces of items and posts them to the others,
+// 14 looks at blocks of values that not every row sees whole.  Keys and values come
 // through a ring of 160 KB, queries through two buffers, so that the next item's
 // first product does not wait for the last one's output.  Pages of a multiple of
 // 8 slots come by TMA, each lane of a loading warp having a box of up to 128 rows
 // by 64 elements inside one page.  Other pages may end anywhere in a block: their rows
 // are gathered by 16-byte copies (a row to a lane, the queries' too), which have about
-// 64 KB in flight per SM where TMA has the whole ring (949 MB of keys and values:
-// 200 us).  Four rows to a TMA gather would move 6.4 bytes a cycle (500 us).
+// 64 KB in flight per SM where TMA has the whole ring.  949 MB of keys and values
+// (2 requests of 115000 keys): 155 us by TMA, 91 % of the copy rate, 200 us gathered;
+// four rows to a TMA gather moved 6.4 bytes a cycle (500 us).
 //
-// Splitting: the blocks of all items form one line, which is cut into equal
-// pieces, one per CTA (each item costs a block more, for its queries and
+// Up to 32 rows (a few drafted tokens of one key head) lie in the tile four times
+// and each copy takes a quarter of a block's keys: all four warps form exponentials
+// then, 720 cycles for a block instead of 1350.
+//
+// Splitting: the steps of all items form one line, which is cut into equal
+// pieces, one per CTA (each item costs some steps more, for its queries and
 // output).  An item that is cut leaves its triples in the workspace and a second
 // kernel joins them in their order.  The cut depends on the lengths, which only
 // the device knows: every CTA scans them itself.
+//
+// What bounds it: bytes, where few rows read many keys (128 requests of up to 5000,
+// 1296 MB: 206 us, 93 % of the copy rate).  Many rows over the same keys: the way of a tile
+// from its scores to its next ones, 1350 cycles of exponentials and 1950 of products
+// and their hand-over, in which the other tile's go by too: 1024 of 1665 cycles of a
+// step the tensor cores are at work (128 queries by 8192 shared keys: 80 us).  Short
+// items: 9000 cycles from the last product to the output and the next item's first
+// weights.  Small calls: 15000 cycles until the first product, most of them code
+// that comes into the instruction cache while every warp waits for it (kept at 100 KB;
+// at 180 KB a third of the issue slots waited throughout), and the second launch.
 #include <type_traits>
 
 #include "kernels.cuh"
@@ -57,8 +73,8 @@ constexpr int kLoaders = 128;
 constexpr int kTile = 128;   // rows of a tile
 constexpr int kRows = 256;   // rows of an item
 constexpr int kBlock = 128;  // keys of a block
-// Blocks that an item costs besides its own (its queries, its output).  1, 2, 4, 8: 228, 209, 192, 192 us for short
-// ragged requests behind shared prefixes, 269, 249, 251, 266 us for 128 long ones (both before later steps).
+// Steps that an item costs besides its own.  3, 4, 5, 6: 169, 162, 165, 162 us for short ragged requests behind a
+// shared prefix of 8192, 38, 34, 39, 37 us behind four of 0 to 6400, 209, 208, 209, 210 us for 128 long ones.
 constexpr int kItemCost = 4;
 constexpr int kMaxCtas = 152;            // one per SM
 constexpr int kMaxKeys = INT_MAX - 4 * kBlock;  // (loads look up to two blocks past the last key)
@@ -92,8 +108,9 @@ struct Entry {     // a request's own keys, or a group's shared ones
     int len;       // row i sees keys below len + i + 1 (-1: all rows see the same keys)
     int table;     // the block table's row
     int tiles, blocks;
-    __device__ long long items(int hkv) const { return (long long)tiles * hkv; }
-    __device__ long long cost(int hkv) const { return items(hkv) * (blocks + kItemCost); }
+    int log_steps; // a block takes 2^log_steps steps: of more than kTile rows it serves two tiles
+    __device__ int units() const { return (blocks << log_steps) + kItemCost; }  // of an item: its steps, and what else it costs
+    __device__ long long cost(int hkv) const { return (long long)tiles * hkv * units(); }
     // past the last key seen by row i of the entry
     __device__ int limit(int i) const { return len < 0 ? end : len + i + 1; }
 };
@@ -142,6 +159,7 @@ __device__ __forceinline__ Entry entry_of(const AttnParams& p, int e) {
         x.len = p.full_block ? -1 : len;
         x.end = len + n;
     }
+    x.log_steps = (long long)x.n * (p.hq / p.hkv) > kTile;
     if (x.n <= 0) {
         x.n = x.tiles = x.blocks = 0;
     } else {
@@ -156,8 +174,9 @@ __device__ __forceinline__ long long divide(long long a, long long b) {
     return (a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
 }
 
-// Units of the line to a CTA.
-__device__ __forceinline__ long long piece_length(long long total, int ctas) { return divide(total + ctas - 1, ctas); }
+// Units of the line to a CTA (two at least, so that a block begins in each piece of an item; at 3, 4, 6 a request
+// of 777 keys takes 15.9, 16.7, 17.7 us, at 2 15.2).
+__device__ __forceinline__ long long piece_length(long long total, int ctas) { return max(divide(total + ctas - 1, ctas), 2LL); }
 
 // What a CTA does of one item: blocks [b0, b1) of it.
 struct Piece {
@@ -210,7 +229,7 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity) {
 
 // The compiler is to know nothing of x: loops whose first rounds leave out a part
 // would else be written out for each of them, and all the warps' code has to stay
-// in the instruction cache (at 180 KB a third of the issue slots waited for it).
+// in the instruction cache.
 __device__ __forceinline__ int opaque(int x) {
     asm volatile("" : "+r"(x));
     return x;
@@ -1168,7 +1187,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
 #pragma unroll 1
             for (int e = (32 * w + l) * per; start < x1 && e < entries && !stopped(); ++e) {
                 const Entry en = entry_of<kGroups>(p, e);
-                const int units = en.blocks + kItemCost;
+                const int units = en.units(), log_steps = en.log_steps, round = (1 << log_steps) - 1;
                 const int items = en.tiles * p.hkv, skip = (int)min(divide(max(x0 - start, 0LL), units), (long long)items);
                 start += (long long)skip * units;
                 int h = skip / max(en.tiles, 1), t = skip - h * en.tiles;
@@ -1177,8 +1196,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                     const int tile_row = t * kRows, n_rows = min(en.n * g - tile_row, kRows);
                     const int high = en.limit((tile_row + n_rows - 1) / g), n_blocks = (high - en.begin + kBlock - 1) / kBlock;
                     const long long first = start + kItemCost;
-                    const int b0 = x0 > first ? (int)(x0 - first) : 0;
-                    const int b1 = x1 - first < n_blocks ? (int)max(x1 - first, 0LL) : n_blocks;
+                    // block b begins at unit first + (b << log_steps)
+                    const int b0 = x0 > first ? (int)((x0 - first + round) >> log_steps) : 0;
+                    const int b1 = (int)min(max(x1 - first + round, 0LL) >> log_steps, (long long)n_blocks);
                     if (b0 < b1) {
                         x.b0 = b0;
                         x.uncut = b0 == 0 && b1 == n_blocks;
@@ -1199,7 +1219,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                         x.log_copies = n_rows <= 32 ? 2 : 0;
                         x.last_cta = 0;
                         if (b0 == 0 && !x.uncut)  // (the last CTA with a piece: every one has `length` units)
-                            x.last_cta = blockIdx.x + 1 + (int)divide(first + n_blocks - 1 - x1, length);
+                            x.last_cta = blockIdx.x + 1 + (int)divide(first + ((n_blocks - 1) << log_steps) - x1, length);
                         post(x);
                         x.g0 += x.steps;
                         x.n_q += 1 + x.pair;
