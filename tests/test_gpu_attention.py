@@ -166,6 +166,34 @@ def test_kv_append_bad_pages_and_lengths(B):
     assert torch.equal(gk, kc) and torch.equal(gv, vc)
 
 
+def test_heads_on_another_stream_and_in_a_graph(B):
+    n, kv_len, page, hq, hkv, d = [3, 5], [20, 0], 16, 4, 2, 128
+    cu, table, kc, vc = append_case(3, n, kv_len, page, hkv, d, BF16)
+    qkv, w, f = normal(4, (8, hq + 2 * hkv, d), BF16), normal(5, (d,), BF16), freqs(d)
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+    lens, status = i32(kv_len), i32([0])
+    args = [i32(cu), lens, i32(table)]
+
+    def run(stream=None):
+        c = [kc.clone(), vc.clone(), torch.zeros(8, hq, d, dtype=BF16, device="cuda")]
+        torch.cuda.synchronize()
+        B.dspark_kv_append(q, k, v, w, w, 1e-6, f, *args, *c, dev_status=status, stream=stream)
+        torch.cuda.synchronize()
+        return c
+
+    want = run()
+    assert all(torch.equal(a, b) for a, b in zip(want, run(torch.cuda.Stream())))
+    c = [kc.clone(), vc.clone(), torch.zeros_like(want[2])]
+    lens.zero_()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        B.dspark_kv_append(q, k, v, w, w, 1e-6, f, *args, *c, dev_status=status)
+    lens.copy_(i32(kv_len))
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, c)) and int(status.item()) == 0
+
+
 # --------------------------------------------------------------------------------------- attention
 def attention_case(seed, n, kv_len, page, hq, hkv, d, shared=0, peak=3.0):
     rng = np.random.default_rng(seed)
@@ -239,6 +267,60 @@ def test_attention_long(B, d, hq, hkv):
     check_attention(B, 5, [3, 1], [20011, 9000], 16, hq, hkv, d)
 
 
+@pytest.mark.parametrize("full", [False, True])
+@pytest.mark.parametrize("page,hq,hkv,d", [(8, 8, 2, 128), (24, 16, 1, 64), (40, 4, 4, 128), (48, 16, 2, 64), (1000, 8, 1, 128)])
+def test_attention_boxes_that_overrun(B, page, hq, hkv, d, full):
+    """Pages of several boxes, whose last one holds slots past the last key (not a number, as all unused ones)."""
+    check_attention(B, 31, [1, 2, 9, 17, 3, 0, 1], [0, 6, 119, 230, 381, 9, 1000], page, hq, hkv, d, full)
+
+
+@pytest.mark.parametrize("full", [False, True])
+@pytest.mark.parametrize("seed,requests,rows,keys,page,hq,hkv,d", [
+    (1, 60, 9, 700, 16, 8, 2, 64), (2, 40, 40, 500, 12, 16, 2, 64), (3, 25, 20, 1500, 32, 32, 2, 128),
+    (4, 90, 3, 300, 5, 4, 4, 128), (5, 12, 70, 2000, 64, 4, 1, 128),
+])
+def test_ragged_batches(B, seed, requests, rows, keys, page, hq, hkv, d, full):
+    """Items of one and two tiles after another, cut anywhere."""
+    rng = np.random.default_rng(seed)
+    n = [int(x) for x in rng.integers(0, rows + 1, requests)]
+    kv_len = [int(x) for x in rng.integers(0, keys, requests)]
+    check_attention(B, seed, n, kv_len, page, hq, hkv, d, full)
+
+
+def test_more_requests_than_threads(B):
+    rng = np.random.default_rng(7)
+    n, kv_len = [int(x) for x in rng.integers(0, 3, 1300)], [int(x) for x in rng.integers(0, 40, 1300)]
+    check_attention(B, 7, n, kv_len, 16, 2, 1, 64)
+
+
+def test_more_groups_than_threads(B):
+    """Every request a group of its own, some of them without a shared part."""
+    rng = np.random.default_rng(8)
+    R = 700
+    n = [int(x) for x in rng.integers(0, 3, R)]
+    shared = [16 * int(x) for x in rng.integers(0, 4, R)]
+    kv_len = [shared[r] + int(rng.integers(0, 40)) for r in range(R)]
+    check_attention(B, 9, n, kv_len, 16, 4, 2, 64, groups=(list(range(R + 1)), shared))
+
+
+@pytest.mark.parametrize("page", [16, 20])
+@pytest.mark.parametrize("d", [64, 128])
+def test_two_tiles_over_a_long_history(B, page, d):
+    """320 rows to a key head, whose two items are cut into dozens of pieces."""
+    check_attention(B, 13, [20], [30011], page, 16, 1, d)
+
+
+@pytest.mark.parametrize("scale", [0.0, 1e-4, 1.0])
+def test_scales(B, scale):
+    n, kv_len, page, hq, hkv, d = [3, 5], [400, 77], 16, 8, 2, 128
+    q, kc, vc, table, cu = attention_case(17, n, kv_len, page, hq, hkv, d)
+    out, z, status = attend(B, q, kc, vc, table, kv_len, cu, scale=scale)
+    assert status == 0
+    ref, lse, tol, ztol = A.attention(q, kc, vc, table, kv_len, cu, float(np.float32(scale)), False)
+    close(out, ref, tol, "out")
+    close(z, lse, ztol, "lse")
+
+
 @pytest.mark.parametrize("peak", [0.0, 0.05, 40.0])
 def test_attention_flat_and_peaked(B, peak):
     """Equal scores, and scores hundreds apart whose running maximum keeps moving."""
@@ -272,6 +354,23 @@ def test_prefix_many_rows(B):
     n, shared, page = [8] * 30 + [0, 0], 640, 16
     kv_len = [shared + 3 * r for r in range(30)] + [shared, shared]
     check_attention(B, 8, n, kv_len, page, 16, 2, 128, groups=([0, 30, 32], [shared, shared]), shared=shared)
+
+
+@pytest.mark.parametrize("page,hq,hkv,d", [(16, 8, 1, 64), (25, 16, 2, 128)])
+def test_prefix_cut_into_pieces(B, page, hq, hkv, d):
+    """Groups of one and several tiles over long shared parts, requests with and without rows of their own."""
+    rng = np.random.default_rng(page)
+    n = [int(x) for x in rng.integers(0, 12, 24)]
+    shared = [page * 150, page * 31]
+    kv_len = [shared[r >= 20] + int(rng.integers(0, 300)) for r in range(24)]
+    q, kc, vc, table, cu = attention_case(14, n, kv_len, page, hq, hkv, d)
+    for r in range(24):
+        table[r, :shared[r >= 20] // page] = table[20 * (r >= 20), :shared[r >= 20] // page]
+    out, z, status = attend(B, q, kc, vc, table, kv_len, cu, groups=([0, 20, 24], shared))
+    assert status == 0
+    ref, lse, tol, ztol = A.attention(q, kc, vc, table, kv_len, cu, float(np.float32(d ** -0.5)), False)
+    close(out, ref, tol, "out")
+    close(z, lse, ztol, "lse")
 
 
 def test_same_bits_twice_and_without_lse(B):
