@@ -609,8 +609,8 @@ size_t dspark_attention_workspace_size(int R, int n_groups, int max_rows, int n_
  *   block_table, kv_len, cu_seqlens  as in dspark_kv_append
  *   out          [max_rows, n_q_heads, head_dim] bf16;  lse [max_rows, n_q_heads] fp32 or NULL
  *   ws, ws_bytes dspark_attention_workspace_size(R, 0, max_rows, n_q_heads, n_kv_heads, head_dim)
- * A request with a negative length, a position past max_blocks * page_size or a page id
- * outside [0, pool_pages) gets NaN rows and is reported (DSPARK_ERR_DEVICE_INPUT); rows from
+ * A request with a negative length, a position past max_blocks * page_size (or 2^31 - 514) or a page
+ * id outside [0, pool_pages) gets NaN rows and is reported (DSPARK_ERR_DEVICE_INPUT); rows from
  * cu_seqlens[R] on are not touched.  cu_seqlens that decreases, does not start at 0 or passes
  * max_rows makes all max_rows rows NaN.  Limits (DSPARK_ERR_UNSUPPORTED): head_dim 64 or 128,
  * at most 128 query heads to a key head, pool_pages * n_kv_heads * page_size < 2^31 - 1,
