@@ -88,18 +88,25 @@ struct Job {
     int first, last;    // CTAs that have a piece
     int row0, tile_row; // rows of q of the entry, and the item's first (row, query head) of it
     int head;           // key head
-    int merge_prefix;   // the rows have a shared part too
-    int pad;
+    int pad[2];
 };
 
-// Workspace of one launch.
+// Workspace.  Of a query row and head, lin = row * g + (its place among the key head's).
 struct Plan {
-    Job* jobs;           // [ctas]
-    float* part;         // [2 * ctas][d / 4][kRows][4]  slot 2c: the item cut before CTA c's piece, 2c + 1: after it
-    float2* part_ml;     // [2 * ctas][kRows]
-    float* whole;        // groups only, [hkv][d / 4][rows * g][4]: the shared part's sums of every row
-    float2* whole_ml;    // [hkv][rows * g]
+    float* part;      // [2 * ctas][d / 4][kRows][4]  sums of slot 2c: the item cut before CTA c's piece, 2c + 1: after it
+    float2* part_ml;  // [2 * ctas][kRows]
+    Job* jobs;        // [ctas]; with shared parts instead, of each row's own and shared part:
+    float* whole;     // [2][hkv][d / 4][rows * g][4]  its sums, if the item was not cut
+    float2* whole_ml; // [2][hkv][rows * g]
+    int* where;       // [2][hkv][rows * g]  a Where
 };
+
+// Where the sums of a row's part lie.
+struct Where {
+    static constexpr int kSkip = -1, kCut = 1 << 24, kShared = 1 << 25;  // (of the own part: there is a shared one)
+    static __device__ __forceinline__ int of(int first, int last, int row) { return kCut | first << 16 | last << 8 | row; }
+};
+static_assert(kMaxCtas <= 256 && kRows <= 256, "bytes of a Where");
 
 struct Entry {     // a request's own keys, or a group's shared ones
     int row0, n;   // its rows of q (0: nothing to do)
@@ -108,6 +115,7 @@ struct Entry {     // a request's own keys, or a group's shared ones
     int len;       // row i sees keys below len + i + 1 (-1: all rows see the same keys)
     int table;     // the block table's row
     int tiles, blocks;
+    bool shared;   // a group's
     int log_steps; // a block takes 2^log_steps steps: of more than kTile rows it serves two tiles
     __device__ int units() const { return (blocks << log_steps) + kItemCost; }  // of an item: its steps, and what else it costs
     __device__ long long cost(int hkv) const { return (long long)tiles * hkv * units(); }
@@ -124,9 +132,8 @@ __device__ __forceinline__ int group_of(const AttnParams& p, int r) {
     return lo;
 }
 
-// Keys below which request r's are shared (0 without groups); -1: its group's length is bad.
+// Keys below which request r's are shared; -1: its group's length is bad.
 __device__ __forceinline__ int shared_of(const AttnParams& p, int r) {
-    if (p.n_groups == 0) return 0;
     const int s = p.shared_len[group_of(p, r)];
     return s >= 0 && s % p.page == 0 ? s : -1;
 }
@@ -136,23 +143,26 @@ __device__ __forceinline__ bool request_ok(const AttnParams& p, int len, int n, 
            (long long)len + n <= kMaxKeys;
 }
 
-template <bool kGroups>
+// Entry e: with kPrefix the groups' come first.
+template <bool kPrefix>
 __device__ __forceinline__ Entry entry_of(const AttnParams& p, int e) {
     Entry x;
     x.begin = 0;
-    if (kGroups) {
+    x.shared = kPrefix && e < p.n_groups;
+    if (x.shared) {
         const int r0 = p.group_start[e], r1 = p.group_start[e + 1];
         const int s = p.shared_len[e];
+        const bool ok = r0 >= 0 && r0 <= r1 && r1 <= p.R && s > 0 && s <= kMaxKeys && s % p.page == 0 && s / p.page <= p.max_blocks;
         x.table = r0;
-        x.row0 = p.cu[r0];
-        x.n = p.cu[r1] - x.row0;
+        x.row0 = ok ? p.cu[r0] : 0;
+        x.n = ok ? p.cu[r1] - x.row0 : 0;
         x.len = -1;
         x.end = s;
-        if (s <= 0 || s % p.page || (long long)s > (long long)p.max_blocks * p.page || s > kMaxKeys) x.n = 0;
     } else {
-        const int lo = p.cu[e], n = p.cu[e + 1] - lo, len = p.kv_len[e];
-        const int shared = shared_of(p, e);
-        x.table = e;
+        const int r = kPrefix ? e - p.n_groups : e;
+        const int lo = p.cu[r], n = p.cu[r + 1] - lo, len = p.kv_len[r];
+        const int shared = kPrefix ? shared_of(p, r) : 0;
+        x.table = r;
         x.row0 = lo;
         x.n = request_ok(p, len, n, shared) ? n : 0;
         x.begin = shared;
@@ -190,6 +200,7 @@ struct Piece {
     int low, high;        // past the last key that the item's first and last row see
     int g0;               // steps of the pieces before
     int last_cta;         // that has a piece of the item
+    int shared;           // of a group's keys
     int spoiled;          // a page is missing: the rows are NaN
     int edge, look;       // first block, from b0 on, that some row does not see whole; that a box may overrun
     int log_copies;       // the rows lie in a tile so many times
@@ -287,10 +298,9 @@ struct Maps {
     int box_rows;      // 0: rows are gathered one by one
 };
 
-template <int kD, bool kGroups>
-__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams p, const Plan plan, const Plan shared_plan,
-                                                               const int max_ctas, const int entries,
-                                                               const __grid_constant__ Maps maps) {
+template <int kD, bool kPrefix>
+__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams p, const Plan plan, const int max_ctas,
+                                                               const int entries, const __grid_constant__ Maps maps) {
     using L = Layout<kD>;
     constexpr int kChunks = kD / 8;
     constexpr int kSlots = L::kSlots;
@@ -335,17 +345,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         }
         tc::fence_barrier_init();
     }
-    // (Nothing before this depends on what earlier kernels wrote.  Behind the shared parts' launch the rest does not
-    // either, but for the shared parts themselves.)
-    if (kGroups || p.n_groups == 0) wait_prior_grid();
+    wait_prior_grid();  // (nothing before this depends on what earlier kernels wrote)
     launch_dependents();
-    if (tid == 0) plan.jobs[blockIdx.x].n_rows = 0;
+    if (!kPrefix && tid == 0) plan.jobs[blockIdx.x].n_rows = 0;
     // every thread has `per` entries
     const int per = (entries + kThreads - 1) / kThreads;
     auto cost_of = [&](int t) {
         long long c = 0;
 #pragma unroll 1
-        for (int e = t * per; e < min(entries, (t + 1) * per); ++e) c += entry_of<kGroups>(p, e).cost(p.hkv);
+        for (int e = t * per; e < min(entries, (t + 1) * per); ++e) c += entry_of<kPrefix>(p, e).cost(p.hkv);
         return c;
     };
     auto scanned = [&](long long c) {  // over the warp, each lane's included
@@ -357,18 +365,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         return c;
     };
     int bad = p.cu[0] != 0 || p.cu[p.R] > p.rows;
-    if (p.n_groups) bad |= p.group_start[0] != 0 || p.group_start[p.n_groups] != p.R;
+    if (kPrefix) bad |= p.group_start[0] != 0 || p.group_start[p.n_groups] != p.R;
 #pragma unroll 1
     for (int r = tid; r < p.R; r += kThreads) bad |= p.cu[r] > p.cu[r + 1];
+    if (kPrefix)
 #pragma unroll 1
-    for (int e = tid; e < p.n_groups; e += kThreads) {
-        const int r0 = p.group_start[e], r1 = p.group_start[e + 1];
-        bad |= r0 < 0 || r0 > r1 || r1 > p.R;
-    }
-    // (a group's entry is formed from its requests' rows: only when these are within cu)
-    long long mine = 0;
-    if (!kGroups || !bad) mine = cost_of(tid);
-    mine = scanned(mine);
+        for (int e = tid; e < p.n_groups; e += kThreads) bad |= p.group_start[e] > p.group_start[e + 1];
+    const long long mine = scanned(cost_of(tid));
     if (lane == 31) sh.scan[warp] = mine;
     long long* const scans = reinterpret_cast<long long*>(base + 2 * L::kOperand);  // each thread's, over its warp (in the ring)
     scans[tid] = mine;
@@ -379,8 +382,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sh.tmem_base, 0);
     if (bad) {  // nothing can be said of any row
         if (warp == 12) tc::tmem_dealloc(tmem, 512);
-        if (kGroups) return;
-        wait_prior_grid();  // (so that whoever waits for this grid waits for the shared parts' too)
         const long long n = (long long)p.rows * p.hq;
 #pragma unroll 1
         for (long long i = (long long)blockIdx.x * kThreads + tid; i < n * kD; i += (long long)gridDim.x * kThreads) p.out[i] = kNan;
@@ -388,6 +389,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
 #pragma unroll 1
             for (long long i = (long long)blockIdx.x * kThreads + tid; i < n; i += (long long)gridDim.x * kThreads)
                 p.lse[i] = __int_as_float(0x7FC00000);
+        if (kPrefix)
+#pragma unroll 1
+            for (long long i = (long long)blockIdx.x * kThreads + tid; i < n; i += (long long)gridDim.x * kThreads)
+                plan.where[i] = Where::kSkip;
         if (blockIdx.x == 0 && tid == 0) report(p.dev_status, DSPARK_ERR_DEVICE_INPUT);
         return;
     }
@@ -457,7 +462,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         int n_step = 0;     // steps of this tile so far
         int n_done = 0;     // of them, the ones whose product is waited for
         int n_merge = 0;
-        bool prior_done = false;
         Cursor at;
         for (; open(at) && !stopped(); close(at), ++at.i) {
             const Piece& w = *at.at;
@@ -626,15 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                 m0 = top;
             };
             m = m == -INFINITY ? -INFINITY : m * sl2;  // base-2 from here on
-            const size_t lin_step = (size_t)p.rows * g, lin0 = (size_t)w.row0 * g + w.tile_row + sub * kTile;
-            const bool prefix = !kGroups && w.uncut && p.n_groups > 0 && w.begin > 0;
-            float2 shared_ml = make_float2(-INFINITY, 0.0f);
-            if (prefix) {  // (asked for early: it is needed after the copies' sums)
-                if (!prior_done) wait_prior_grid();
-                prior_done = true;
-                shared_ml = shared_plan.whole_ml[(size_t)w.head * lin_step + lin0 + (live ? t_row : 0)];
-            }
-            float f1 = 1.0f, f2 = 0.0f, f3 = 0.0f;     // scales of this tile's, the other tile's, the shared part's sums
+            float f1 = 1.0f, f2 = 0.0f;                // scales of this tile's, the other tile's sums
             if (two) {
                 wait(&sh.merge, n_merge);
                 tc::tc_fence_after();
@@ -663,24 +659,19 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
             }
             if (w.spoiled) l = __int_as_float(0x7FC00000);
             const bool uncut = w.uncut != 0;
-            const bool final = !kGroups && uncut;
+            const bool final = !kPrefix && uncut;
             const size_t slot = (size_t)(2 * blockIdx.x + (w.b0 == 0)) * kRows;  // its first row
-            // partial sums lie by four columns, then rows, so that a warp's stores are contiguous
-            if (prefix) {
-                float fa;
-                add(m, l, shared_ml.x, shared_ml.y, fa, f3);
-                f1 *= fa;
-                f2 *= fa;
-            }
             if (final) {
                 const float inv = 1.0f / l;
                 f1 *= inv;
                 f2 *= inv;
-                f3 *= inv;
             }
-            const float4* const shared_part = reinterpret_cast<const float4*>(shared_plan.whole + (size_t)w.head * lin_step * kD);
-            float4* const to = reinterpret_cast<float4*>(uncut ? plan.whole + (size_t)w.head * lin_step * kD : plan.part + slot * kD);
-            const size_t to0 = uncut ? lin0 : sub * kTile, to_step = uncut ? lin_step : kRows;
+            // partial sums lie by four columns, then rows, so that a warp's stores are contiguous
+            const bool whole = kPrefix && uncut;
+            const size_t lin_step = (size_t)p.rows * g, lin0 = (size_t)w.row0 * g + w.tile_row + sub * kTile;
+            const size_t part_of = (size_t)(w.shared * p.hkv + w.head) * lin_step;  // in the rows' own or shared parts
+            float4* const to = reinterpret_cast<float4*>(whole ? plan.whole + part_of * kD : plan.part + slot * kD);
+            const size_t to0 = whole ? lin0 : sub * kTile, to_step = whole ? lin_step : kRows;
             auto row_of_out = [&](int r) {  // of this tile's row r
                 const int i = (w.tile_row + sub * kTile + r) / g;
                 return (size_t)(w.row0 + i) * p.hq + w.head * g + (w.tile_row + sub * kTile + r - i * g);
@@ -709,16 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
 #pragma unroll 1
                 for (int c = 0; c < kD; c += 16) {
                     float o[16];
-                    float4 next[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        next[j] = !prefix || !live ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : shared_part[(size_t)(c / 4 + j) * lin_step + lin0 + t_row];
                     sums(c, o);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        o[4 * j] += next[j].x * f3; o[4 * j + 1] += next[j].y * f3;
-                        o[4 * j + 2] += next[j].z * f3; o[4 * j + 3] += next[j].w * f3;
-                    }
                     if (live) {
                         uint2 b[4];
 #pragma unroll
@@ -736,17 +718,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
             } else {
                 // The copies' sums meet in the item's query buffer, half of the columns at a time.
                 float4* const stage = reinterpret_cast<float4*>(base + (w.n_q & 1) * L::kOperand);  // [c / 4][128 lanes]
-                if (final) sh.ml[X][t128] = make_float2(f3, __int_as_float(live ? (int)row_of_out(t_row) : 0));
+                if (final) sh.ml[X][t128].x = __int_as_float(live ? (int)row_of_out(t_row) : 0);
                 constexpr int kQuads = kD / 8, kApart = kTile / kQuads, kBatch = 32 / kApart;
                 const int my_q = opaque(t128) % kQuads, my_r0 = opaque(t128) / kQuads;  // of the output: four columns of every kApart-th row
-                float4 pre[kBatch];                                     // the shared part's sums of them
 #pragma unroll 1
                 for (int c0 = 0; c0 < kD; c0 += kD / 2) {
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i)  // (there by the time the sums are in their places)
-                        pre[i] = !prefix || my_r0 + i * kApart >= n_rows
-                                     ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
-                                     : shared_part[(size_t)(c0 / 4 + my_q) * lin_step + lin0 + my_r0 + i * kApart];
 #pragma unroll 1
                     for (int c = 0; c < kD / 2; c += 16) {
                         float o[16];
@@ -772,11 +748,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                         for (int i = 0; i < kBatch; ++i) {
                             const int r = my_r0 + i * kApart;
                             if (r < n_rows) {
-                                const float2 f = sh.ml[X][r];
-                                float4 y = sum_of(my_q, r);
-                                y.x += pre[i].x * f.x; y.y += pre[i].y * f.x;
-                                y.z += pre[i].z * f.x; y.w += pre[i].w * f.x;
-                                *reinterpret_cast<uint2*>(p.out + (size_t)__float_as_int(f.y) * kD + c0 + 4 * my_q) = pack(y);
+                                const int at_row = __float_as_int(sh.ml[X][r].x);
+                                *reinterpret_cast<uint2*>(p.out + (size_t)at_row * kD + c0 + 4 * my_q) = pack(sum_of(my_q, r));
                             }
                         }
                     } else {  // a column's rows
@@ -789,10 +762,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                 if (t128 == 0) tc::mbar_arrive(&sh.q_empty[w.n_q & 1]);
             }
             if (live && t128 == t_row) {
-                if (!final) (uncut ? plan.whole_ml + (size_t)w.head * lin_step : plan.part_ml + slot)[to0 + t_row] = make_float2(m, l);
+                if (!final) (whole ? plan.whole_ml + part_of : plan.part_ml + slot)[to0 + t_row] = make_float2(m, l);
                 else if (p.lse) p.lse[row_of_out(t_row)] = (m + log2f(l)) * kLn2;
+                if (kPrefix && w.b0 == 0)
+                    plan.where[part_of + lin0 + t_row] = (uncut ? 0 : Where::of(blockIdx.x, w.last_cta, sub * kTile + t_row)) |
+                                                         (w.begin > 0 ? Where::kShared : 0);
             }
-            if (t128 == 0 && !uncut && w.b0 == 0 && sub == 0) {
+            if (!kPrefix && t128 == 0 && !uncut && w.b0 == 0 && sub == 0) {
                 Job j;
                 j.n_rows = w.n_rows;
                 j.first = blockIdx.x;
@@ -800,8 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                 j.row0 = w.row0;
                 j.tile_row = w.tile_row;
                 j.head = w.head;
-                j.merge_prefix = !kGroups && p.n_groups > 0 && w.begin > 0;
-                j.pad = 0;
+                j.pad[0] = j.pad[1] = 0;
                 plan.jobs[blockIdx.x] = j;
             }
         }
@@ -1186,7 +1161,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
             __syncwarp();
 #pragma unroll 1
             for (int e = (32 * w + l) * per; start < x1 && e < entries && !stopped(); ++e) {
-                const Entry en = entry_of<kGroups>(p, e);
+                const Entry en = entry_of<kPrefix>(p, e);
                 const int units = en.units(), log_steps = en.log_steps, round = (1 << log_steps) - 1;
                 const int items = en.tiles * p.hkv, skip = (int)min(divide(max(x0 - start, 0LL), units), (long long)items);
                 start += (long long)skip * units;
@@ -1210,6 +1185,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                         x.end = en.end;
                         x.len = en.len;
                         x.table = en.table;
+                        x.shared = en.shared;
                         x.low = en.limit(t ? tile_row / g : 0);
                         x.high = high;
                         x.edge = x.low < high ? max((x.low - en.begin) / kBlock - b0, 0) : INT_MAX;
@@ -1233,20 +1209,23 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         }
         x.steps = 0;
         post(x);
-        if (!kGroups && p.n_groups > 0) wait_prior_grid();  // (so that whoever waits for this grid waits for those too)
-        if (!kGroups) {  // requests that cannot be right
+        // requests that cannot be right
 #pragma unroll 1
-            for (int r = blockIdx.x; r < p.R; r += gridDim.x) {
-                const int n = p.cu[r + 1] - p.cu[r];
-                if (n == 0 || entry_of<false>(p, r).n > 0) continue;
-                const long long from = (long long)p.cu[r] * p.hq, to = (long long)p.cu[r + 1] * p.hq;
+        for (int r = blockIdx.x; r < p.R; r += gridDim.x) {
+            const int n = p.cu[r + 1] - p.cu[r];
+            if (n == 0 || entry_of<kPrefix>(p, kPrefix ? p.n_groups + r : r).n > 0) continue;
+            const long long from = (long long)p.cu[r] * p.hq, to = (long long)p.cu[r + 1] * p.hq;
 #pragma unroll 1
-                for (long long j = from * kD + lane; j < to * kD; j += 32) p.out[j] = kNan;
-                if (p.lse)
+            for (long long j = from * kD + lane; j < to * kD; j += 32) p.out[j] = kNan;
+            if (p.lse)
 #pragma unroll 1
-                    for (long long j = from + lane; j < to; j += 32) p.lse[j] = __int_as_float(0x7FC00000);
-                if (lane == 0) report(p.dev_status, DSPARK_ERR_DEVICE_INPUT);
-            }
+                for (long long j = from + lane; j < to; j += 32) p.lse[j] = __int_as_float(0x7FC00000);
+            if (kPrefix)
+#pragma unroll 1
+                for (int h = 0; h < p.hkv; ++h)
+                    for (long long j = (long long)p.cu[r] * g + lane; j < (long long)p.cu[r + 1] * g; j += 32)
+                        plan.where[(long long)h * p.rows * g + j] = Where::kSkip;
+            if (lane == 0) report(p.dev_status, DSPARK_ERR_DEVICE_INPUT);
         }
     }
     __syncwarp();
@@ -1261,33 +1240,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
 // ---------------------------------------------------------------- joining the pieces
 constexpr int kJoinCols = 16;  // of a CTA
 
-// CTA (c, i): columns [16 i, 16 i + 16) of the item that CTA c of the attention
-// kernel began and did not finish, a thread to a row; the pieces are added in
-// their order, the shared part first.
-template <int kD, bool kGroups>
-__global__ void __launch_bounds__(kRows) join_kernel(const AttnParams p, const Plan plan, const Plan shared_plan) {
-    constexpr int kQuads = kJoinCols / 4;
-    launch_dependents();
-    wait_prior_grid();
-    const Job job = plan.jobs[blockIdx.x];
-    const int r = threadIdx.x, g = p.hq / p.hkv;
-    if (r >= job.n_rows) return;
-    const int col = blockIdx.y * kQuads;  // in fours
-    const int lin = job.row0 * g + job.tile_row + r;
-    const size_t lin_step = (size_t)p.rows * g, lin_ml = (size_t)job.head * p.rows * g + lin;
-    const size_t lin_at = ((size_t)job.head * (kD / 4) + col) * lin_step + lin;
+// A row's sums over 16 columns, from col (in fours) on.
+struct RowSum {
+    static constexpr int kQuads = kJoinCols / 4;
     float m = -INFINITY, l = 0.0f;
-    float4 o[kQuads];
-#pragma unroll
-    for (int q = 0; q < kQuads; ++q) o[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int c = job.first - job.merge_prefix; c <= job.last; ++c) {
-        const bool shared = c < job.first;
-        const size_t slot = (size_t)(2 * c + (c == job.first)) * kRows;
-        const float2 ml = shared ? shared_plan.whole_ml[lin_ml] : plan.part_ml[slot + r];
-        const float4* from = shared ? reinterpret_cast<const float4*>(shared_plan.whole) + lin_at
-                                    : reinterpret_cast<const float4*>(plan.part + slot * kD) + col * kRows + r;
-        const size_t step = shared ? lin_step : kRows;
+    float4 o[kQuads] = {};
+
+    __device__ __forceinline__ void add(float2 ml, const float4* from, size_t step) {
         const float top = fmaxf(m, ml.x);
         const float fa = m == -INFINITY ? 0.0f : exp2_approx(m - top), fb = ml.x == -INFINITY ? 0.0f : exp2_approx(ml.x - top);
         l = (m == -INFINITY ? l : l * fa) + (ml.x == -INFINITY ? ml.y : ml.y * fb);
@@ -1299,13 +1258,17 @@ __global__ void __launch_bounds__(kRows) join_kernel(const AttnParams p, const P
             o[q].z = o[q].z * fa + v.z * fb; o[q].w = o[q].w * fa + v.w * fb;
         }
     }
-    if (kGroups) {
-#pragma unroll
-        for (int q = 0; q < kQuads; ++q) reinterpret_cast<float4*>(plan.whole)[lin_at + q * lin_step] = o[q];
-        if (col == 0) plan.whole_ml[lin_ml] = make_float2(m, l);
-    } else {
-        const int i = (job.tile_row + r) / g;
-        const size_t item = (size_t)(job.row0 + i) * p.hq + job.head * g + (job.tile_row + r - i * g);
+    // Row r of the item that CTAs first .. last have pieces of.
+    template <int kD>
+    __device__ __forceinline__ void add_pieces(const Plan& plan, int first, int last, int r, int col) {
+#pragma unroll 4
+        for (int c = first; c <= last; ++c) {
+            const size_t slot = (size_t)(2 * c + (c == first)) * kRows;
+            add(plan.part_ml[slot + r], reinterpret_cast<const float4*>(plan.part + slot * kD) + col * kRows + r, kRows);
+        }
+    }
+    template <int kD>
+    __device__ __forceinline__ void write(const AttnParams& p, size_t row, int col) const {
         const float inv = 1.0f / l;
         alignas(16) __nv_bfloat162 w[2 * kQuads];
 #pragma unroll
@@ -1313,25 +1276,72 @@ __global__ void __launch_bounds__(kRows) join_kernel(const AttnParams p, const P
             w[2 * q] = __floats2bfloat162_rn(o[q].x * inv, o[q].y * inv);
             w[2 * q + 1] = __floats2bfloat162_rn(o[q].z * inv, o[q].w * inv);
         }
-        uint4* to = reinterpret_cast<uint4*>(p.out + item * kD + col * 4);
+        uint4* to = reinterpret_cast<uint4*>(p.out + row * kD + col * 4);
 #pragma unroll
         for (int q = 0; q < kQuads / 2; ++q) to[q] = reinterpret_cast<const uint4*>(w)[q];
-        if (p.lse && col == 0) p.lse[item] = (m + log2f(l)) * kLn2;
+        if (p.lse && col == 0) p.lse[row] = (m + log2f(l)) * kLn2;
     }
+};
+
+// CTA (c, i): columns [16 i, 16 i + 16) of the item that CTA c of the attention
+// kernel began and did not finish, a thread to a row; the pieces are added in
+// their order.
+template <int kD>
+__global__ void __launch_bounds__(kRows) join_kernel(const AttnParams p, const Plan plan) {
+    launch_dependents();
+    wait_prior_grid();
+    const Job job = plan.jobs[blockIdx.x];
+    const int r = threadIdx.x, g = p.hq / p.hkv, col = blockIdx.y * RowSum::kQuads;
+    if (r >= job.n_rows) return;
+    RowSum sum;
+    sum.add_pieces<kD>(plan, job.first, job.last, r, col);
+    const int i = (job.tile_row + r) / g;
+    sum.write<kD>(p, (size_t)(job.row0 + i) * p.hq + job.head * g + (job.tile_row + r - i * g), col);
+}
+
+// CTA (i, j): columns [16 j, 16 j + 16) of 256 rows of a key head, a thread to a
+// row: its shared part, then its own.
+template <int kD>
+__global__ void __launch_bounds__(kRows) prefix_join_kernel(const AttnParams p, const Plan plan) {
+    launch_dependents();
+    wait_prior_grid();
+    const int g = p.hq / p.hkv, col = blockIdx.y * RowSum::kQuads;
+    const long long lins = (long long)p.rows * g, blocks = (lins + kRows - 1) / kRows;
+    const int head = (int)(blockIdx.x / blocks);
+    const long long lin = (blockIdx.x - head * blocks) * kRows + threadIdx.x, row = lin / g;
+    if (row >= min(p.cu[p.R], p.rows)) return;
+    const int own = plan.where[head * lins + lin];
+    if (own == Where::kSkip) return;
+    RowSum sum;
+#pragma unroll
+    for (int side = 1; side >= 0; --side) {
+        if (side && !(own & Where::kShared)) continue;
+        const long long at = (side * p.hkv + head) * lins + lin;
+        const int w = side ? plan.where[at] : own;
+        if (w & Where::kCut) sum.add_pieces<kD>(plan, w >> 16 & 255, w >> 8 & 255, w & 255, col);
+        else sum.add(plan.whole_ml[at], reinterpret_cast<const float4*>(plan.whole) + (at - lin) * (kD / 4) + col * lins + lin, lins);
+    }
+    sum.write<kD>(p, row * p.hq + head * g + (lin - row * g), col);
 }
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
-// One launch's plan in the workspace at `off` (which moves on).
-Plan plan_at(void* ws, size_t& off, long long items, int d, bool whole) {
+// The plan in the workspace; its size.
+size_t plan_at(void* ws, Plan& p, long long items, int d, bool prefix) {
     unsigned char* b = static_cast<unsigned char*>(ws);
-    Plan p;
-    p.jobs = reinterpret_cast<Job*>(b + off); off += up(sizeof(Job) * kMaxCtas);
-    p.part = reinterpret_cast<float*>(b + off); off += sizeof(float) * 2 * kMaxCtas * kRows * (size_t)d;
-    p.part_ml = reinterpret_cast<float2*>(b + off); off += sizeof(float2) * 2 * kMaxCtas * kRows;
-    p.whole = reinterpret_cast<float*>(b + off); off += whole ? up(sizeof(float) * (size_t)items * d) : 0;
-    p.whole_ml = reinterpret_cast<float2*>(b + off); off += whole ? up(sizeof(float2) * (size_t)items) : 0;
-    return p;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        void* at = b + off;
+        off += up(bytes);
+        return at;
+    };
+    p.part = static_cast<float*>(take(sizeof(float) * 2 * kMaxCtas * kRows * (size_t)d));
+    p.part_ml = static_cast<float2*>(take(sizeof(float2) * 2 * kMaxCtas * kRows));
+    p.jobs = static_cast<Job*>(take(prefix ? 0 : sizeof(Job) * kMaxCtas));
+    p.whole = static_cast<float*>(take(prefix ? sizeof(float) * 2 * (size_t)items * d : 0));
+    p.whole_ml = static_cast<float2*>(take(prefix ? sizeof(float2) * 2 * (size_t)items : 0));
+    p.where = static_cast<int*>(take(prefix ? sizeof(int) * 2 * (size_t)items : 0));
+    return off;
 }
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -1361,8 +1371,8 @@ bool encode_boxes(CUtensorMap* m, const void* base, long long rows, int d, int b
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kD>
-cudaError_t launch_d(const AttnParams& p, cudaStream_t stream) {
+template <int kD, bool kPrefix>
+cudaError_t launch_as(const AttnParams& p, cudaStream_t stream) {
     Maps maps{};
     int box_rows = 128;  // the largest power of two that every page is a multiple of
     while (p.page % box_rows) box_rows /= 2;
@@ -1377,35 +1387,29 @@ cudaError_t launch_d(const AttnParams& p, cudaStream_t stream) {
     if (err != cudaSuccess) return err;
     if ((err = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return err;
     const int ctas = n_sm < kMaxCtas ? n_sm : kMaxCtas;
-    const long long items = (long long)p.rows * p.hq;
-    size_t off = 0;
-    const Plan plan = plan_at(p.ws, off, items, kD, false);
-    Plan shared_plan = plan;
+    Plan plan;
+    plan_at(p.ws, plan, (long long)p.rows * p.hq, kD, kPrefix);
     const int smem = Layout<kD>::kTotal;
-    const dim3 join_grid(ctas, kD / kJoinCols);
-    if ((err = cudaFuncSetAttribute(attention_kernel<kD, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
+    if ((err = cudaFuncSetAttribute(attention_kernel<kD, kPrefix>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
         return err;
-    if (p.n_groups > 0) {
-        shared_plan = plan_at(p.ws, off, items, kD, true);
-        if ((err = cudaFuncSetAttribute(attention_kernel<kD, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
-            return err;
-        if ((err = launch_after(attention_kernel<kD, true>, dim3(ctas), kThreads, smem, stream, p, shared_plan, shared_plan, ctas, p.n_groups, maps)) != cudaSuccess)
-            return err;
-        if ((err = launch_after(join_kernel<kD, true>, join_grid, kRows, 0, stream, p, shared_plan, shared_plan)) != cudaSuccess)
-            return err;
-    }
-    if ((err = launch_after(attention_kernel<kD, false>, dim3(ctas), kThreads, smem, stream, p, plan, shared_plan, ctas, p.R, maps)) != cudaSuccess)
+    if ((err = launch_after(attention_kernel<kD, kPrefix>, dim3(ctas), kThreads, smem, stream, p, plan, ctas,
+                            kPrefix ? p.n_groups + p.R : p.R, maps)) != cudaSuccess)
         return err;
-    return launch_after(join_kernel<kD, false>, join_grid, kRows, 0, stream, p, plan, shared_plan);
+    if (!kPrefix) return launch_after(join_kernel<kD>, dim3(ctas, kD / kJoinCols), kRows, 0, stream, p, plan);
+    const long long blocks = ((long long)p.rows * (p.hq / p.hkv) + kRows - 1) / kRows * p.hkv;
+    return launch_after(prefix_join_kernel<kD>, dim3((unsigned)blocks, kD / kJoinCols), kRows, 0, stream, p, plan);
+}
+
+template <int kD>
+cudaError_t launch_d(const AttnParams& p, cudaStream_t stream) {
+    return p.n_groups > 0 ? launch_as<kD, true>(p, stream) : launch_as<kD, false>(p, stream);
 }
 
 }  // namespace
 
 size_t attention_workspace(int, int n_groups, int rows, int hq, int, int d) {
-    size_t off = 0;
-    plan_at(nullptr, off, (long long)rows * hq, d, false);
-    if (n_groups > 0) plan_at(nullptr, off, (long long)rows * hq, d, true);
-    return off;
+    Plan plan;
+    return plan_at(nullptr, plan, (long long)rows * hq, d, n_groups > 0);
 }
 
 cudaError_t launch_attention(const AttnParams& p, cudaStream_t stream) {
