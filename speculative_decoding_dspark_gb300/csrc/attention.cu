@@ -48,18 +48,20 @@
 // Splitting: the steps of all items form one line, which is cut into equal
 // pieces, one per CTA (each item costs some steps more, for its queries and
 // output).  An item that is cut leaves its triples in the workspace and a second
-// kernel joins them in their order.  The cut depends on the lengths, which only
-// the device knows: every CTA scans them itself.
+// kernel joins them in a fixed order.  With shared pages the groups' items (their
+// keys, the rows of all their requests) and the requests' own go into the same line,
+// and the second kernel adds each row's parts.  The cut depends on the lengths, which
+// only the device knows: every CTA scans them itself.
 //
 // What bounds it: bytes, where few rows read many keys (128 requests of up to 5000,
-// 1296 MB: 206 us, 93 % of the copy rate).  Many rows over the same keys: the way of a tile
-// from its scores to its next ones, 1350 cycles of exponentials and 1950 of products
-// and their hand-over, in which the other tile's go by too: 1024 of 1665 cycles of a
-// step the tensor cores are at work (128 queries by 8192 shared keys: 80 us).  Short
-// items: 9000 cycles from the last product to the output and the next item's first
-// weights.  Small calls: 15000 cycles until the first product, most of them code
-// that comes into the instruction cache while every warp waits for it (kept at 100 KB;
-// at 180 KB a third of the issue slots waited throughout), and the second launch.
+// 1296 MB: 206 us, 93 % of the copy rate).  Many rows over the same keys: the way of
+// a tile from its scores to its next ones, 1350 cycles of exponentials and 1950 of
+// products and their hand-over, in which the other tile's go by too: 1024 of 1665
+// cycles of a step the tensor cores are at work.  Short items: some 9000 cycles from
+// the last product to the output and the next item's first weights.  Small calls:
+// 15000 cycles until the first product, most of them code that comes into the
+// instruction cache while every warp waits for it (92 KB of it; at 180 KB a third of
+// the issue slots waited throughout), and the second launch.
 #include <type_traits>
 
 #include "kernels.cuh"
@@ -73,8 +75,9 @@ constexpr int kLoaders = 128;
 constexpr int kTile = 128;   // rows of a tile
 constexpr int kRows = 256;   // rows of an item
 constexpr int kBlock = 128;  // keys of a block
-// Steps that an item costs besides its own.  3, 4, 5, 6: 169, 162, 165, 162 us for short ragged requests behind a
-// shared prefix of 8192, 38, 34, 39, 37 us behind four of 0 to 6400, 209, 208, 209, 210 us for 128 long ones.
+// Steps that an item costs besides its own.  3, 4, 5, 6: 207, 207, 208, 209 us for 128 long ragged requests, 33, 34,
+// 36, 38 us for 103 single rows behind shared prefixes of up to 6944; 160, 147, 136, 140 us for 128 short ragged
+// requests behind one of 8192, where it is a matter of where the cuts fall.
 constexpr int kItemCost = 4;
 constexpr int kMaxCtas = 152;            // one per SM
 constexpr int kMaxKeys = INT_MAX - 4 * kBlock;  // (loads look up to two blocks past the last key)
@@ -1258,14 +1261,26 @@ struct RowSum {
             o[q].z = o[q].z * fa + v.z * fb; o[q].w = o[q].w * fa + v.w * fb;
         }
     }
-    // Row r of the item that CTAs first .. last have pieces of.
+    // Row r of the item that CTAs first .. last have pieces of: the k-th of them and every n-th from there on.
     template <int kD>
-    __device__ __forceinline__ void add_pieces(const Plan& plan, int first, int last, int r, int col) {
+    __device__ __forceinline__ void add_pieces(const Plan& plan, int first, int last, int k, int n, int r, int col) {
 #pragma unroll 4
-        for (int c = first; c <= last; ++c) {
+        for (int c = first + k; c <= last; c += n) {
             const size_t slot = (size_t)(2 * c + (c == first)) * kRows;
             add(plan.part_ml[slot + r], reinterpret_cast<const float4*>(plan.part + slot * kD) + col * kRows + r, kRows);
         }
+    }
+    // Adds the sums of the threads `apart` from each other to those of the first of them.  (Called by the whole CTA.)
+    __device__ __forceinline__ void gather(int apart) {
+        __shared__ float2 all_ml[kRows];
+        __shared__ float4 all[kQuads][kRows];
+        all_ml[threadIdx.x] = make_float2(m, l);
+#pragma unroll
+        for (int q = 0; q < kQuads; ++q) all[q][threadIdx.x] = o[q];
+        __syncthreads();
+        if (threadIdx.x < apart)
+#pragma unroll 1
+            for (int t = threadIdx.x + apart; t < kRows; t += apart) add(all_ml[t], &all[0][t], kRows);
     }
     template <int kD>
     __device__ __forceinline__ void write(const AttnParams& p, size_t row, int col) const {
@@ -1284,44 +1299,50 @@ struct RowSum {
 };
 
 // CTA (c, i): columns [16 i, 16 i + 16) of the item that CTA c of the attention
-// kernel began and did not finish, a thread to a row; the pieces are added in
-// their order.
+// kernel began and did not finish.  A thread to a row; where there are many pieces
+// and few rows, up to 32 threads that share the pieces (a request of 13000 keys in 50
+// of them: 16 us instead of 38; where there are few it costs 0.6 us).
+constexpr int kManyPieces = 8;
 template <int kD>
 __global__ void __launch_bounds__(kRows) join_kernel(const AttnParams p, const Plan plan) {
     launch_dependents();
     wait_prior_grid();
     const Job job = plan.jobs[blockIdx.x];
-    const int r = threadIdx.x, g = p.hq / p.hkv, col = blockIdx.y * RowSum::kQuads;
-    if (r >= job.n_rows) return;
+    const bool share = job.last - job.first >= kManyPieces;
+    if (!share && (int)threadIdx.x >= job.n_rows) return;
+    int log_rows = share ? 3 : 8;
+    while (1 << log_rows < job.n_rows) ++log_rows;
+    const int r = threadIdx.x & ((1 << log_rows) - 1), g = p.hq / p.hkv, col = blockIdx.y * RowSum::kQuads;
     RowSum sum;
-    sum.add_pieces<kD>(plan, job.first, job.last, r, col);
+    if (r < job.n_rows) sum.add_pieces<kD>(plan, job.first, job.last, threadIdx.x >> log_rows, kRows >> log_rows, r, col);
+    if (share) sum.gather(1 << log_rows);
+    if ((int)threadIdx.x >= job.n_rows) return;
     const int i = (job.tile_row + r) / g;
     sum.write<kD>(p, (size_t)(job.row0 + i) * p.hq + job.head * g + (job.tile_row + r - i * g), col);
 }
 
-// CTA (i, j): columns [16 j, 16 j + 16) of 256 rows of a key head, a thread to a
-// row: its shared part, then its own.
+// CTA (i, j): columns [16 j, 16 j + 16) of 2^log_rows rows of a key head: their
+// shared parts, then their own.  (256 / 2^log_rows threads to a row share the pieces.)
 template <int kD>
-__global__ void __launch_bounds__(kRows) prefix_join_kernel(const AttnParams p, const Plan plan) {
+__global__ void __launch_bounds__(kRows) prefix_join_kernel(const AttnParams p, const Plan plan, const int log_rows) {
     launch_dependents();
     wait_prior_grid();
-    const int g = p.hq / p.hkv, col = blockIdx.y * RowSum::kQuads;
-    const long long lins = (long long)p.rows * g, blocks = (lins + kRows - 1) / kRows;
+    const int g = p.hq / p.hkv, col = blockIdx.y * RowSum::kQuads, k = threadIdx.x >> log_rows;
+    const long long lins = (long long)p.rows * g, blocks = (lins + (1 << log_rows) - 1) >> log_rows;
     const int head = (int)(blockIdx.x / blocks);
-    const long long lin = (blockIdx.x - head * blocks) * kRows + threadIdx.x, row = lin / g;
-    if (row >= min(p.cu[p.R], p.rows)) return;
-    const int own = plan.where[head * lins + lin];
-    if (own == Where::kSkip) return;
+    const long long lin = ((blockIdx.x - head * blocks) << log_rows) + threadIdx.x - (k << log_rows), row = lin / g;
+    const int own = row < min(p.cu[p.R], p.rows) ? plan.where[head * lins + lin] : Where::kSkip;
     RowSum sum;
 #pragma unroll
     for (int side = 1; side >= 0; --side) {
-        if (side && !(own & Where::kShared)) continue;
+        if (own == Where::kSkip || (side && !(own & Where::kShared))) continue;
         const long long at = (side * p.hkv + head) * lins + lin;
         const int w = side ? plan.where[at] : own;
-        if (w & Where::kCut) sum.add_pieces<kD>(plan, w >> 16 & 255, w >> 8 & 255, w & 255, col);
-        else sum.add(plan.whole_ml[at], reinterpret_cast<const float4*>(plan.whole) + (at - lin) * (kD / 4) + col * lins + lin, lins);
+        if (w & Where::kCut) sum.add_pieces<kD>(plan, w >> 16 & 255, w >> 8 & 255, k, kRows >> log_rows, w & 255, col);
+        else if (k == 0) sum.add(plan.whole_ml[at], reinterpret_cast<const float4*>(plan.whole) + (at - lin) * (kD / 4) + col * lins + lin, lins);
     }
-    sum.write<kD>(p, row * p.hq + head * g + (lin - row * g), col);
+    if (kRows >> log_rows > 1) sum.gather(1 << log_rows);
+    if (k == 0 && own != Where::kSkip) sum.write<kD>(p, row * p.hq + head * g + (lin - row * g), col);
 }
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
@@ -1396,8 +1417,12 @@ cudaError_t launch_as(const AttnParams& p, cudaStream_t stream) {
                             kPrefix ? p.n_groups + p.R : p.R, maps)) != cudaSuccess)
         return err;
     if (!kPrefix) return launch_after(join_kernel<kD>, dim3(ctas, kD / kJoinCols), kRows, 0, stream, p, plan);
-    const long long blocks = ((long long)p.rows * (p.hq / p.hkv) + kRows - 1) / kRows * p.hkv;
-    return launch_after(prefix_join_kernel<kD>, dim3((unsigned)blocks, kD / kJoinCols), kRows, 0, stream, p, plan);
+    // Few rows are few items in many pieces: eight threads to a row (2500 rows of a key head: 22 us instead of 26; 18000
+    // rows: 168 instead of 147).
+    const long long lins = (long long)p.rows * (p.hq / p.hkv);
+    const int log_rows = lins * p.hkv <= 16 * kRows ? 5 : 8;
+    const long long blocks = ((lins + (1 << log_rows) - 1) >> log_rows) * p.hkv;
+    return launch_after(prefix_join_kernel<kD>, dim3((unsigned)blocks, kD / kJoinCols), kRows, 0, stream, p, plan, log_rows);
 }
 
 template <int kD>
