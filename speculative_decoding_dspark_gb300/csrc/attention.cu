@@ -256,7 +256,7 @@ __device__ __forceinline__ uint32_t chunk_offset(int r, int c) {
 }
 
 constexpr int kPieces = 4;    // ahead of the products
-constexpr int kReaders = 14;  // warps that read them (with TMA one more)
+constexpr int kReaders = 15;  // warps that read them
 
 // kSteps: more than the loads can be ahead.
 template <int kSlots, int kSteps>
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
             tc::mbar_init(&sh.empty[lane], 1);
         }
         if (lane < 2) {
-            tc::mbar_init(&sh.q_full[lane], maps.box_rows > 0 ? 32 : kLoaders);
+            tc::mbar_init(&sh.q_full[lane], 32);
             tc::mbar_init(&sh.q_empty[lane], 2);
             tc::mbar_init(&sh.s_full[lane], 1);
             tc::mbar_init(&sh.p_full[lane], 4);
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         }
         if (lane < kPieces) {
             tc::mbar_init(&sh.piece_full[lane], 1);
-            tc::mbar_init(&sh.piece_empty[lane], kReaders + (maps.box_rows > 0));
+            tc::mbar_init(&sh.piece_empty[lane], kReaders);
         }
         if (lane == 0) {
             tc::mbar_init(&sh.merge, 4);
@@ -406,6 +406,19 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         const bool ok = wait_bounded(bar, parity & 1);
         if (!ok) sh.abort_flag = 1;
         return ok;
+    };
+
+    // Whether the phase is there already.
+    auto test = [&](uint64_t* bar, uint32_t parity) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(tc::smem_u32(bar)), "r"(parity & 1)
+            : "memory");
+        return __all_sync(0xFFFFFFFFu, ok) != 0;
     };
 
     // A warp's place in the sequence of pieces: piece `i` and step `u` of it.
@@ -873,10 +886,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         }
     } else if (warp < 12 || warp == 15) {
         // ================================================================ rows copied one by one
-        // (with TMA: of the queries alone, by warp 15)
+        // (the queries' by warp 15; with TMA no others)
         constexpr int kNone = -1, kMissing = -2;
         const int part = warp & 3;
-        uint32_t n_q = 0;
         auto first_key = [](const Cursor& c) { return c.at->begin + (c.at->b0 + c.block()) * kBlock; };
         // the cache row of this lane's key of the cursor's block
         auto row_of = [&](const Cursor& c) -> int {
@@ -900,31 +912,27 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                 tc::cp_async_16(dst + chunk_offset(r, c), from + (size_t)max(from_row, 0) * (kD * 2), from_row < 0 ? 0 : 16);
             }
         };
-        // parts [p0, p1) of a tile's queries
-        auto load_q = [&](const Piece& w, int sub, int p0, int p1) {
-            const int q = n_q & 1;
-            if (n_q >= 2) wait(&sh.q_empty[q], (n_q >> 1) - 1);
-#pragma unroll 1
-            for (int i = p0; i < p1; ++i) {
-                const int t_row = (32 * i + lane) & ((kTile >> w.log_copies) - 1), at = w.tile_row + sub * kTile + t_row, qi = at / g;
-                copy(sQ + q * L::kOperand, i, p.q,
-                     sub * kTile + t_row < w.n_rows ? (w.row0 + qi) * p.hq + w.head * g + (at - qi * g) : kNone);
-            }
-            cp_async_arrive_noinc(&sh.q_full[q]);
-            ++n_q;
-        };
         Cursor k;
-        bool more = open(k);
-        if (maps.box_rows > 0) {  // queries alone
+        if (warp == 15) {
+            uint32_t n_q = 0;
 #pragma unroll 1
-            while (more && !stopped()) {
+            for (; open(k) && !stopped(); close(k), ++k.i) {
+                const Piece& w = *k.at;
 #pragma unroll 1
-                for (k.u = 0; k.u <= k.pair; ++k.u) load_q(*k.at, k.u, 0, 4);
-                close(k);
-                ++k.i;
-                more = open(k);
+                for (int sub = 0; sub <= k.pair; ++sub, ++n_q) {
+                    const int q = n_q & 1;
+                    if (n_q >= 2) wait(&sh.q_empty[q], (n_q >> 1) - 1);
+#pragma unroll 1
+                    for (int i = 0; i < 4; ++i) {
+                        const int t_row = (32 * i + lane) & ((kTile >> w.log_copies) - 1), at = w.tile_row + sub * kTile + t_row, qi = at / g;
+                        copy(sQ + q * L::kOperand, i, p.q,
+                             sub * kTile + t_row < w.n_rows ? (w.row0 + qi) * p.hq + w.head * g + (at - qi * g) : kNone);
+                    }
+                    cp_async_arrive_noinc(&sh.q_full[q]);
+                }
             }
-        } else if (warp < 12) {
+        } else {
+            bool more = open(k);
             // Keys two steps ahead of the values, as the products take them.  A block's rows are looked up once, a
             // step before its keys are loaded, and kept until its values are.
             Cursor v;
@@ -933,21 +941,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
             Ring ring;
             uint32_t filled = 0;
             if (more) next = row_of(k);
-            // (a tile's queries go before its own first keys: a buffer may come free only after the step between)
-            bool queries = more;
 #pragma unroll 1
-            for (int i = opaque(-4); v.steps > 0 && !stopped();) {  // values of a step, keys of the step after the next
+            for (int i = opaque(-4); v.steps > 0 && !stopped(); ++i) {  // values of a step, keys of the step after the next
                 const bool is_k = i & 1;
-                if (is_k ? !more : i < 0) {
-                    ++i;
-                    continue;
-                }
-                if (is_k && queries) {
-                    load_q(*k.at, k.u, part, part + 1);
-                    queries = false;
-                    continue;
-                }
-                ++i;
+                if (is_k ? !more : i < 0) continue;
                 const Cursor& c = is_k ? k : v;
                 if (c.leads()) {
                     const int row = is_k ? next : kept0;
@@ -979,7 +976,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                         ++k.i;
                         more = open(k);
                     }
-                    queries = k.u <= k.pair;
                     if (more && k.leads()) next = row_of(k);
                 } else if (++v.u == v.steps) {
                     close(v);
@@ -1062,13 +1058,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         constexpr uint32_t idesc_o = tc::idesc_bf16_f32(kTile, kD) | tc::kIdescBTransposed;
         const bool copied = maps.box_rows == 0;  // (not by the async proxy)
         Ring ring;
-        uint32_t n_q = 0, k_slot = 0, v_slot = 0;
+        uint32_t n_q = 0, k_slot = 0, k_phase = 0, v_slot = 0;
         int gk = 0, gv = 0;                 // steps of the two walks
         uint32_t used[2] = {0, 0};          // items that used each tile's output
         Cursor k, v;
         bool more = open(k);
         open(v);
-        int owed = 0;  // scores that may be formed
+        int owed = 0;             // scores that may be formed
+        bool slot_known = false;  // of the next ones' keys
 #pragma unroll 1
         for (int i = opaque(-2);; ++i) {  // values of a step, then scores of the step after the next
             if (i >= 0) {
@@ -1101,19 +1098,23 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                 }
             }
             if (v.steps == 0 || stopped()) break;
-            // (a pair's last product goes before the next item's scores, whose queries may wait for the pair's first half)
             ++owed;
-            if (k.u == 0 && (v.u & v.pair)) continue;
 #pragma unroll 1
             for (; owed > 0 && more; --owed) {
                 const int X = gk & 1, sub = k.u & k.pair;
                 const uint32_t q = n_q + sub;
-                if (k.u <= k.pair) wait(&sh.q_full[q & 1], q >> 1);
-                if (sub == 0) {
+                if (!slot_known && sub == 0) {
                     k_slot = ring.s;
-                    wait(&sh.full[k_slot], ring.phase);
+                    k_phase = ring.phase;
                     ring.next();
                 }
+                slot_known = true;
+                // An item's first scores wait for its queries, these for the output of the item before the last, and the
+                // product that comes next for neither: it goes first.
+                if (k.u == 0 && n_q >= 2 && gk > gv && !test(&sh.q_full[q & 1], q >> 1)) break;
+                slot_known = false;
+                if (k.u <= k.pair) wait(&sh.q_full[q & 1], q >> 1);
+                if (sub == 0) wait(&sh.full[k_slot], k_phase);
                 if (copied || k.u <= k.pair) tc::fence_proxy_async_smem();
                 tc::tc_fence_after();
                 __syncwarp();
