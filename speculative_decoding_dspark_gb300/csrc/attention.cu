@@ -75,10 +75,10 @@ constexpr int kLoaders = 128;
 constexpr int kTile = 128;   // rows of a tile
 constexpr int kRows = 256;   // rows of an item
 constexpr int kBlock = 128;  // keys of a block
-// Steps that an item costs besides its own.  3, 4, 5, 6: 207, 207, 208, 209 us for 128 long ragged requests, 33, 34,
-// 36, 38 us for 103 single rows behind shared prefixes of up to 6944; 160, 147, 136, 140 us for 128 short ragged
-// requests behind one of 8192, where it is a matter of where the cuts fall.
-constexpr int kItemCost = 4;
+// Steps that an item costs besides its own.  2, 3, 4, 5: 205, 207, 209, 210 us for 128 long ragged requests, 139, 129,
+// 134, 141 us for 128 short ones behind a shared prefix of 8192, 30, 32, 33, 35 us for 103 single rows behind shared
+// prefixes of up to 6944.
+constexpr int kItemCost = 3;
 constexpr int kMaxCtas = 152;            // one per SM
 constexpr int kMaxKeys = INT_MAX - 4 * kBlock;  // (loads look up to two blocks past the last key)
 constexpr float kGrowth = 8.0f;
@@ -119,9 +119,11 @@ struct Entry {     // a request's own keys, or a group's shared ones
     int table;     // the block table's row
     int tiles, blocks;
     bool shared;   // a group's
-    int log_steps; // a block takes 2^log_steps steps: of more than kTile rows it serves two tiles
-    __device__ int units() const { return (blocks << log_steps) + kItemCost; }  // of an item: its steps, and what else it costs
-    __device__ long long cost(int hkv) const { return (long long)tiles * hkv * units(); }
+    bool last_pair; // its last item has more than kTile rows (as all others)
+    // A block of an item takes 2^log_steps(t) steps; what the item costs, and all of a key head.
+    __device__ int log_steps(int t) const { return t < tiles - 1 || last_pair; }
+    __device__ int units(int t) const { return (blocks << log_steps(t)) + kItemCost; }
+    __device__ long long per_head() const { return tiles ? (long long)(tiles - 1) * units(0) + units(tiles - 1) : 0; }
     // past the last key seen by row i of the entry
     __device__ int limit(int i) const { return len < 0 ? end : len + i + 1; }
 };
@@ -172,11 +174,12 @@ __device__ __forceinline__ Entry entry_of(const AttnParams& p, int e) {
         x.len = p.full_block ? -1 : len;
         x.end = len + n;
     }
-    x.log_steps = (long long)x.n * (p.hq / p.hkv) > kTile;
+    const int rows = x.n * (p.hq / p.hkv);
+    x.last_pair = (rows - 1) % kRows >= kTile;
     if (x.n <= 0) {
         x.n = x.tiles = x.blocks = 0;
     } else {
-        x.tiles = (int)(((long long)x.n * (p.hq / p.hkv) + kRows - 1) / kRows);
+        x.tiles = (rows - 1) / kRows + 1;
         x.blocks = (x.end - x.begin + kBlock - 1) / kBlock;
     }
     return x;
@@ -356,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
     auto cost_of = [&](int t) {
         long long c = 0;
 #pragma unroll 1
-        for (int e = t * per; e < min(entries, (t + 1) * per); ++e) c += entry_of<kPrefix>(p, e).cost(p.hkv);
+        for (int e = t * per; e < min(entries, (t + 1) * per); ++e) c += entry_of<kPrefix>(p, e).per_head() * p.hkv;
         return c;
     };
     auto scanned = [&](long long c) {  // over the warp, each lane's included
@@ -688,10 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
             const size_t part_of = (size_t)(w.shared * p.hkv + w.head) * lin_step;  // in the rows' own or shared parts
             float4* const to = reinterpret_cast<float4*>(whole ? plan.whole + part_of * kD : plan.part + slot * kD);
             const size_t to0 = whole ? lin0 : sub * kTile, to_step = whole ? lin_step : kRows;
-            auto row_of_out = [&](int r) {  // of this tile's row r
-                const int i = (w.tile_row + sub * kTile + r) / g;
-                return (size_t)(w.row0 + i) * p.hq + w.head * g + (w.tile_row + sub * kTile + r - i * g);
-            };
+            const size_t out_row = (size_t)(w.row0 + my_i) * p.hq + w.head * g + (my_r - my_i * g);
             auto sums = [&](int c, float (&o)[16]) {  // 16 columns of this lane's row, of both tiles
                 float o2[16];
                 tc::tmem_ld_32x32b_x16<0>(tO + c, o);
@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
             if (!log_copies) {
                 // A row to a lane: a column of a warp's sums lies in one piece, and of the output each lane writes whole
                 // sectors.
-                __nv_bfloat16* const out = p.out + (final && live ? row_of_out(t_row) : 0) * kD;
+                __nv_bfloat16* const out = p.out + out_row * kD;
 #pragma unroll 1
                 for (int c = 0; c < kD; c += 16) {
                     float o[16];
@@ -734,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
             } else {
                 // The copies' sums meet in the item's query buffer, half of the columns at a time.
                 float4* const stage = reinterpret_cast<float4*>(base + (w.n_q & 1) * L::kOperand);  // [c / 4][128 lanes]
-                if (final) sh.ml[X][t128].x = __int_as_float(live ? (int)row_of_out(t_row) : 0);
+                if (final) sh.ml[X][t128].x = __int_as_float((int)out_row);
                 constexpr int kQuads = kD / 8, kApart = kTile / kQuads, kBatch = 32 / kApart;
                 const int my_q = opaque(t128) % kQuads, my_r0 = opaque(t128) / kQuads;  // of the output: four columns of every kApart-th row
 #pragma unroll 1
@@ -779,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
             }
             if (live && t128 == t_row) {
                 if (!final) (whole ? plan.whole_ml + part_of : plan.part_ml + slot)[to0 + t_row] = make_float2(m, l);
-                else if (p.lse) p.lse[row_of_out(t_row)] = (m + log2f(l)) * kLn2;
+                else if (p.lse) p.lse[out_row] = (m + log2f(l)) * kLn2;
                 if (kPrefix && w.b0 == 0)
                     plan.where[part_of + lin0 + t_row] = (uncut ? 0 : Where::of(blockIdx.x, w.last_cta, sub * kTile + t_row)) |
                                                          (w.begin > 0 ? Where::kShared : 0);
@@ -1166,12 +1166,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
 #pragma unroll 1
             for (int e = (32 * w + l) * per; start < x1 && e < entries && !stopped(); ++e) {
                 const Entry en = entry_of<kPrefix>(p, e);
-                const int units = en.units(), log_steps = en.log_steps, round = (1 << log_steps) - 1;
-                const int items = en.tiles * p.hkv, skip = (int)min(divide(max(x0 - start, 0LL), units), (long long)items);
-                start += (long long)skip * units;
-                int h = skip / max(en.tiles, 1), t = skip - h * en.tiles;
+                const long long per_head = en.per_head();
+                if (per_head == 0) continue;
+                int h = (int)min(divide(max(x0 - start, 0LL), per_head), (long long)p.hkv);
+                start += h * per_head;
+                int t = h < p.hkv ? (int)min(divide(max(x0 - start, 0LL), en.units(0)), en.tiles - 1LL) : 0;
+                start += (long long)t * en.units(0);
 #pragma unroll 1
-                for (int item = skip; item < items && start < x1; ++item, start += units) {
+                while (h < p.hkv && start < x1) {
+                    const int log_steps = en.log_steps(t), round = (1 << log_steps) - 1;
                     const int tile_row = t * kRows, n_rows = min(en.n * g - tile_row, kRows);
                     const int high = en.limit((tile_row + n_rows - 1) / g), n_blocks = (high - en.begin + kBlock - 1) / kBlock;
                     const long long first = start + kItemCost;
@@ -1204,6 +1207,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                         x.g0 += x.steps;
                         x.n_q += 1 + x.pair;
                     }
+                    start += en.units(t);
                     if (++t == en.tiles) {
                         t = 0;
                         ++h;
