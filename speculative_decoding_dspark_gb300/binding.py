@@ -429,6 +429,11 @@ def dspark_kv_commit(kv_len, l, n_accepted, page_size, block_table, free_pages, 
 
 def _rows(t, name, dtype=None, shape=None):
     """A [rows, heads, head_dim] tensor whose rows may lie apart; the elements between rows."""
+    if (t is not None and t.is_cuda and len(size := t.shape) == 3 and (shape is None or size == shape)
+            and (dtype is None or t.dtype is dtype)):
+        s0, s1, s2 = t.stride()
+        if s2 == 1 and s1 == size[2]:
+            return s0 if size[0] > 1 else size[1] * s1
     if t is None:
         raise ValueError(f"{name} is required")
     if not t.is_cuda:
