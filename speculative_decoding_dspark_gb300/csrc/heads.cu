@@ -26,7 +26,7 @@
 // 16384 rows of 32 + 8 heads of 128 in bf16 (336 MB): a head at a time with eight
 // elements to a lane took 191 us, 104 with its next in registers, this 58 us, 85 %
 // of the copy rate.  10200 rows of 24 + 8 + 8 heads of 64 from fp32 into pages of
-// 12 (157 MB): 42 us, 54 %: there a CTA's start, four loads that wait for each
+// 12 (157 MB): 44 us, 53 %: there a CTA's start, four loads that wait for each
 // other until it knows its pages, is a third of its life.
 #include "kernels.cuh"
 #include "tc_ptx.cuh"
