@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                     }
                     const float mb = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                     // move the reference when the maximum has grown by more than 2^kGrowth
-                    const bool move = mb > m && !((mb - m) * sl2 <= kGrowth);
+                    const bool move = live && mb > m && !((mb - m) * sl2 <= kGrowth);
                     if (__any_sync(0xFFFFFFFFu, move)) {
                         const float f = !move ? 1.0f : m == -INFINITY ? 0.0f : exp2_approx((m - mb) * sl2);
                         if (move) m = mb;
@@ -887,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
     } else if (warp < 12 || warp == 15) {
         // ================================================================ rows copied one by one
         // (the queries' by warp 15; with TMA no others)
-        constexpr int kNone = -1, kMissing = -2;
+        constexpr int kNone = -1, kMissing = -2, kPerPass = 32 / kChunks;  // (rows that 32 chunks make up)
         const int part = warp & 3;
         auto first_key = [](const Cursor& c) { return c.at->begin + (c.at->b0 + c.block()) * kBlock; };
         // the cache row of this lane's key of the cursor's block
@@ -902,7 +902,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         };
         // This lane's row and those of its warp (row < 0: zeros) to their places of an operand.
         auto copy = [&](uint32_t dst, int part, const __nv_bfloat16* rows, int row) {
-            constexpr int kPerPass = 32 / kChunks;  // rows that 32 chunks make up
             const int c = lane % kChunks;
             const char* const from = reinterpret_cast<const char*>(rows) + c * 16;
             dst += part * 32 * 128;
@@ -922,11 +921,27 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                 for (int sub = 0; sub <= k.pair; ++sub, ++n_q) {
                     const int q = n_q & 1;
                     if (n_q >= 2) wait(&sh.q_empty[q], (n_q >> 1) - 1);
+                    // Only rows that there are (the others' scores are their own), each to all its copies.
+                    const int at0 = w.tile_row + sub * kTile, n_rows = min(w.n_rows - sub * kTile, kTile);
+                    const bool copies = w.log_copies != 0;
 #pragma unroll 1
-                    for (int i = 0; i < 4; ++i) {
-                        const int t_row = (32 * i + lane) & ((kTile >> w.log_copies) - 1), at = w.tile_row + sub * kTile + t_row, qi = at / g;
-                        copy(sQ + q * L::kOperand, i, p.q,
-                             sub * kTile + t_row < w.n_rows ? (w.row0 + qi) * p.hq + w.head * g + (at - qi * g) : kNone);
+                    for (int r0 = 0; r0 < n_rows; r0 += 32) {
+                        const int at = at0 + min(r0 + lane, n_rows - 1), qi = at / g;
+                        const int row = (w.row0 + qi) * p.hq + w.head * g + (at - qi * g);
+                        if (!copies) {
+                            copy(sQ + q * L::kOperand, r0 / 32, p.q, row);
+                            continue;
+                        }
+                        const int c = lane % kChunks;
+                        const char* const from = reinterpret_cast<const char*>(p.q) + c * 16;
+#pragma unroll 1
+                        for (int i = 0; i < n_rows; i += kPerPass) {
+                            const int r = i + lane / kChunks, from_row = __shfl_sync(0xFFFFFFFFu, row, r);
+                            const uint32_t to = sQ + q * L::kOperand + chunk_offset(r, c);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)  // (rows 32 apart have a chunk in the same place)
+                                tc::cp_async_16(to + k * 32 * 128, from + (size_t)from_row * (kD * 2), 16);
+                        }
                     }
                     cp_async_arrive_noinc(&sh.q_full[q]);
                 }
@@ -1343,7 +1358,7 @@ __global__ void __launch_bounds__(kRows) prefix_join_kernel(const AttnParams p, 
         if (own == Where::kSkip || (side && !(own & Where::kShared))) continue;
         const long long at = (side * p.hkv + head) * lins + lin;
         const int w = side ? plan.where[at] : own;
-        if (w & Where::kCut) sum.add_pieces<kD>(plan, w >> 16 & 255, w >> 8 & 255, k, kRows >> log_rows, w & 255, col);
+        if (w & Where::kCut) sum.add_pieces<kD>(plan, w >> 16 & 255, min(w >> 8 & 255, kMaxCtas - 1), k, kRows >> log_rows, w & 255, col);
         else if (k == 0) sum.add(plan.whole_ml[at], reinterpret_cast<const float4*>(plan.whole) + (at - lin) * (kD / 4) + col * lins + lin, lins);
     }
     if (kRows >> log_rows > 1) sum.gather(1 << log_rows);
