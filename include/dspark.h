@@ -614,7 +614,7 @@ size_t dspark_attention_workspace_size(int R, int n_groups, int max_rows, int n_
  * cu_seqlens[R] on are not touched.  cu_seqlens that decreases, does not start at 0 or passes
  * max_rows makes all max_rows rows NaN.  Limits (DSPARK_ERR_UNSUPPORTED): head_dim 64 or 128,
  * at most 128 query heads to a key head, pool_pages * n_kv_heads * page_size < 2^31 - 1,
- * max_rows * n_q_heads < 2^31, q, out and the caches 16-byte aligned.
+ * max_rows * n_q_heads < 2^31, R + n_groups < 2^30, q, out and the caches 16-byte aligned.
  */
 int dspark_verify_attention(const void* q, const void* k_cache, const void* v_cache,
                             const int32_t* block_table, const int32_t* kv_len, const int32_t* cu_seqlens,

@@ -114,7 +114,7 @@ int attention_call(AttnParams& p, size_t ws_bytes, unsigned flags, cudaStream_t 
         return DSPARK_ERR_INVALID_ARG;
     if (p.hq % p.hkv || !(p.scale >= 0.0f) || p.scale == INFINITY || (flags & ~DSPARK_ATTN_FULL_BLOCK)) return DSPARK_ERR_INVALID_ARG;
     if ((p.d != 64 && p.d != 128) || p.hq / p.hkv > 128) return DSPARK_ERR_UNSUPPORTED;
-    if ((long long)p.R + p.n_groups > INT_MAX / 2) return DSPARK_ERR_UNSUPPORTED;  // (counted together, in 32 bits)
+    if ((long long)p.R + p.n_groups > INT_MAX / 2) return DSPARK_ERR_UNSUPPORTED;  // (counted together)
     // rows of the cache are counted in 31 bits
     if ((double)p.pool_pages * p.hkv * p.page >= 2147483647.0 || (long long)p.rows * p.hq >= (1LL << 31)) return DSPARK_ERR_UNSUPPORTED;
     if (!aligned16(p.q) || !aligned16(p.k_cache) || !aligned16(p.v_cache) || !aligned16(p.out)) return DSPARK_ERR_UNSUPPORTED;

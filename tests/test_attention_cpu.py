@@ -105,6 +105,7 @@ def test_prefix_refusals_and_workspace(lib):
     assert call(lib, "dspark_prefix_attention", PRE_T, PRE, group_start=None) == INVALID
     assert call(lib, "dspark_prefix_attention", PRE_T, PRE, shared=None) == INVALID
     assert call(lib, "dspark_prefix_attention", PRE_T, PRE, n_groups=0) == INVALID
+    assert call(lib, "dspark_prefix_attention", PRE_T, PRE, R=1 << 30, n_groups=1 << 30) == UNSUPPORTED
     size = lib.dspark_attention_workspace_size
     size.restype, size.argtypes = ctypes.c_size_t, [i32] * 6
     assert size(4, 0, 9, 8, 2, 128) > 0 and size(4, 2, 9, 8, 2, 128) >= size(4, 0, 9, 8, 2, 128)

@@ -303,6 +303,12 @@ def test_more_groups_than_threads(B):
     check_attention(B, 9, n, kv_len, 16, 4, 2, 64, groups=(list(range(R + 1)), shared))
 
 
+@pytest.mark.parametrize("n,kv_len,page,hq,hkv,d", [([700], [100], 16, 8, 2, 128), ([513, 1, 300], [0, 600, 77], 12, 4, 1, 64)])
+def test_prompts(B, n, kv_len, page, hq, hkv, d):
+    """Many tiles of rows, each of which sees other keys."""
+    check_attention(B, 19, n, kv_len, page, hq, hkv, d)
+
+
 @pytest.mark.parametrize("page", [16, 20])
 @pytest.mark.parametrize("d", [64, 128])
 def test_two_tiles_over_a_long_history(B, page, d):
