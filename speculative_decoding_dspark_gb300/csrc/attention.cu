@@ -38,7 +38,7 @@
 // by 64 elements inside one page.  Other pages may end anywhere in a block: their rows
 // are gathered by 16-byte copies (a row to a lane, the queries' too), which have about
 // 64 KB in flight per SM where TMA has the whole ring.  949 MB of keys and values
-// (2 requests of 115000 keys): 155 us by TMA, 91 % of the copy rate, 200 us gathered;
+// (2 requests of 115000 keys): 148 us by TMA, 94 % of the copy rate, 200 us gathered;
 // four rows to a TMA gather moved 6.4 bytes a cycle (500 us).
 //
 // Up to 32 rows (a few drafted tokens of one key head) lie in the tile four times
@@ -54,13 +54,13 @@
 // only the device knows: every CTA scans them itself.
 //
 // What bounds it: bytes, where few rows read many keys (128 requests of up to 5000,
-// 1296 MB: 206 us, 93 % of the copy rate).  Many rows over the same keys: the way of
+// 1296 MB: 207 us, 92 % of the copy rate).  Many rows over the same keys: the way of
 // a tile from its scores to its next ones, 1350 cycles of exponentials and 1950 of
 // products and their hand-over, in which the other tile's go by too: 1024 of 1665
 // cycles of a step the tensor cores are at work.  Short items: some 9000 cycles from
 // the last product to the output and the next item's first weights.  Small calls:
-// 15000 cycles until the first product, most of them code that comes into the
-// instruction cache while every warp waits for it (92 KB of it; at 180 KB a third of
+// 14000 cycles until the first product, most of them code that comes into the
+// instruction cache while every warp waits for it (90 KB of it; at 180 KB a third of
 // the issue slots waited throughout), and the second launch.
 #include <type_traits>
 
@@ -191,7 +191,7 @@ __device__ __forceinline__ long long divide(long long a, long long b) {
 }
 
 // Units of the line to a CTA (two at least, so that a block begins in each piece of an item; at 3, 4, 6 a request
-// of 777 keys takes 15.9, 16.7, 17.7 us, at 2 15.2).
+// of 777 keys took 15.9, 16.7, 17.7 us, at 2 15.2).
 __device__ __forceinline__ long long piece_length(long long total, int ctas) { return max(divide(total + ctas - 1, ctas), 2LL); }
 
 // What a CTA does of one item: blocks [b0, b1) of it.
