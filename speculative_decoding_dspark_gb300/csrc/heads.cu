@@ -44,6 +44,13 @@ struct RowPlace {
     int pad;
 };
 
+// Shared memory of a CTA besides the rows' turns and the places for rows on their way.
+struct HeadsShared {
+    RowPlace place[kHeadRows];
+    long long pos[kHeadRows];
+    long long steps[DSPARK_HEADS_MAX_D / 2];  // a pair's turn from one position to the next, in 2^-63
+};
+
 // Eight elements as they lie in memory.
 template <typename T> struct Octet;
 template <> struct Octet<float> {
@@ -87,8 +94,7 @@ __global__ void __launch_bounds__(kHeadThreads, 4) heads_kernel(const HeadsParam
     // [kHeadAhead][octet][16-byte part][thread]
     extern __shared__ __align__(16) float turn_smem[];
     constexpr int kParts = Octet<TIn>::kParts;
-    __shared__ RowPlace place[kHeadRows];
-    __shared__ long long pos[kHeadRows], steps[DSPARK_HEADS_MAX_D / 2];
+    __shared__ HeadsShared sh;
     const int half = p.rot / 2;
     const int row0 = blockIdx.x * rows_per_cta;
     const int rows = min(rows_per_cta, p.rows - row0);
@@ -168,20 +174,19 @@ __global__ void __launch_bounds__(kHeadThreads, 4) heads_kernel(const HeadsParam
                 if (at_pos < 0) at.state = 2;
             }
             if (at.state == 2) report(p.dev_status, DSPARK_ERR_DEVICE_INPUT);
-            place[i] = at;
-            pos[i] = at_pos;
+            sh.place[i] = at;
+            sh.pos[i] = at_pos;
         }
     }
-    // a pair's turn from one position to the next, in 2^-63
     for (int f = threadIdx.x; f < half; f += blockDim.x) {
         const double turn = (double)p.inv_freq[f] * 0.15915494309189533577;  // 1 / (2 pi)
         const double part = turn - rint(turn);                                // whole turns leave no trace
-        steps[f] = __double2ll_rn(part * 18446744073709551616.0 * 0.5);
+        sh.steps[f] = __double2ll_rn(part * 18446744073709551616.0 * 0.5);
     }
     __syncthreads();
     for (int j = threadIdx.x; j < rows * half; j += blockDim.x) {
         const int i = j / half, f = j - i * half;
-        const int left = (int)(2 * (unsigned long long)pos[i] * (unsigned long long)steps[f] >> 32);  // of a turn, in 2^-32
+        const int left = (int)(2 * (unsigned long long)sh.pos[i] * (unsigned long long)sh.steps[f] >> 32);  // of a turn, in 2^-32
         float s, c;
         sincospif((float)left * 0x1p-31f, &s, &c);
         turn_smem[2 * i * half + f] = c;
@@ -270,7 +275,7 @@ __global__ void __launch_bounds__(kHeadThreads, 4) heads_kernel(const HeadsParam
                     }
                 }
             }
-            const RowPlace at = place[i];
+            const RowPlace at = sh.place[i];
             if (there && (at.state == 0 || (at.state == 2 && !cached))) {  // (of a bad row nothing goes into the cache)
                 if (at.state == 2) {
 #pragma unroll
@@ -310,7 +315,7 @@ cudaError_t launch_typed(const HeadsParams& p, cudaStream_t stream) {
     void (*const kernel)(const HeadsParams, int, int) =
         p.pairs ? (append ? heads_kernel<TIn, TOut, true, true> : heads_kernel<TIn, TOut, true, false>)
                 : (append ? heads_kernel<TIn, TOut, false, true> : heads_kernel<TIn, TOut, false, false>);
-    if (smem > 48 * 1024) {
+    if (smem + sizeof(HeadsShared) > 48 * 1024) {  // (more than a launch has unasked)
         const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (err != cudaSuccess) return err;
     }
