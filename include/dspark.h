@@ -363,7 +363,10 @@ int dspark_verify_static_scratch(const float* target_logits, const int32_t* cu_s
  * *dev_status, and the CUDA context stays usable.  Outputs of a call that
  * reported DSPARK_ERR_TIMEOUT are invalid (requests decided before the wait
  * ran out may have been written; the others are left untouched).  The waits
- * of a CTA on its own asynchronous copies (mbarriers) keep a fixed 2 s limit.
+ * of a CTA on its own asynchronous copies (mbarriers) keep a fixed 2 s limit,
+ * and so do the waits of the attention kernels' warps on one another: when one
+ * runs out, all warps of that CTA stop (those that run ahead of the others wait
+ * as long as these work), and DSPARK_ERR_TIMEOUT is reported in the same way.
  *
  * dspark_set_wait_limit_ns sets the limit of the grid-wide waits for every
  * later call of this process (0 or anything above 2 s: the default, 2 s) and
@@ -373,11 +376,14 @@ int dspark_verify_static_scratch(const float* target_logits, const int32_t* cu_s
  * DSPARK_INJECT_VERIFY_BARRIER the verify rounds' barriers, with
  * DSPARK_INJECT_DRAFT_BARRIER the draft's position barriers, count one
  * arrival more than the grid has, so that no CTA is ever released and every
- * wait runs out after the limit above.  Returns the previous mask; 0 turns
+ * wait runs out after the limit above; with DSPARK_INJECT_ATTENTION_QUERIES the
+ * attention kernels' queries are never complete, and the wait for them runs out
+ * after 2 s.  Returns the previous mask; 0 turns
  * injection off.  Both settings are read when a call is enqueued.
  */
 #define DSPARK_INJECT_VERIFY_BARRIER 1u
 #define DSPARK_INJECT_DRAFT_BARRIER 2u
+#define DSPARK_INJECT_ATTENTION_QUERIES 4u
 
 uint64_t dspark_set_wait_limit_ns(uint64_t limit_ns);
 unsigned dspark_set_fault_injection(unsigned mask);

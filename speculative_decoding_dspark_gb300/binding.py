@@ -39,7 +39,7 @@ DSPARK_DRAFT_FORCE_SIMT = 1
 DSPARK_VERIFY_HOST_TARGET = 1
 DSPARK_SELECT_FIXED, DSPARK_SELECT_HISTORY, DSPARK_SELECT_CURRENT, DSPARK_SELECT_FIRST_STOP = 0, 1, 2, 3
 DSPARK_SELECT_CONF_CUTOFF, DSPARK_SELECT_SURVIVAL_CUTOFF = 4, 5
-DSPARK_INJECT_VERIFY_BARRIER, DSPARK_INJECT_DRAFT_BARRIER = 1, 2
+DSPARK_INJECT_VERIFY_BARRIER, DSPARK_INJECT_DRAFT_BARRIER, DSPARK_INJECT_ATTENTION_QUERIES = 1, 2, 4
 
 EXPORTED = ["dspark_status_string", "dspark_version", "dspark_workspace_size", "dspark_philox4x32_10",
             "dspark_markov_draft_uses_tensor_cores", "dspark_markov_draft", "dspark_verify",

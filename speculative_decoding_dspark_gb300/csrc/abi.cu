@@ -123,6 +123,7 @@ int attention_call(AttnParams& p, size_t ws_bytes, unsigned flags, cudaStream_t 
     if (need == 0) return DSPARK_ERR_UNSUPPORTED;
     if (ws_bytes < need) return DSPARK_ERR_WORKSPACE;
     p.full_block = (flags & DSPARK_ATTN_FULL_BLOCK) != 0;
+    p.inject = (fault_injection_mask() & DSPARK_INJECT_ATTENTION_QUERIES) != 0;
     return p.rows == 0 ? DSPARK_OK : cuda_status(launch_attention(p, stream));
 }
 
@@ -146,7 +147,7 @@ uint64_t dspark_set_wait_limit_ns(uint64_t limit_ns) {
 }
 
 unsigned dspark_set_fault_injection(unsigned mask) {
-    return g_inject.exchange(mask & (DSPARK_INJECT_VERIFY_BARRIER | DSPARK_INJECT_DRAFT_BARRIER));
+    return g_inject.exchange(mask & (DSPARK_INJECT_VERIFY_BARRIER | DSPARK_INJECT_DRAFT_BARRIER | DSPARK_INJECT_ATTENTION_QUERIES));
 }
 
 const char* dspark_status_string(int status) {

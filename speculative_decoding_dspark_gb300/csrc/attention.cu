@@ -225,21 +225,47 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
     return y;
 }
-// Waits until the phase of `parity` completes, at most 2^20 suspensions of up to 20 us.
-__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity) {
+// Waits until the phase of `parity` completes, at most *limit ns (0 once the CTA is to stop).
+constexpr uint32_t kWaitNs = 2000000000;
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, const volatile uint32_t* limit) {
     uint32_t ok;
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b32 n;\n\tmov.b32 n, 1048576;\n"
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 from, now, most;\n\tmov.u32 from, %%globaltimer_lo;\n"
         "again:\n\t"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
         "@p bra done;\n\t"
-        "sub.u32 n, n, 1;\n\t"
-        "setp.ne.u32 q, n, 0;\n\t"
+        "ld.volatile.shared.u32 most, [%3];\n\t"
+        "mov.u32 now, %%globaltimer_lo;\n\t"
+        "sub.u32 now, now, from;\n\t"
+        "setp.lt.u32 q, now, most;\n\t"
         "@q bra again;\n"
         "done:\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(tc::smem_u32(bar)), "r"(parity)
+        : "r"(tc::smem_u32(bar)), "r"(parity), "r"(tc::smem_u32(const_cast<const uint32_t*>(limit)))
+        : "memory");
+    return ok != 0;
+}
+
+// The same for the warps that run ahead of the products (pieces, queries, values that are looked at): they wait as long as
+// the work on the items before takes, whose own waits have the limit, and give up when one of those has.  (At most 2^24
+// suspensions, a minute or so.)
+__device__ __forceinline__ bool wait_ahead_bounded(uint64_t* bar, uint32_t parity, const volatile uint32_t* limit) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 n, most;\n\tmov.u32 n, 16777216;\n"
+        "again:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+        "@p bra done;\n\t"
+        "ld.volatile.shared.u32 most, [%3];\n\t"
+        "sub.u32 n, n, 1;\n\t"
+        "setp.ne.u32 q, n, 0;\n\t"
+        "setp.ne.and.u32 q, most, 0, q;\n\t"
+        "@q bra again;\n"
+        "done:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(tc::smem_u32(bar)), "r"(parity), "r"(tc::smem_u32(const_cast<const uint32_t*>(limit)))
         : "memory");
     return ok != 0;
 }
@@ -275,7 +301,7 @@ struct Shared {
     Piece pieces[kPieces];
     float2 ml[2][kTile];                   // each tile's m and l of its rows, for the other tile or its own copies
     uint32_t odd[kSteps][4];               // by step: keys of a block whose values are not finite
-    volatile int abort_flag;
+    volatile uint32_t limit, last_limit;   // of the waits, ns (0: one ran out); of the last one
     uint32_t tmem_base;
     long long scan[kThreads / 32];
 };
@@ -333,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
             tc::mbar_init(&sh.empty[lane], 1);
         }
         if (lane < 2) {
-            tc::mbar_init(&sh.q_full[lane], 32);
+            tc::mbar_init(&sh.q_full[lane], 32 + p.inject);
             tc::mbar_init(&sh.q_empty[lane], 2);
             tc::mbar_init(&sh.s_full[lane], 1);
             tc::mbar_init(&sh.p_full[lane], 4);
@@ -347,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         if (lane == 0) {
             tc::mbar_init(&sh.merge, 4);
             tc::mbar_init(&sh.drain, 1);
-            sh.abort_flag = 0;
+            sh.limit = sh.last_limit = kWaitNs;
         }
         tc::fence_barrier_init();
     }
@@ -403,13 +429,21 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         return;
     }
     const float sl2 = fmaxf(p.scale * kLog2e, 1e-37f);  // (a masked score, -inf, weighs nothing at a scale of 0 too)
-    // Waits for the phase of that parity; false (and the CTA stops) when it does not come in some seconds.  (No
-    // function is called: the register split below leaves none for a call's frame.)
+    // Waits for the phase of that parity; false (and the CTA stops) when the limit passes, and from then on at once.  What
+    // is waited for may then be missing: nothing goes out of bounds by it, and what the call writes is not valid.
+    // (No function is called: the register split below leaves none for a call's frame.)
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        const bool ok = wait_bounded(bar, parity & 1);
-        if (!ok) sh.abort_flag = 1;
+        const bool ok = wait_bounded(bar, parity & 1, &sh.limit);
+        if (!ok) sh.limit = 0;
         return ok;
     };
+    auto wait_ahead = [&](uint64_t* bar, uint32_t parity) {
+        const bool ok = wait_ahead_bounded(bar, parity & 1, &sh.limit);
+        if (!ok) sh.limit = 0;
+        return ok;
+    };
+    // The same, one answer for the warp.
+    auto held = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0; };
 
     // Whether the phase is there already.
     auto test = [&](uint64_t* bar, uint32_t parity) {
@@ -441,8 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
             }
         }
     };
-    auto open = [&](Cursor& c) {  // false: there are no more
-        const bool ok = wait(&sh.piece_full[c.i % kPieces], c.i / kPieces);
+    auto read = [&](Cursor& c, bool ok) {  // false: there are no more
         c.at = &sh.pieces[c.i % kPieces];
         // (what a shuffle gives is the same for all lanes, and the compiler keeps it in uniform registers)
         c.steps = __shfl_sync(0xFFFFFFFFu, ok ? c.at->steps : 0, 0);
@@ -451,7 +484,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         c.u = 0;
         return c.steps > 0;
     };
-    auto stopped = [&]() { return __any_sync(0xFFFFFFFFu, sh.abort_flag); };
+    auto open = [&](Cursor& c) { return read(c, wait(&sh.piece_full[c.i % kPieces], c.i / kPieces)); };
+    auto open_ahead = [&](Cursor& c) { return read(c, wait_ahead(&sh.piece_full[c.i % kPieces], c.i / kPieces)); };
+    auto stopped = [&]() { return __any_sync(0xFFFFFFFFu, sh.limit == 0); };
     auto close = [&](Cursor& c) {  // done with the piece; on to the next
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sh.piece_empty[c.i % kPieces]);
@@ -478,11 +513,25 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
             __syncwarp();  // (the barrier counts warps: their lanes have to come together)
             asm volatile("bar.sync %0, 128;" ::"r"(1 + X) : "memory");
         };
+        // Whether all four warps of the tile go on: they meet in tile_sync, which has no limit, the same number of times.
+        auto all_go = [&](bool go) {
+            uint32_t all;
+            __syncwarp();
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\t"
+                "setp.ne.u32 p, %1, 0;\n\t"
+                "bar.red.and.pred q, %2, 128, p;\n\t"
+                "selp.u32 %0, 1, 0, q;\n\t}"
+                : "=r"(all)
+                : "r"((uint32_t)go), "r"(1 + X)
+                : "memory");
+            return all != 0;
+        };
         int n_step = 0;     // steps of this tile so far
         int n_done = 0;     // of them, the ones whose product is waited for
         int n_merge = 0;
         Cursor at;
-        for (; open(at) && !stopped(); close(at), ++at.i) {
+        for (; all_go(open(at) && !stopped()); close(at), ++at.i) {
             const Piece& w = *at.at;
             const int g0 = w.g0, steps = at.steps;
             const int u0 = X ^ (g0 & 1);
@@ -563,9 +612,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                     tc::tmem_st_wait();
                 };
                 // (the scores are formed after the last product with V of this tile: that one is done too)
-                wait(&sh.s_full[X], n_step);
+                if (!held(&sh.s_full[X], n_step)) break;
                 tc::tc_fence_after();
-                __syncwarp();
                 if (warp_live) {
                     const int seen = my_limit - key0;  // keys of the block this row sees
                     if (!__all_sync(0xFFFFFFFFu, seen >= kBlock)) {
@@ -863,7 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                     if (c.block() >= c.at->look) bar = &sh.landed[ring.s];
                 }
                 if ((int)(ring.s & 3) == (warp & 3)) {
-                    if (filled == kSlots) wait(&sh.empty[ring.s], ring.phase ^ 1);
+                    if (filled == kSlots && !held(&sh.empty[ring.s], ring.phase ^ 1)) break;  // (its last fill may be on its way)
                     __syncwarp();  // (what a lane noted of a missing page goes before the arrival)
                     if (lane == 0) tc::mbar_arrive_expect_tx(bar, L::kOperand);
                     __syncwarp();
@@ -915,12 +963,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         if (warp == 15) {
             uint32_t n_q = 0;
 #pragma unroll 1
-            for (; open(k) && !stopped(); close(k), ++k.i) {
+            for (; open_ahead(k) && !stopped(); close(k), ++k.i) {
                 const Piece& w = *k.at;
 #pragma unroll 1
                 for (int sub = 0; sub <= k.pair; ++sub, ++n_q) {
                     const int q = n_q & 1;
-                    if (n_q >= 2) wait(&sh.q_empty[q], (n_q >> 1) - 1);
+                    if (n_q >= 2) wait_ahead(&sh.q_empty[q], (n_q >> 1) - 1);
                     // Only rows that there are (the others' scores are their own), each to all its copies.
                     const int at0 = w.tile_row + sub * kTile, n_rows = min(w.n_rows - sub * kTile, kTile);
                     const bool copies = w.log_copies != 0;
@@ -1008,8 +1056,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         Ring ring;
         uint32_t gv = 0, parity = 0;
         Cursor k, v;
-        bool more = open(k);
-        open(v);
+        bool more = open_ahead(k);
+        open_ahead(v);
 #pragma unroll 1
         for (int i = opaque(-2); v.steps > 0 && !stopped(); ++i) {
             if (i >= 0 && v.leads()) {
@@ -1018,7 +1066,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                     const uint32_t s = ring.s;
                     const int key0 = w.begin + (w.b0 + v.block()) * kBlock;
                     const bool edge = v.block() >= v.edge, past = key0 + kBlock > w.high && maps.box_rows > 0;
-                    wait(&sh.landed[s], parity >> s);
+                    wait_ahead(&sh.landed[s], parity >> s);
                     parity ^= 1u << s;
                     unsigned char* const at = base + (2 + s) * L::kOperand;
                     if (lane < 4) sh.odd[gv % kOddRing][lane] = 0;
@@ -1055,7 +1103,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                 if (k.leads()) ring.next();
                 if (++k.u == k.steps) {
                     ++k.i;
-                    more = open(k);
+                    more = open_ahead(k);
                 }
             }
             if (i >= 0) {
@@ -1063,7 +1111,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                 if (++v.u == v.steps) {
                     close(v);
                     ++v.i;
-                    open(v);
+                    open_ahead(v);
                 }
             }
         }
@@ -1153,12 +1201,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         }
         __syncwarp();
         tc::umma_commit_elect(&sh.drain);
-        wait_bounded(&sh.drain, 0);  // (whatever made the CTA stop, its products are done before tensor memory is given back)
+        wait_bounded(&sh.drain, 0, &sh.last_limit);  // (whatever made the CTA stop, its products are done before tensor memory is given back)
     } else if (warp == 13) {
         // ================================================================ the pieces, one after the other
         int i = 0;
         auto post = [&](const Piece& x) {
-            if (i >= kPieces) wait(&sh.piece_empty[i % kPieces], i / kPieces - 1);
+            if (i >= kPieces && !__all_sync(0xFFFFFFFFu, wait_ahead(&sh.piece_empty[i % kPieces], i / kPieces - 1)))
+                return;  // (others may still read the one before)
             if (lane == 0) {
                 sh.pieces[i % kPieces] = x;
                 tc::mbar_arrive(&sh.piece_full[i % kPieces]);
@@ -1188,7 +1237,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                 int t = h < p.hkv ? (int)min(divide(max(x0 - start, 0LL), en.units(0)), en.tiles - 1LL) : 0;
                 start += (long long)t * en.units(0);
 #pragma unroll 1
-                while (h < p.hkv && start < x1) {
+                while (h < p.hkv && start < x1 && !stopped()) {
                     const int log_steps = en.log_steps(t), round = (1 << log_steps) - 1;
                     const int tile_row = t * kRows, n_rows = min(en.n * g - tile_row, kRows);
                     const int high = en.limit((tile_row + n_rows - 1) / g), n_blocks = (high - en.begin + kBlock - 1) / kBlock;
@@ -1253,7 +1302,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
     }
     __syncwarp();
     __syncthreads();
-    if (sh.abort_flag) {
+    if (sh.limit == 0) {
         if (tid == 0) report(p.dev_status, DSPARK_ERR_TIMEOUT);
         for (const uint64_t t0 = global_ns(); global_ns() - t0 < 1000000;) {}  // (copies in flight land before the CTA ends)
     }

@@ -237,6 +237,7 @@ struct AttnParams {
     float scale;
     int full_block;
     int R, rows, hq, hkv, d, page, max_blocks, pool_pages;
+    int inject;  // 1 (tests): no queries are ever complete
     __nv_bfloat16* out;
     float* lse;
     int32_t* dev_status;
