@@ -295,12 +295,13 @@ struct Shared {
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], p_full[2];         // per tile: scores formed, weights written
     uint64_t o_done[2], o_free[2];         // a product with V is done; the output was read
+    uint64_t odd_done[2];                  // values that are not finite were added: the weights may be written over
     uint64_t merge;                        // the second tile's sums are ready
     uint64_t drain;
     uint64_t piece_full[kPieces], piece_empty[kPieces];
     Piece pieces[kPieces];
     float2 ml[2][kTile];                   // each tile's m and l of its rows, for the other tile or its own copies
-    uint32_t odd[kSteps][4];               // by step: keys of a block whose values are not finite
+    alignas(16) uint32_t odd[kSteps][4];   // by step: keys of a block whose values are not finite
     volatile uint32_t limit, last_limit;   // of the waits, ns (0: one ran out); of the last one
     uint32_t tmem_base;
     long long scan[kThreads / 32];
@@ -365,6 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
             tc::mbar_init(&sh.p_full[lane], 4);
             tc::mbar_init(&sh.o_done[lane], 1);
             tc::mbar_init(&sh.o_free[lane], 4);
+            tc::mbar_init(&sh.odd_done[lane], 4);
         }
         if (lane < kPieces) {
             tc::mbar_init(&sh.piece_full[lane], 1);
@@ -637,13 +639,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                 ++n_step;
                 if ((at.pair ? u >> 1 : u) >= at.edge) {
                     // Some row does not see all of these keys.  Values that are not finite were taken out of the
-                    // block, so that they reach no row through a zero weight; here the rows that do see them get them.
+                    // block, so that they reach no row through a zero weight; here the rows that do see them get them,
+                    // by the weights in tensor memory; until odd_done the tile's next scores are not formed over them.
                     wait(&sh.o_done[X], n_done);
                     if (u + 2 < steps) ++n_done;
                     tc::tc_fence_after();
                     __syncwarp();
                     const uint32_t* odd = sh.odd[(g0 + (at.pair ? u & ~1 : u)) % kOddRing];
-                    if (warp_live && (odd[0] | odd[1] | odd[2] | odd[3])) {
+                    const bool some = (odd[0] | odd[1] | odd[2] | odd[3]) != 0;
+                    if (warp_live && some) {
 #pragma unroll 1
                         for (int key = col0; key < col0 + (1 << log_rows); ++key) {
                             if (!(odd[key >> 5] >> (key & 31) & 1)) continue;
@@ -668,6 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                         }
                     }
                     tc::tc_fence_before();
+                    if (some) arrive(&sh.odd_done[X]);
                 }
             }
             // ---- the triple of this tile's rows
@@ -1127,6 +1132,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         Cursor k, v;
         bool more = open(k);
         open(v);
+        uint32_t odd_phase = 0;              // of odd_done, a bit to a tile
         int owed = 0;             // scores that may be formed
         bool slot_known = false;  // of the next ones' keys
 #pragma unroll 1
@@ -1153,6 +1159,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                                            vd + (uint64_t)(j * (2048 >> 4)), idesc_o, v.u >= 2 || j != 0);
                 if (sub == v.pair) tc::umma_commit_elect(&sh.empty[v_slot]);
                 if (v.u + 2 >= v.steps || v.block() >= v.edge) tc::umma_commit_elect(&sh.o_done[X]);
+                if (v.block() >= v.edge) {
+                    // Weights that values are still to be added by must not be written over by the tile's next scores.
+                    const uint32_t* odd = sh.odd[(gv - sub) % kOddRing];
+                    if (odd[0] | odd[1] | odd[2] | odd[3]) {
+                        wait(&sh.odd_done[X], odd_phase >> X);
+                        odd_phase ^= 1u << X;
+                    }
+                }
                 ++gv;
                 if (++v.u == v.steps) {
                     close(v);
