@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
 
     // A warp's place in the sequence of pieces: piece `i` and step `u` of it.
     struct Cursor {
-        int i = 0, u = 0, steps = 0, pair = 0, edge = 0;
+        int i = 0, u = 0, steps = 0, pair = 0, edge = 0, copies = 0;
         const Piece* at = nullptr;
         __device__ __forceinline__ int block() const { return pair ? u >> 1 : u; }     // from the piece's first on
         __device__ __forceinline__ bool leads() const { return !(u & pair); }          // the step brings a block
@@ -483,6 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         c.steps = __shfl_sync(0xFFFFFFFFu, ok ? c.at->steps : 0, 0);
         c.pair = __shfl_sync(0xFFFFFFFFu, c.at->pair, 0);
         c.edge = __shfl_sync(0xFFFFFFFFu, c.at->edge, 0);
+        c.copies = __shfl_sync(0xFFFFFFFFu, c.at->log_copies, 0);
         c.u = 0;
         return c.steps > 0;
     };
@@ -605,12 +606,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                         tc::tmem_st_32x32b_x16<0>(tS + (col0 + c) / 2, v);
                     }
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                    if constexpr (N < kBlock) {  // the other copies' keys weigh nothing here
-                        const uint32_t zero[16] = {};
-#pragma unroll
-                        for (int c = 0; c < kBlock; c += 32)
-                            if (c < col0 || c >= col0 + N) tc::tmem_st_32x32b_x16<0>(tS + c / 2, zero);
-                    }
                     tc::tmem_st_wait();
                 };
                 // (the scores are formed after the last product with V of this tile: that one is done too)
@@ -1153,10 +1148,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                 tc::tc_fence_after();
                 __syncwarp();
                 const uint64_t vd = tc::smem_desc_sw128_mn(sRing + v_slot * L::kOperand, L::kHalf);
+                // Copies of the rows (32 lanes each) take a quarter of the keys each: the other lanes stay as they are.
+                // (Weights of zero for the other quarters would make an infinite value a NaN.)
+                const uint32_t off = v.copies ? 0xFFFFFFFFu : 0u;
 #pragma unroll
                 for (int j = 0; j < kBlock / 16; ++j)
-                    tc::umma_bf16_ta_elect(tmem + kTmemO + X * kBlock, tmem + X * kBlock + 8 * j,
-                                           vd + (uint64_t)(j * (2048 >> 4)), idesc_o, v.u >= 2 || j != 0);
+                    tc::umma_bf16_ta_lanes_elect(tmem + kTmemO + X * kBlock, tmem + X * kBlock + 8 * j,
+                                                 vd + (uint64_t)(j * (2048 >> 4)), idesc_o,
+                                                 v.u >= 2 || (j & 1) || (j != 0 && !off), j >> 1, off);
                 if (sub == v.pair) tc::umma_commit_elect(&sh.empty[v_slot]);
                 if (v.u + 2 >= v.steps || v.block() >= v.edge) tc::umma_commit_elect(&sh.o_done[X]);
                 if (v.block() >= v.edge) {

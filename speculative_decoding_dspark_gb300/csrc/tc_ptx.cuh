@@ -235,6 +235,19 @@ __device__ __forceinline__ void umma_bf16_ta_elect(uint32_t d_tmem, uint32_t a_t
         : "memory");
 }
 
+// The same; with `off` all ones the lanes of D outside quarter `lanes` (of 32) are left as they are, whatever A has there.
+__device__ __forceinline__ void umma_bf16_ta_lanes_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                                         uint32_t accumulate, int lanes, uint32_t off) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %6, %7, %8}, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lanes == 0 ? 0u : off), "r"(lanes == 1 ? 0u : off),
+        "r"(lanes == 2 ? 0u : off), "r"(lanes == 3 ? 0u : off)
+        : "memory");
+}
+
 // Arrive on `bar` once every tcgen05 operation the elected lane issued so far completes.
 __device__ __forceinline__ void umma_commit_elect(uint64_t* bar) {
     asm volatile(

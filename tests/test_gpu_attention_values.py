@@ -68,3 +68,33 @@ def test_values_of_late_rows(B, requests, n, keys, page, hq, hkv, d, shared):
         for i in sorted({rows[r] - 1 - r % 3, rows[r] // 2, rows[r] // 5}):
             put(vc, table, r, kv_len[r] + i, (7 * r + 5 * i) % d, (INF, -INF, INF, NAN)[(r + i) % 4])
     check(B, case, kv_len, groups=groups)
+
+
+@pytest.mark.parametrize("full", [False, True])
+@pytest.mark.parametrize("n,kv_len,page,hq,hkv,d", [
+    ([1], [300], 16, 8, 2, 128),                     # one token: 4 rows a key head
+    ([8, 1, 3], [900, 130, 5000], 16, 8, 2, 64),     # up to 32 rows, blocks of both tiles, pieces that are joined
+    ([8, 5], [900, 260], 10, 4, 1, 128),
+    ([40, 90], [300, 1000], 16, 4, 1, 64),           # 160 and 360 rows
+    ([9], [700], 12, 4, 1, 128),                     # 36 rows: one tile
+])
+def test_values_that_all_rows_see(B, n, kv_len, page, hq, hkv, d, full):
+    """Infinities and NaN in the history, in keys of every quarter of a block."""
+    case = attention_case(29, n, kv_len, page, hq, hkv, d, peak=1.0)
+    for r in range(len(n)):
+        for pos, channel, x in ((3, 5, INF), (40, 6, -INF), (70, 7, INF), (100, 8, -INF), (kv_len[r] // 128 * 128 - 5, 9, INF),
+                                (64, 10, NAN), (1, 11, INF), (33, 11, -INF)):
+            put(case[2], case[3], r, pos, channel, x)
+    check(B, case, kv_len, full)
+
+
+def test_values_of_a_shared_part(B):
+    n, page, hq, hkv, d = [8, 1, 4, 0, 2], 16, 8, 2, 128
+    kv_len = [512 + 40, 512, 512 + 300, 512, 512 + 7]
+    case = attention_case(30, n, kv_len, page, hq, hkv, d, peak=1.0)
+    groups = ([0, 5], [512])
+    share(case[3], *groups, page)
+    put(case[2], case[3], 0, 17, 3, INF)
+    put(case[2], case[3], 0, 300, 4, -INF)
+    put(case[2], case[3], 2, 520, 5, INF)
+    check(B, case, kv_len, groups=groups)
