@@ -185,9 +185,20 @@ __device__ __forceinline__ Entry entry_of(const AttnParams& p, int e) {
     return x;
 }
 
-// a / b, which is short where both fit 32 bits.
+// a / b for a >= 0, b > 0.  Both fit 32 bits but for more units than the GPU does in half a minute; then bit by bit, which is
+// 3 KB less code than the compiler's 64-bit divisions (code is what short items pay for: see above).
 __device__ __forceinline__ long long divide(long long a, long long b) {
-    return (a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+    if (!((a | b) >> 32)) return (long long)((uint32_t)a / (uint32_t)b);
+    long long q = 0, rest = 0;
+#pragma unroll 1
+    for (int i = 62; i >= 0; --i) {
+        rest = rest << 1 | (a >> i & 1);
+        if (rest >= b) {
+            rest -= b;
+            q |= 1LL << i;
+        }
+    }
+    return q;
 }
 
 // Units of the line to a CTA (two at least, so that a block begins in each piece of an item; at 3, 4, 6 a request
@@ -1233,7 +1244,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
         const long long total = __shfl_sync(0xFFFFFFFFu, upto, 31), length = piece_length(total, max_ctas);
         const long long x0 = min(blockIdx.x * length, total), x1 = min(x0 + length, total);
         Piece x;
-        x.g0 = x.spoiled = x.n_q = 0;
+        x.g0 = x.n_q = 0;
         if (x0 < x1) {
             const int w = __ffs(__ballot_sync(0xFFFFFFFFu, x0 < upto)) - 1;
             const long long before = __shfl_sync(0xFFFFFFFFu, upto - sums, w), end = before + scans[32 * w + lane];
@@ -1280,6 +1291,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                         x.last_cta = 0;
                         if (b0 == 0 && !x.uncut)  // (the last CTA with a piece: every one has `length` units)
                             x.last_cta = blockIdx.x + 1 + (int)divide(first + ((n_blocks - 1) << log_steps) - x1, length);
+                        // A page that only later rows of the request see spoils these rows too.  (One piece of an item does.)
+                        x.spoiled = 0;
+                        if (b0 == 0 && high < en.end) {
+                            bool missing = false;
+#pragma unroll 1
+                            for (int pb = (high - 1) / p.page + 1 + lane; (long long)pb * p.page < en.end; pb += 32) {
+                                const int id = __ldg(p.block_table + (long long)en.table * p.max_blocks + pb);
+                                missing |= id < 0 || id >= p.pool_pages;
+                            }
+                            x.spoiled = __any_sync(0xFFFFFFFFu, missing);
+                            if (x.spoiled) report(p.dev_status, DSPARK_ERR_DEVICE_INPUT);
+                        }
                         post(x);
                         x.g0 += x.steps;
                         x.n_q += 1 + x.pair;
