@@ -48,7 +48,7 @@ struct RowPlace {
 struct HeadsShared {
     RowPlace place[kHeadRows];
     long long pos[kHeadRows];
-    long long steps[DSPARK_HEADS_MAX_D / 2];  // a pair's turn from one position to the next, in 2^-63
+    long long steps[DSPARK_HEADS_MAX_D / 2];  // a pair's turn from one position to the next, in 2^-63 (LLONG_MIN: it has none)
 };
 
 // Eight elements as they lie in memory.
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kHeadThreads, 4) heads_kernel(const HeadsParam
     for (int f = threadIdx.x; f < half; f += blockDim.x) {
         const double turn = (double)p.inv_freq[f] * 0.15915494309189533577;  // 1 / (2 pi)
         const double part = turn - rint(turn);                                // whole turns leave no trace
-        sh.steps[f] = __double2ll_rn(part * 18446744073709551616.0 * 0.5);
+        sh.steps[f] = isnan(part) ? LLONG_MIN : __double2ll_rn(part * 18446744073709551616.0 * 0.5);
     }
     __syncthreads();
     for (int j = threadIdx.x; j < rows * half; j += blockDim.x) {
@@ -189,6 +189,7 @@ __global__ void __launch_bounds__(kHeadThreads, 4) heads_kernel(const HeadsParam
         const int left = (int)(2 * (unsigned long long)sh.pos[i] * (unsigned long long)sh.steps[f] >> 32);  // of a turn, in 2^-32
         float s, c;
         sincospif((float)left * 0x1p-31f, &s, &c);
+        if (sh.steps[f] == LLONG_MIN) s = c = __int_as_float(0x7FC00000);
         turn_smem[2 * i * half + f] = c;
         turn_smem[2 * i * half + half + f] = s;
     }
