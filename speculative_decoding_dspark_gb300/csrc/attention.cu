@@ -658,7 +658,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                         for (int key = col0; key < col0 + (1 << log_rows); ++key) {
                             if (!(odd[key >> 5] >> (key & 31) & 1)) continue;
                             const int pos = key0 + key, pb = pos / p.page;
-                            const int id = p.block_table[(long long)w.table * p.max_blocks + pb];
+                            const int id = IN_BOUNDS(pb < p.max_blocks, p.dev_status) ? p.block_table[(long long)w.table * p.max_blocks + pb] : 0;
+                            if (!IN_BOUNDS(id >= 0 && id < p.pool_pages, p.dev_status)) continue;
                             const __nv_bfloat16* v = p.v_cache + (((size_t)id * p.hkv + w.head) * p.page + (pos - pb * p.page)) * kD;
                             const uint32_t both = tc::tmem_ld_32x32b_x1(tS + key / 2);
                             tc::tmem_ld_wait();
@@ -751,6 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
             float4* const to = reinterpret_cast<float4*>(whole ? plan.whole + part_of * kD : plan.part + slot * kD);
             const size_t to0 = whole ? lin0 : sub * kTile, to_step = whole ? lin_step : kRows;
             const size_t out_row = (size_t)(w.row0 + my_i) * p.hq + w.head * g + (my_r - my_i * g);
+            const bool writes = live && IN_BOUNDS(w.row0 >= 0 && my_i >= 0 && w.head < p.hkv && out_row < (size_t)p.rows * p.hq, p.dev_status);
             auto sums = [&](int c, float (&o)[16]) {  // 16 columns of this lane's row, of both tiles
                 float o2[16];
                 tc::tmem_ld_32x32b_x16<0>(tO + c, o);
@@ -776,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                 for (int c = 0; c < kD; c += 16) {
                     float o[16];
                     sums(c, o);
-                    if (live) {
+                    if (writes) {
                         uint2 b[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -824,19 +826,20 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                             const int r = my_r0 + i * kApart;
                             if (r < n_rows) {
                                 const int at_row = __float_as_int(sh.ml[X][r].x);
+                                if (!IN_BOUNDS(at_row >= 0 && at_row / p.hq < p.rows, p.dev_status)) continue;
                                 *reinterpret_cast<uint2*>(p.out + (size_t)at_row * kD + c0 + 4 * my_q) = pack(sum_of(my_q, r));
                             }
                         }
                     } else {  // a column's rows
 #pragma unroll 1
-                        for (int q = t128 >> log_rows; q < kQuads && live; q += 1 << log_copies)
+                        for (int q = t128 >> log_rows; q < kQuads && writes; q += 1 << log_copies)
                             to[(size_t)(c0 / 4 + q) * to_step + to0 + t_row] = sum_of(q, t_row);
                     }
                     tile_sync();
                 }
                 if (t128 == 0) tc::mbar_arrive(&sh.q_empty[w.n_q & 1]);
             }
-            if (live && t128 == t_row) {
+            if (writes && t128 == t_row) {
                 if (!final) (whole ? plan.whole_ml + part_of : plan.part_ml + slot)[to0 + t_row] = make_float2(m, l);
                 else if (p.lse) p.lse[out_row] = (m + log2f(l)) * kLn2;
                 if (kPrefix && w.b0 == 0)
@@ -882,7 +885,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
             table = p.block_table + (long long)w.table * p.max_blocks;
             high = w.high;
             head = w.head;
-            if (pos < high) id = __ldg(table + page);
+            if (pos < high) id = IN_BOUNDS(page < p.max_blocks, p.dev_status) ? __ldg(table + page) : -1;
         };
         open_k();
         open(v);
@@ -898,7 +901,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                 if (is_k) {
                     row = none;
                     if (pos < high) {
-                        if (id >= 0 && id < p.pool_pages) {
+                        if (id >= 0 && id < p.pool_pages && IN_BOUNDS(head < p.hkv && slot >= 0 && slot < p.page, p.dev_status)) {
                             row = (id * p.hkv + head) * p.page + slot;
                         } else {
                             sh.pieces[k.i % kPieces].spoiled = 1;
@@ -915,7 +918,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
                         slot -= p.page;
                         ++page;
                     }
-                    if (pos < high) id = __ldg(table + page);
+                    if (pos < high) id = IN_BOUNDS(page < p.max_blocks, p.dev_status) ? __ldg(table + page) : -1;
                 } else {
                     kept0 = kept1;
                     --n_kept;
@@ -955,6 +958,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
             const int pos = first_key(c) + part * 32 + lane;
             if (pos >= w.high) return kNone;
             const int pb = pos / p.page;
+            if (!IN_BOUNDS(w.table < p.R && pb < p.max_blocks && w.head < p.hkv, p.dev_status)) return kMissing;
             const int id = __ldg(p.block_table + (long long)w.table * p.max_blocks + pb);
             if (id < 0 || id >= p.pool_pages) return kMissing;
             return (id * p.hkv + w.head) * p.page + (pos - pb * p.page);
@@ -986,7 +990,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const AttnParams
 #pragma unroll 1
                     for (int r0 = 0; r0 < n_rows; r0 += 32) {
                         const int at = at0 + min(r0 + lane, n_rows - 1), qi = at / g;
-                        const int row = (w.row0 + qi) * p.hq + w.head * g + (at - qi * g);
+                        int row = (w.row0 + qi) * p.hq + w.head * g + (at - qi * g);
+                        if (!IN_BOUNDS(row >= 0 && row / p.hq < p.rows, p.dev_status)) row = 0;
                         if (!copies) {
                             copy(sQ + q * L::kOperand, r0 / 32, p.q, row);
                             continue;
@@ -1368,9 +1373,9 @@ struct RowSum {
     }
     // Row r of the item that CTAs first .. last have pieces of: the k-th of them and every n-th from there on.
     template <int kD>
-    __device__ __forceinline__ void add_pieces(const Plan& plan, int first, int last, int k, int n, int r, int col) {
+    __device__ __forceinline__ void add_pieces(const Plan& plan, int first, int last, int k, int n, int r, int col, int32_t* dev_status) {
 #pragma unroll 4
-        for (int c = first + k; c <= last; c += n) {
+        for (int c = first + k; c <= last && IN_BOUNDS(c >= 0 && c < kMaxCtas && r >= 0 && r < kRows, dev_status); c += n) {
             const size_t slot = (size_t)(2 * c + (c == first)) * kRows;
             add(plan.part_ml[slot + r], reinterpret_cast<const float4*>(plan.part + slot * kD) + col * kRows + r, kRows);
         }
@@ -1389,6 +1394,7 @@ struct RowSum {
     }
     template <int kD>
     __device__ __forceinline__ void write(const AttnParams& p, size_t row, int col) const {
+        if (!IN_BOUNDS(row < (size_t)p.rows * p.hq && col * 4 < p.d, p.dev_status)) return;
         const float inv = 1.0f / l;
         alignas(16) __nv_bfloat162 w[2 * kQuads];
 #pragma unroll
@@ -1419,7 +1425,7 @@ __global__ void __launch_bounds__(kRows) join_kernel(const AttnParams p, const P
     while (1 << log_rows < job.n_rows) ++log_rows;
     const int r = threadIdx.x & ((1 << log_rows) - 1), g = p.hq / p.hkv, col = blockIdx.y * RowSum::kQuads;
     RowSum sum;
-    if (r < job.n_rows) sum.add_pieces<kD>(plan, job.first, job.last, threadIdx.x >> log_rows, kRows >> log_rows, r, col);
+    if (r < job.n_rows) sum.add_pieces<kD>(plan, job.first, job.last, threadIdx.x >> log_rows, kRows >> log_rows, r, col, p.dev_status);
     if (share) sum.gather(1 << log_rows);
     if ((int)threadIdx.x >= job.n_rows) return;
     const int i = (job.tile_row + r) / g;
@@ -1443,7 +1449,7 @@ __global__ void __launch_bounds__(kRows) prefix_join_kernel(const AttnParams p, 
         if (own == Where::kSkip || (side && !(own & Where::kShared))) continue;
         const long long at = (side * p.hkv + head) * lins + lin;
         const int w = side ? plan.where[at] : own;
-        if (w & Where::kCut) sum.add_pieces<kD>(plan, w >> 16 & 255, min(w >> 8 & 255, kMaxCtas - 1), k, kRows >> log_rows, w & 255, col);
+        if (w & Where::kCut) sum.add_pieces<kD>(plan, w >> 16 & 255, min(w >> 8 & 255, kMaxCtas - 1), k, kRows >> log_rows, w & 255, col, p.dev_status);
         else if (k == 0) sum.add(plan.whole_ml[at], reinterpret_cast<const float4*>(plan.whole) + (at - lin) * (kD / 4) + col * lins + lin, lins);
     }
     if (kRows >> log_rows > 1) sum.gather(1 << log_rows);

@@ -116,7 +116,7 @@ __device__ __forceinline__ void report(int32_t* dev_status, int code) {
 // reports DSPARK_ERR_BOUNDS when cond fails, so that the guarded access can be
 // skipped instead of faulting; in a normal build it is `true` and costs nothing.
 // The checks cover indices computed inside the kernels (decoded tokens, rows
-// of the packed target, statistics and workspace slots, pages); the inputs the
+// of the packed target and of queries, statistics and workspace slots, pages); the inputs the
 // pages define (token ids < V, cu_seqlens monotone, l <= gamma) are checked in
 // every build.
 #ifdef DSPARK_DEBUG

@@ -277,7 +277,10 @@ __global__ void __launch_bounds__(kHeadThreads, 4) heads_kernel(const HeadsParam
                 }
             }
             const RowPlace at = sh.place[i];
-            if (there && (at.state == 0 || (at.state == 2 && !cached))) {  // (of a bad row nothing goes into the cache)
+            const bool inside = IN_BOUNDS(row0 + i < p.rows && (!cached || at.state != 0 ||
+                                                                (at.at >= 0 && at.at < ((p.pool_pages - 1LL) * p.hkv + 1) * p.page * p.d)),
+                                          p.dev_status);
+            if (inside && there && (at.state == 0 || (at.state == 2 && !cached))) {  // (of a bad row nothing goes into the cache)
                 if (at.state == 2) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[e] = make_float2(__int_as_float(0x7FC00000), __int_as_float(0x7FC00000));
