@@ -607,6 +607,8 @@ size_t dspark_attention_workspace_size(int R, int n_groups, int max_rows, int n_
  * DSPARK_ATTN_FULL_BLOCK: j < kv_len[r] + n, for a drafter whose block positions
  * see each other both ways):
  *   s_j = scale * q . K[j] (scale >= 0),  lse = log sum_j exp(s_j),  out = sum_j exp(s_j - lse) V[j]
+ * Scores, lse and all sums are fp32.  Each weight is rounded to bf16 before its product with V (by at most 2^-8 of
+ * it; lse adds the unrounded ones), and out once at the end.
  * What lies in the pages past a request's last position, and what a row does not
  * see, has no influence on it, NaN and infinities among it.
  *

@@ -38,17 +38,26 @@
 // by 64 elements inside one page.  Other pages may end anywhere in a block: their rows
 // are gathered by 16-byte copies (a row to a lane, the queries' too), which have about
 // 64 KB in flight per SM where TMA has the whole ring.  949 MB of keys and values
-// (2 requests of 115000 keys): 148 us by TMA, 94 % of the copy rate, 200 us gathered;
+// (2 requests of 115000 keys): 150 us by TMA, 93 % of the copy rate, 200 us gathered;
 // four rows to a TMA gather moved 6.4 bytes a cycle (500 us).
 //
 // Up to 32 rows (a few drafted tokens of one key head) lie in the tile four times
 // and each copy takes a quarter of a block's keys: all four warps form exponentials
-// then, 720 cycles for a block instead of 1350.
+// then, 720 cycles for a block instead of 1350.  The product with V of a quarter's keys
+// leaves the other copies' lanes alone.
+//
+// Values that are not finite: a weight of zero times one of them would be a NaN in rows
+// that do not see it.  In a block that not all rows see whole such keys are taken out
+// before the product and added by hand, by the weights in tensor memory, to the rows
+// that see them; until then the issuing warp does not let the tile's next scores lie
+// over the weights.
 //
 // Splitting: the steps of all items form one line, which is cut into equal
 // pieces, one per CTA (each item costs some steps more, for its queries and
-// output).  An item that is cut leaves its triples in the workspace and a second
-// kernel joins them in a fixed order.  With shared pages the groups' items (their
+// output).  Each is charged its request's keys, so a prompt's early items, which see
+// fewer, are less than their share: 8192 rows without history take 853 us (floor 290).
+// An item that is cut leaves its triples in the workspace and a second kernel joins
+// them in a fixed order.  With shared pages the groups' items (their
 // keys, the rows of all their requests) and the requests' own go into the same line,
 // and the second kernel adds each row's parts.  The cut depends on the lengths, which
 // only the device knows: every CTA scans them itself.
@@ -60,8 +69,9 @@
 // cycles of a step the tensor cores are at work.  Short items: some 9000 cycles from
 // the last product to the output and the next item's first weights.  Small calls:
 // 14000 cycles until the first product, most of them code that comes into the
-// instruction cache while every warp waits for it (90 KB of it; at 180 KB a third of
-// the issue slots waited throughout), and the second launch.
+// instruction cache while every warp waits for it (95 KB of it; at 180 KB a third of
+// the issue slots waited throughout, and waits that took 10 KB more made 128 short
+// requests behind a shared prefix a fifth slower), and the second launch.
 #include <type_traits>
 
 #include "kernels.cuh"
@@ -75,9 +85,9 @@ constexpr int kLoaders = 128;
 constexpr int kTile = 128;   // rows of a tile
 constexpr int kRows = 256;   // rows of an item
 constexpr int kBlock = 128;  // keys of a block
-// Steps that an item costs besides its own.  2, 3, 4, 5: 205, 207, 209, 210 us for 128 long ragged requests, 139, 129,
-// 134, 141 us for 128 short ones behind a shared prefix of 8192, 30, 32, 33, 35 us for 103 single rows behind shared
-// prefixes of up to 6944.
+// Steps that an item costs besides its own.  At 2, 3, 4, 5: 205, 206, 208, 210 us for 128 long ragged requests, 143, 141,
+// 146, 151 for 128 short ones behind a shared prefix of 8192 keys, 74, 77, 81, 86 behind one of 2048, 59.2, 58.5, 59.2, 60.3
+// for 48 blocks of 17 rows: 2 and 3 are within 4 % of each other either way.
 constexpr int kItemCost = 3;
 constexpr int kMaxCtas = 152;            // one per SM
 constexpr int kMaxKeys = INT_MAX - 4 * kBlock;  // (loads look up to two blocks past the last key)
@@ -1528,8 +1538,9 @@ cudaError_t launch_as(const AttnParams& p, cudaStream_t stream) {
                             kPrefix ? p.n_groups + p.R : p.R, maps)) != cudaSuccess)
         return err;
     if (!kPrefix) return launch_after(join_kernel<kD>, dim3(ctas, kD / kJoinCols), kRows, 0, stream, p, plan);
-    // Few rows are few items in many pieces: eight threads to a row (2500 rows of a key head: 22 us instead of 26; 18000
-    // rows: 168 instead of 147).
+    // Few rows are few items in many pieces: eight threads to a row up to 4096 rows of all heads.  Eight threads, one: 27 and
+    // 33 us at 1900 rows (of 32 query heads behind a prefix of 4096), 36.8 and 38.1 at 3500, 42.4 and 42.7 at 4700, 56 and 54
+    // at 7800, 79 and 71 at 11600.
     const long long lins = (long long)p.rows * (p.hq / p.hkv);
     const int log_rows = lins * p.hkv <= 16 * kRows ? 5 : 8;
     const long long blocks = ((lins + (1 << log_rows) - 1) >> log_rows) * p.hkv;
