@@ -25,6 +25,10 @@
  * out, and attention over those pages, with or without a prefix that several
  * requests share.
  *
+ * Beside the cycle, from the same rows: log probabilities of the emitted tokens
+ * with their alternatives, and the learning step of a drafter (the loss against
+ * the target's top tokens, the gradients of its logits and Markov factors).
+ *
  * Conventions shared by every call:
  *   - Every array argument is a DEVICE pointer owned by the caller; the
  *     library allocates no memory and keeps no state between calls (apart
@@ -94,10 +98,20 @@ typedef struct CUstream_st* dspark_stream_t;
 #define DSPARK_OP_VERIFY_MARKOV 3
 #define DSPARK_OP_CALIBRATE 4
 #define DSPARK_OP_DRAFT_FUSED 5
+#define DSPARK_OP_MARKOV_GRAD 6
 
 /* ---- flags of the attention step -------------------------------------------- */
 #define DSPARK_ROPE_INTERLEAVED 1u  /* rotate the pairs (2f, 2f + 1) instead of (f, f + rot / 2) */
 #define DSPARK_ATTN_FULL_BLOCK 1u   /* every row of a request sees all of its rows           */
+
+/* ---- flags of the learning step ----------------------------------------------- */
+#define DSPARK_DISTILL_REST 1u      /* tokens that are not listed are one more class    */
+#define DSPARK_GRAD_ACCUMULATE 1u   /* add to dW1 and dW2 instead of writing them        */
+
+/* Most alternatives of dspark_token_logprobs and listed tokens of dspark_distill_loss,
+ * and the longest row (V) of either. */
+#define DSPARK_TOP_MAX 128
+#define DSPARK_ROWS_MAX_V 4194304
 
 /* Largest head dspark_qk_norm_rope and dspark_kv_append take. */
 #define DSPARK_HEADS_MAX_D 256
@@ -136,13 +150,15 @@ const char* dspark_status_string(int status);
  * conf_min in dspark_select_prefix, dspark_plan_cycles, the wait settings,
  * dspark_fit_temperatures, dspark_kv_reserve and dspark_kv_commit; 1.2.0:
  * dspark_markov_draft_fused; 1.3.0: dspark_qk_norm_rope, dspark_kv_append,
- * dspark_verify_attention, dspark_prefix_attention). */
+ * dspark_verify_attention, dspark_prefix_attention; 1.4.0: dspark_token_logprobs,
+ * dspark_distill_loss, dspark_markov_grad). */
 int dspark_version(void);
 
 /* Bytes of workspace one call of `op` needs for these sizes (0 on bad
  * arguments).  For DSPARK_OP_DRAFT pass the weights' element type and the
- * draft flags; for DSPARK_OP_VERIFY, max_rows bounds cu_seqlens[R]; other
- * arguments may be 0 where unused. */
+ * draft flags; for DSPARK_OP_VERIFY, max_rows bounds cu_seqlens[R]; for
+ * DSPARK_OP_MARKOV_GRAD max_rows is the rows of the gradient; other arguments may
+ * be 0 where unused. */
 size_t dspark_workspace_size(int op, int R, int gamma, int V, int rank, int max_rows,
                              int w_dtype, unsigned flags);
 
@@ -655,6 +671,108 @@ int dspark_prefix_attention(const void* q, const void* k_cache, const void* v_ca
                             int head_dim, int page_size, int max_blocks, int pool_pages, void* out,
                             float* lse, unsigned flags, void* ws, size_t ws_bytes, int32_t* dev_status,
                             dspark_stream_t stream);
+
+/*
+ * dspark_token_logprobs -- log probabilities of given tokens, entropy and top
+ * alternatives of vocabulary rows: what a server answers beside the tokens a
+ * verify emitted (out_tokens of dspark_verify as it is), the score of a prompt,
+ * or a teacher's top tokens for dspark_distill_loss.
+ *
+ * For each row x of V logits, with t = x * invT, invT = 1.0f / temperature:
+ *   lse = log sum_v exp(t_v)      entropy = -sum_v p_v log p_v,  p = exp(t - lse)
+ *   logprob = t[token] - lse
+ *   top_ids, top_logprobs: the top_k tokens of largest x (not t: of equal x the lowest
+ *     id first, -0 and 0 are equal) and their t - lse, best first.  A token whose x is
+ *     -inf is not listed; places that no token fills hold id -1 and -inf.
+ * Sums are fp32 (differences from the row's maximum); -inf logits have probability 0.
+ *
+ *   logits       [rows, V] dtype (F32 or BF16), row_stride elements from row to row
+ *   tokens       cu_seqlens NULL: [rows] int32, or NULL: every row, no token asked for.
+ *                cu_seqlens given ([R + 1] int32, from 0, non-decreasing, up to rows): [R, width]
+ *                int32; row cu_seqlens[r] + j has token tokens[r][j] (j >= width: none), rows
+ *                from cu_seqlens[R] on are not touched
+ *   logprob [rows] fp32 out (NULL iff tokens is NULL; 0 where no token was asked for)
+ *   lse, entropy [rows] fp32 out or NULL
+ *   top_ids [rows, top_k] int32, top_logprobs [rows, top_k] fp32 out (both NULL iff top_k == 0)
+ * A row whose token is negative is not read: its logprob, lse and entropy are 0, its list is
+ * empty.  A token >= V, a row that holds a NaN or +inf, and one that holds -inf alone get NaN
+ * (ids -1) and are reported (DSPARK_ERR_DEVICE_INPUT).  A request whose cu_seqlens entries
+ * break the rules above is reported and its rows are not touched.  No workspace; the same call
+ * gives the same results.  Limits: temperature > 0 with a finite invT *
+ * log2(e); top_k <= DSPARK_TOP_MAX and V <= DSPARK_ROWS_MAX_V (else
+ * DSPARK_ERR_UNSUPPORTED, as for 2^27 rows or R * width and more).
+ */
+int dspark_token_logprobs(const void* logits, int64_t row_stride, int dtype, const int32_t* tokens,
+                          const int32_t* cu_seqlens, int R, int width, float temperature, int rows,
+                          int V, int top_k, float* logprob, float* lse, float* entropy,
+                          int32_t* top_ids, float* top_logprobs, int32_t* dev_status,
+                          dspark_stream_t stream);
+
+/*
+ * dspark_distill_loss -- a drafter's rows held to a teacher's top tokens: the
+ * loss of each row and, if asked for, the gradient of the drafter's logits.
+ *
+ * With t = student * invT, q = softmax(t) over the row, and the row's listed tokens k
+ * (teacher_ids[n][k] >= 0; negative ids are places without a token):
+ *   p_k = exp(value_k) / sum_j exp(value_j),  value = teacher_logprobs[n]
+ *     (log probabilities or logits, at the loss's temperature),
+ *   L = sum_k p_k (log p_k - log q_k),   dL/dt_v = q_v - p_v
+ * and with DSPARK_DISTILL_REST, where the tokens that are not listed are a class of their own,
+ *   p_k = exp(value_k) (log probabilities over the whole vocabulary, as dspark_token_logprobs
+ *     gives them),  p_rest = max(0, 1 - sum p_k), q_rest = sum of q over tokens not listed
+ *     (p_rest = 0 where no such token has a logit above -inf),
+ *   L = sum_k p_k (log p_k - log q_k) + p_rest (log p_rest - log q_rest),
+ *   dL/dt_v = q_v M - p_v (listed), q_v M - p_rest q_v / q_rest (not listed), M = sum p_k + p_rest.
+ * A class of p = 0 adds nothing.  loss[n] = w L and grad[n] = w invT dL/dt, w = row_weight[n]:
+ * the weight of the row in the sum that is minimised (or the gradient of its loss, when called
+ * from a backward pass).  A row of weight 0 is not read (loss and gradient 0); without a listed
+ * token a row has loss and gradient 0.
+ *
+ *   student      [rows, V] student_dtype (F32 or BF16), student_stride elements from row to row
+ *                (for instance dspark_markov_draft's q_logits, which are scaled already: temperature 1)
+ *   teacher_ids [rows, top_k] int32, teacher_logprobs [rows, top_k] fp32, 1 <= top_k <= DSPARK_TOP_MAX
+ *   row_weight   [rows] fp32, or NULL: all 1
+ *   loss         [rows] fp32 out
+ *   grad         [rows, V] grad_dtype with grad_stride, out, rounded once, or NULL: the loss alone
+ *                (grad_dtype and grad_stride are then ignored).  It may be student itself (same pointer, type and
+ *                stride), else the two must not overlap.
+ * A row gets NaN for its loss and gradient and is reported (DSPARK_ERR_DEVICE_INPUT) if an id is >= V or
+ * listed twice, a value or its logits hold a NaN or +inf, all its logits are -inf, or its weight is not
+ * finite (or, with DSPARK_DISTILL_REST, sum p_k is not).  No workspace.  Limits as dspark_token_logprobs.
+ */
+int dspark_distill_loss(const void* student, int64_t student_stride, int student_dtype,
+                        const int32_t* teacher_ids, const float* teacher_logprobs, int top_k,
+                        const float* row_weight, float temperature, int rows, int V, float* loss,
+                        void* grad, int64_t grad_stride, int grad_dtype, unsigned flags,
+                        int32_t* dev_status, dspark_stream_t stream);
+
+/*
+ * dspark_markov_grad -- gradients of the Markov factors, the backward pass of
+ * logits[n] = U[n] + W2 . W1[prev[n]] (the drafter's logits of dspark_markov_draft;
+ * U's gradient is the logits').
+ *
+ *   grad_prev[n] = sum_v grad[n][v] W2[v]
+ *   dW1[a]       = sum of grad_prev[n] over the rows with prev[n] = a, in row order,
+ *                  for the tokens a that occur; its other rows are not touched
+ *   dW2[v]       = sum_n grad[n][v] W1[prev[n]]
+ * or, with DSPARK_GRAD_ACCUMULATE, these sums added to dW1 and dW2.  A row with prev < 0 has no
+ * bias: it gives nothing and its grad_prev is 0.  Products of bf16 values are exact, sums fp32 in
+ * an order that the sizes alone decide.
+ *
+ *   grad         [rows, V] bf16, grad_stride elements from row to row (dspark_distill_loss's grad)
+ *   prev         [rows] int32, the token before each row: the anchor, then the drafted ones
+ *   W1, W2       [V, rank] bf16
+ *   grad_prev    [rows, rank] fp32 out;  dW1, dW2 [V, rank] fp32, or NULL: not wanted
+ *   ws, ws_bytes dspark_workspace_size(DSPARK_OP_MARKOV_GRAD, 0, 0, V, rank, rows, DSPARK_BF16, 0)
+ * A row with prev >= V is reported (DSPARK_ERR_DEVICE_INPUT), gives nothing to dW1 and dW2, and
+ * its grad_prev is NaN.  rows == 0 gives zeros (dW2) without DSPARK_GRAD_ACCUMULATE.
+ * Limits (DSPARK_ERR_UNSUPPORTED): rank % 64 == 0 up to 512, V % 8 == 0, rows < 2^24; grad, W1, W2, grad_prev, dW1
+ * and dW2 16-byte aligned, grad_stride a multiple of 8.
+ */
+int dspark_markov_grad(const void* grad, int64_t grad_stride, const int32_t* prev, const void* W1,
+                       const void* W2, int rows, int V, int rank, float* grad_prev, float* dW1,
+                       float* dW2, unsigned flags, void* ws, size_t ws_bytes, int32_t* dev_status,
+                       dspark_stream_t stream);
 
 /*
  * dspark_commit_lengths -- per-request commit and rollback counts

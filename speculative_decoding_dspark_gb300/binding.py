@@ -31,6 +31,11 @@ DSPARK_ERR_BOUNDS = -8
 DSPARK_F32, DSPARK_BF16 = 0, 1
 DSPARK_OP_DRAFT, DSPARK_OP_VERIFY, DSPARK_OP_SELECT, DSPARK_OP_VERIFY_MARKOV, DSPARK_OP_CALIBRATE = 0, 1, 2, 3, 4
 DSPARK_OP_DRAFT_FUSED = 5
+DSPARK_OP_MARKOV_GRAD = 6
+DSPARK_DISTILL_REST = 1
+DSPARK_GRAD_ACCUMULATE = 1
+DSPARK_TOP_MAX = 128
+DSPARK_ROWS_MAX_V = 1 << 22
 DSPARK_FUSED_MAX_D = 16384
 DSPARK_HEADS_MAX_D = 256
 DSPARK_ROPE_INTERLEAVED = 1
@@ -47,7 +52,8 @@ EXPORTED = ["dspark_status_string", "dspark_version", "dspark_workspace_size", "
             "dspark_verify_markov", "dspark_set_wait_limit_ns", "dspark_set_fault_injection",
             "dspark_plan_cycles", "dspark_fit_temperatures", "dspark_kv_reserve", "dspark_kv_commit",
             "dspark_markov_draft_fused", "dspark_qk_norm_rope", "dspark_kv_append",
-            "dspark_attention_workspace_size", "dspark_verify_attention", "dspark_prefix_attention"]
+            "dspark_attention_workspace_size", "dspark_verify_attention", "dspark_prefix_attention",
+            "dspark_token_logprobs", "dspark_distill_loss", "dspark_markov_grad"]
 
 
 class DSparkError(RuntimeError):
@@ -113,6 +119,12 @@ def _load():
     L.dspark_verify_attention.restype = i32
     L.dspark_prefix_attention.argtypes = [vp] * 8 + [i32, f32] + [i32] * 8 + [vp, vp, u, vp, sz, vp, vp]
     L.dspark_prefix_attention.restype = i32
+    L.dspark_token_logprobs.argtypes = [vp, i64, i32, vp, vp, i32, i32, f32, i32, i32, i32] + [vp] * 7
+    L.dspark_token_logprobs.restype = i32
+    L.dspark_distill_loss.argtypes = [vp, i64, i32, vp, vp, i32, vp, f32, i32, i32, vp, vp, i64, i32, u, vp, vp]
+    L.dspark_distill_loss.restype = i32
+    L.dspark_markov_grad.argtypes = [vp, i64, vp, vp, vp, i32, i32, i32, vp, vp, vp, u, vp, sz, vp, vp]
+    L.dspark_markov_grad.restype = i32
     L.dspark_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
     L.dspark_set_wait_limit_ns.restype = ctypes.c_uint64
     L.dspark_set_fault_injection.argtypes = [ctypes.c_uint]
@@ -541,6 +553,91 @@ def dspark_prefix_attention(q, k_cache, v_cache, block_table, kv_len, cu_seqlens
                                     *sizes, _ptr(out), _ptr(lse), DSPARK_ATTN_FULL_BLOCK if full_block else 0,
                                     _ptr(ws), ws.numel(), _ptr(dev_status), _stream(stream))
     _raise("dspark_prefix_attention", st)
+
+
+def _vocab_rows(t, name, dtype=None, shape=None):
+    """A [rows, V] tensor whose rows may lie apart; the elements from row to row."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must have shape {shape or '[rows, V]'}, got {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    rows, V = t.shape
+    if V > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.stride(0) if rows > 1 else V
+
+
+def dspark_token_logprobs(logits, tokens, temperature, logprob, lse=None, entropy=None, top_ids=None,
+                          top_logprobs=None, cu_seqlens=None, dev_status=None, stream=None):
+    stride = _vocab_rows(logits, "logits")
+    rows, V = logits.shape
+    R = width = 0
+    if cu_seqlens is not None:
+        if tokens is None or tokens.dim() != 2:
+            raise ValueError("tokens must have shape [R, width] beside cu_seqlens")
+        R, width = tokens.shape
+        _check(cu_seqlens, "cu_seqlens", torch.int32, (R + 1,))
+    _check(tokens, "tokens", torch.int32, None if cu_seqlens is not None else (rows,), allow_none=True)
+    _check(logprob, "logprob", torch.float32, (rows,), allow_none=tokens is None)
+    _check(lse, "lse", torch.float32, (rows,), allow_none=True)
+    _check(entropy, "entropy", torch.float32, (rows,), allow_none=True)
+    if (top_ids is None) != (top_logprobs is None):
+        raise ValueError("top_ids and top_logprobs go together")
+    top_k = 0
+    if top_ids is not None:
+        if top_ids.dim() != 2:
+            raise ValueError("top_ids must have shape [rows, top_k]")
+        top_k = top_ids.shape[1]
+        _check(top_ids, "top_ids", torch.int32, (rows, top_k))
+        _check(top_logprobs, "top_logprobs", torch.float32, (rows, top_k))
+    _check(dev_status, "dev_status", torch.int32, allow_none=True)
+    st = _L.dspark_token_logprobs(_ptr(logits), stride, _dtype_code(logits), _ptr(tokens), _ptr(cu_seqlens), R, width,
+                                  float(temperature), rows, V, top_k, _ptr(logprob), _ptr(lse), _ptr(entropy),
+                                  _ptr(top_ids), _ptr(top_logprobs), _ptr(dev_status), _stream(stream))
+    _raise("dspark_token_logprobs", st)
+
+
+def dspark_distill_loss(student, teacher_ids, teacher_logprobs, temperature, loss, grad=None, row_weight=None,
+                        rest=False, dev_status=None, stream=None):
+    stride = _vocab_rows(student, "student")
+    rows, V = student.shape
+    if teacher_ids is None or teacher_ids.dim() != 2:
+        raise ValueError("teacher_ids must have shape [rows, top_k]")
+    top_k = teacher_ids.shape[1]
+    _check(teacher_ids, "teacher_ids", torch.int32, (rows, top_k))
+    _check(teacher_logprobs, "teacher_logprobs", torch.float32, (rows, top_k))
+    _check(row_weight, "row_weight", torch.float32, (rows,), allow_none=True)
+    _check(loss, "loss", torch.float32, (rows,))
+    _check(dev_status, "dev_status", torch.int32, allow_none=True)
+    grad_stride = 0 if grad is None else _vocab_rows(grad, "grad", shape=student.shape)
+    st = _L.dspark_distill_loss(_ptr(student), stride, _dtype_code(student), _ptr(teacher_ids), _ptr(teacher_logprobs),
+                                top_k, _ptr(row_weight), float(temperature), rows, V, _ptr(loss), _ptr(grad),
+                                grad_stride, 0 if grad is None else _dtype_code(grad),
+                                DSPARK_DISTILL_REST if rest else 0, _ptr(dev_status), _stream(stream))
+    _raise("dspark_distill_loss", st)
+
+
+def dspark_markov_grad(grad, prev, W1, W2, grad_prev, dW1=None, dW2=None, accumulate=False, ws=None, dev_status=None,
+                       stream=None):
+    stride = _vocab_rows(grad, "grad", torch.bfloat16)
+    rows, V = grad.shape
+    rank = W1.shape[1]
+    _check(prev, "prev", torch.int32, (rows,))
+    _check(W1, "W1", torch.bfloat16, (V, rank))
+    _check(W2, "W2", torch.bfloat16, (V, rank))
+    _check(grad_prev, "grad_prev", torch.float32, (rows, rank))
+    _check(dW1, "dW1", torch.float32, (V, rank), allow_none=True)
+    _check(dW2, "dW2", torch.float32, (V, rank), allow_none=True)
+    _check(ws, "ws", torch.uint8)
+    _check(dev_status, "dev_status", torch.int32, allow_none=True)
+    st = _L.dspark_markov_grad(_ptr(grad), stride, _ptr(prev), _ptr(W1), _ptr(W2), rows, V, rank, _ptr(grad_prev),
+                               _ptr(dW1), _ptr(dW2), DSPARK_GRAD_ACCUMULATE if accumulate else 0, _ptr(ws), ws.numel(),
+                               _ptr(dev_status), _stream(stream))
+    _raise("dspark_markov_grad", st)
 
 
 def dspark_philox4x32_10(ctr, keys, out, stream=None):

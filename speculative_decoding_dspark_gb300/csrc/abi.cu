@@ -127,6 +127,23 @@ int attention_call(AttnParams& p, size_t ws_bytes, unsigned flags, cudaStream_t 
     return p.rows == 0 ? DSPARK_OK : cuda_status(launch_attention(p, stream));
 }
 
+// The scale of the logits of a call with `temperature` > 0; false if there is none.
+bool row_scale(float temperature, float* invT, float* c2) {
+    if (!(temperature > 0.0f) || temperature == INFINITY) return false;
+    *invT = 1.0f / temperature;
+    *c2 = (float)(1.4426950408889634 * (double)*invT);
+    return *c2 > 0.0f && *c2 < INFINITY;
+}
+
+// What dspark_token_logprobs and dspark_distill_loss ask of a matrix of vocabulary rows.
+bool valid_rows(const void* x, int64_t stride, int dtype, int V) {
+    return valid_dtype(dtype) && stride >= V && (reinterpret_cast<uintptr_t>(x) & (dtype == DSPARK_F32 ? 3 : 1)) == 0;
+}
+
+bool markov_grad_supported(int rows, int V, int rank) {
+    return rows >= 0 && V > 0 && rank > 0 && rank % 64 == 0 && rank <= 512 && V % 8 == 0 && rows < (1 << 24);
+}
+
 // Process-wide settings of the grid-wide waits (see dspark_set_wait_limit_ns).
 constexpr unsigned long long kDefaultWaitNs = 2000000000ull;
 std::atomic<unsigned long long> g_wait_ns{kDefaultWaitNs};
@@ -165,7 +182,7 @@ const char* dspark_status_string(int status) {
     }
 }
 
-int dspark_version(void) { return 10300; }
+int dspark_version(void) { return 10400; }
 
 int dspark_markov_draft_uses_tensor_cores(int u_dtype, int w_dtype, int R, int V, int rank,
                                           unsigned flags) {
@@ -175,6 +192,7 @@ int dspark_markov_draft_uses_tensor_cores(int u_dtype, int w_dtype, int R, int V
 size_t dspark_workspace_size(int op, int R, int gamma, int V, int rank, int max_rows,
                              int w_dtype, unsigned flags) {
     if (op == DSPARK_OP_CALIBRATE) return (gamma <= 0 || gamma > 16) ? 0 : calibrate_workspace(gamma);
+    if (op == DSPARK_OP_MARKOV_GRAD) return markov_grad_supported(max_rows, V, rank) ? markov_grad_workspace(max_rows, V, rank) : 0;
     if (R <= 0) return 0;
     switch (op) {
         case DSPARK_OP_DRAFT:
@@ -547,6 +565,68 @@ int dspark_prefix_attention(const void* q, const void* k_cache, const void* v_ca
     p.page = page_size; p.max_blocks = max_blocks; p.pool_pages = pool_pages;
     p.out = static_cast<__nv_bfloat16*>(out); p.lse = lse; p.dev_status = dev_status; p.ws = ws;
     return attention_call(p, ws_bytes, flags, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int dspark_token_logprobs(const void* logits, int64_t row_stride, int dtype, const int32_t* tokens,
+                          const int32_t* cu_seqlens, int R, int width, float temperature, int rows,
+                          int V, int top_k, float* logprob, float* lse, float* entropy,
+                          int32_t* top_ids, float* top_logprobs, int32_t* dev_status,
+                          dspark_stream_t stream) {
+    LogprobsParams p{};
+    if (rows < 0 || V <= 0 || top_k < 0 || !valid_rows(logits, row_stride, dtype, V)) return DSPARK_ERR_INVALID_ARG;
+    if (cu_seqlens && (!tokens || R <= 0 || width <= 0)) return DSPARK_ERR_INVALID_ARG;
+    if (rows != 0 && (!logits || (tokens && !logprob) || (top_k > 0 && (!top_ids || !top_logprobs))))
+        return DSPARK_ERR_INVALID_ARG;
+    if (!row_scale(temperature, &p.invT, &p.c2)) return DSPARK_ERR_INVALID_ARG;
+    if (top_k > DSPARK_TOP_MAX || V > DSPARK_ROWS_MAX_V) return DSPARK_ERR_UNSUPPORTED;
+    if (rows >= (1 << 27) || (cu_seqlens && (int64_t)R * width >= (1 << 27))) return DSPARK_ERR_UNSUPPORTED;
+    p.logits = logits; p.stride = row_stride; p.dtype = dtype; p.tokens = tokens; p.cu = cu_seqlens;
+    p.R = R; p.width = width; p.rows = rows; p.V = V; p.top_k = top_k;
+    p.logprob = logprob; p.lse = lse; p.entropy = entropy; p.top_ids = top_ids; p.top_logprobs = top_logprobs;
+    p.dev_status = dev_status;
+    return rows == 0 ? DSPARK_OK : cuda_status(launch_logprobs(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int dspark_distill_loss(const void* student, int64_t student_stride, int student_dtype,
+                        const int32_t* teacher_ids, const float* teacher_logprobs, int top_k,
+                        const float* row_weight, float temperature, int rows, int V, float* loss,
+                        void* grad, int64_t grad_stride, int grad_dtype, unsigned flags,
+                        int32_t* dev_status, dspark_stream_t stream) {
+    DistillParams p{};
+    if (rows < 0 || V <= 0 || top_k <= 0 || !valid_rows(student, student_stride, student_dtype, V))
+        return DSPARK_ERR_INVALID_ARG;
+    if (grad && !valid_rows(grad, grad_stride, grad_dtype, V)) return DSPARK_ERR_INVALID_ARG;
+    if (grad && grad == student && (grad_dtype != student_dtype || grad_stride != student_stride))
+        return DSPARK_ERR_INVALID_ARG;
+    if (rows != 0 && (!student || !teacher_ids || !teacher_logprobs || !loss)) return DSPARK_ERR_INVALID_ARG;
+    if ((flags & ~DSPARK_DISTILL_REST) != 0) return DSPARK_ERR_INVALID_ARG;
+    if (!row_scale(temperature, &p.invT, &p.c2)) return DSPARK_ERR_INVALID_ARG;
+    if (top_k > DSPARK_TOP_MAX || V > DSPARK_ROWS_MAX_V || rows >= (1 << 27)) return DSPARK_ERR_UNSUPPORTED;
+    p.student = student; p.stride = student_stride; p.dtype = student_dtype;
+    p.ids = teacher_ids; p.teacher = teacher_logprobs; p.top_k = top_k; p.weight = row_weight;
+    p.rows = rows; p.V = V; p.rest = (flags & DSPARK_DISTILL_REST) != 0;
+    p.loss = loss; p.grad = grad; p.grad_stride = grad_stride; p.grad_dtype = grad_dtype; p.dev_status = dev_status;
+    return rows == 0 ? DSPARK_OK : cuda_status(launch_distill(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int dspark_markov_grad(const void* grad, int64_t grad_stride, const int32_t* prev, const void* W1,
+                       const void* W2, int rows, int V, int rank, float* grad_prev, float* dW1,
+                       float* dW2, unsigned flags, void* ws, size_t ws_bytes, int32_t* dev_status,
+                       dspark_stream_t stream) {
+    if (rows < 0 || V <= 0 || rank <= 0 || !W1 || !W2 || (rows != 0 && (!grad || !prev || !grad_prev)))
+        return DSPARK_ERR_INVALID_ARG;
+    if (grad_stride < V || (flags & ~DSPARK_GRAD_ACCUMULATE) != 0) return DSPARK_ERR_INVALID_ARG;
+    if (!markov_grad_supported(rows, V, rank) || grad_stride % 8) return DSPARK_ERR_UNSUPPORTED;
+    for (const void* x : {grad, W1, W2, (const void*)grad_prev, (const void*)dW1, (const void*)dW2})
+        if (!aligned16(x)) return DSPARK_ERR_UNSUPPORTED;
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) % kAlign) != 0) return DSPARK_ERR_WORKSPACE;
+    if (ws_bytes < markov_grad_workspace(rows, V, rank)) return DSPARK_ERR_WORKSPACE;
+    MarkovGradParams p{};
+    p.grad = static_cast<const uint16_t*>(grad); p.stride = grad_stride; p.prev = prev;
+    p.W1 = static_cast<const uint16_t*>(W1); p.W2 = static_cast<const uint16_t*>(W2);
+    p.rows = rows; p.V = V; p.rank = rank; p.accumulate = (flags & DSPARK_GRAD_ACCUMULATE) != 0;
+    p.grad_prev = grad_prev; p.dW1 = dW1; p.dW2 = dW2; p.dev_status = dev_status; p.ws = ws;
+    return cuda_status(launch_markov_grad(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int dspark_philox4x32_10(const uint32_t* ctr, const uint64_t* keys, int n, uint32_t* out,

@@ -247,6 +247,58 @@ struct AttnParams {
 size_t attention_workspace(int R, int n_groups, int rows, int hq, int hkv, int d);
 cudaError_t launch_attention(const AttnParams& p, cudaStream_t stream);
 
+// ----------------------------------------------------------------------------
+// Log probabilities, distillation, the Markov factors' gradient
+// ----------------------------------------------------------------------------
+struct LogprobsParams {
+    const void* logits;
+    int64_t stride;  // elements between rows
+    int dtype;
+    const int32_t *tokens, *cu;  // [rows], or [R, width] beside cu; NULL: every row, no token
+    int R, width, rows, V, top_k;
+    float invT, c2;              // 1 / T, log2(e) / T
+    float *logprob, *lse, *entropy;
+    int32_t* top_ids;
+    float* top_logprobs;
+    int32_t* dev_status;
+};
+
+cudaError_t launch_logprobs(const LogprobsParams& p, cudaStream_t stream);
+
+struct DistillParams {
+    const void* student;
+    int64_t stride;
+    int dtype;
+    const int32_t* ids;
+    const float* teacher;
+    int top_k;
+    const float* weight;
+    int rows, V, rest;
+    float invT, c2;
+    float* loss;
+    void* grad;
+    int64_t grad_stride;
+    int grad_dtype;
+    int staged;      // the rows stay in shared memory for their gradient
+    int32_t* dev_status;
+};
+
+cudaError_t launch_distill(DistillParams p, cudaStream_t stream);
+
+struct MarkovGradParams {
+    const uint16_t* grad;  // [rows, V] bf16
+    int64_t stride;
+    const int32_t* prev;
+    const uint16_t *W1, *W2;
+    int rows, V, rank, accumulate;
+    float *grad_prev, *dW1, *dW2;
+    int32_t* dev_status;
+    void* ws;
+};
+
+size_t markov_grad_workspace(int rows, int V, int rank);
+cudaError_t launch_markov_grad(const MarkovGradParams& p, cudaStream_t stream);
+
 cudaError_t launch_commit(const int32_t* n_acc, const int32_t* l, int R, int gamma,
                           int32_t* commit_len, int32_t* cu_commit, int32_t* discard,
                           int32_t* total, int32_t* dev_status, cudaStream_t stream);

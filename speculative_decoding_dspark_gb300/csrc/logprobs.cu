@@ -1,0 +1,333 @@
+// logprobs.cu -- log probabilities of given tokens, entropy and top alternatives
+// of the target's rows.
+//
+// With t = x / T over the row's V logits x, m its largest x and s = sum exp(t - t_m):
+//   lse = t_m + log s,  logprob = t_token - lse,  entropy = log s - sum (t - t_m) exp(t - t_m) / s
+// in one pass with the running maximum and sums of each thread, joined at the end.
+//
+// The K best: a thread's largest value is one of the row's values, so the K-th
+// largest of the threads' maxima is a bound that at least K values reach, and
+// few more do.  The pass leaves the maximum of every batch of 64 bytes in shared
+// memory; only batches whose maximum reaches the bound are looked at again, and
+// their values that reach it (the candidates) are ranked by counting: the value
+// falls, then the place rises.  A row with more candidates than the list holds
+// (equal values in their hundreds) has its bound found by counting the values'
+// bits from the top, and equal values taken in the order of their places.
+#include <algorithm>
+
+#include "kernels.cuh"
+#include "rows.cuh"
+
+namespace dspark {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kUnroll = 4;       // pieces of a batch
+constexpr int kCandidates = 1024;
+
+__device__ __forceinline__ uint32_t order_of(float x) {
+    const uint32_t b = __float_as_uint(x + 0.0f);  // (-0 is 0)
+    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float of_order(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
+__device__ __forceinline__ uint64_t rank_key(float x, int v) {
+    return ((uint64_t)order_of(x) << 32) | (0xFFFFFFFFu - (uint32_t)v);
+}
+
+struct Shared {
+    uint64_t cand[kCandidates];
+    float maxima[kThreads];
+    SoftSum part[kWarps];
+    SoftSum row;      // this CTA's part of the row
+    float bound;      // its K-th largest thread maximum
+    uint32_t n_cand;  // leader: candidates of all CTAs
+    uint32_t hist[256];
+    uint32_t found;
+    uint32_t count[kWarps];
+    uint32_t prefix, need;
+};
+
+// The K best when the list was too short; leaves exactly K of them in sh.cand.
+template <typename T>
+__device__ __noinline__ void select_by_bits(const T* row, int V, int K, Shared& sh) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint32_t prefix = 0, mask = 0, need = (uint32_t)K;
+    for (int shift = 24; shift >= 0; shift -= 8) {
+        sh.hist[tid] = 0;
+        __syncthreads();
+        uint32_t bin = 0, run = 0;  // equal neighbours are counted together
+        for (int64_t v = tid; v < V; v += kThreads) {
+            const float x = Elem<T>::to_float(row[v]);
+            const uint32_t k = order_of(x);
+            if (x == -INFINITY || (k & mask) != prefix) continue;
+            const uint32_t b = (k >> shift) & 255u;
+            if (run && b != bin) {
+                atomicAdd(&sh.hist[bin], run);
+                run = 0;
+            }
+            bin = b;
+            ++run;
+        }
+        if (run) atomicAdd(&sh.hist[bin], run);
+        __syncthreads();
+        if (tid == 0) {
+            uint32_t above = 0;
+            int b = 255;
+            while (b > 0 && above + sh.hist[b] < need) above += sh.hist[b--];
+            sh.prefix = prefix | ((uint32_t)b << shift);
+            sh.need = need - above;
+        }
+        __syncthreads();
+        prefix = sh.prefix;
+        need = sh.need;
+        mask |= 255u << shift;
+    }
+    if (tid == 0) sh.n_cand = 0;
+    __syncthreads();
+    for (int64_t v = tid; v < V; v += kThreads) {
+        const float x = Elem<T>::to_float(row[v]);
+        if (order_of(x) > prefix) {
+            const uint32_t at = atomicAdd(&sh.n_cand, 1u);
+            if (at < (uint32_t)kCandidates) sh.cand[at] = rank_key(x, (int)v);
+        }
+    }
+    __syncthreads();
+    uint32_t taken = 0;
+    for (int64_t v0 = 0; v0 < V && taken < need; v0 += kThreads) {
+        const int64_t v = v0 + tid;
+        const float x = v < V ? Elem<T>::to_float(row[v]) : -INFINITY;
+        const bool here = v < V && order_of(x) == prefix;
+        const uint32_t votes = __ballot_sync(0xFFFFFFFFu, here);
+        if (lane == 0) sh.count[warp] = __popc(votes);
+        __syncthreads();
+        uint32_t before = taken, all = taken;
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) before += sh.count[w];
+            all += sh.count[w];
+        }
+        before += __popc(votes & ((1u << lane) - 1u));
+        if (here && before < need) sh.cand[(uint32_t)K - need + before] = rank_key(x, (int)v);
+        taken = all;
+        __syncthreads();
+    }
+    if (tid == 0) sh.n_cand = (uint32_t)K;
+    __syncthreads();
+}
+
+// One row's outputs, all of them the same value.
+__device__ __forceinline__ void fill_row(const LogprobsParams& p, int64_t n, float value, float top_value) {
+    if (threadIdx.x == 0) {
+        if (p.logprob) p.logprob[n] = value;
+        if (p.lse) p.lse[n] = value;
+        if (p.entropy) p.entropy[n] = value;
+    }
+    for (int k = threadIdx.x; k < p.top_k; k += kThreads) {
+        p.top_ids[n * p.top_k + k] = -1;
+        p.top_logprobs[n * p.top_k + k] = top_value;
+    }
+}
+
+template <typename T, bool kEntropy, bool kTop>
+__global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsParams p) {
+    constexpr int kVec = Elem<T>::kVec;
+    extern __shared__ float batch_max[];  // [batches of this CTA][thread]
+    __shared__ Shared sh;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = cluster_rank(), size = cluster_size();
+    // ---- which row, which token (the same for all CTAs of the cluster)
+    const int64_t at = blockIdx.x / size;
+    int64_t n = at;
+    int token = 0;
+    if (p.cu) {
+        const int r = (int)(at / p.width), j = (int)(at % p.width);
+        const int a = p.cu[r], b = p.cu[r + 1];
+        if (a < 0 || b < a || b > p.rows || (r == 0 && a != 0)) {
+            if (tid == 0) report(p.dev_status, DSPARK_ERR_DEVICE_INPUT);
+            return;
+        }
+        if (rank == 0 && j == p.width - 1)  // rows that no token can stand beside
+            for (int64_t rest = (int64_t)a + p.width; rest < b; ++rest) fill_row(p, rest, 0.0f, -INFINITY);
+        if (j >= b - a) return;
+        n = a + j;
+        token = p.tokens[at];
+    } else if (p.tokens) {
+        token = p.tokens[n];
+    }
+    if (token < 0) {
+        if (rank == 0) fill_row(p, n, 0.0f, -INFINITY);
+        return;
+    }
+    if (token >= p.V) {
+        if (rank == 0) {
+            fill_row(p, n, NAN, NAN);
+            if (tid == 0) report(p.dev_status, DSPARK_ERR_DEVICE_INPUT);
+        }
+        return;
+    }
+    const T* row = reinterpret_cast<const T*>(p.logits) + n * p.stride;
+    const float x_token = Elem<T>::to_float(row[token]);
+    const RowView<T> view(row, p.V);
+    const int first = (int)((int64_t)view.pieces * rank / size), end = (int)((int64_t)view.pieces * (rank + 1) / size);
+    if (kTop && rank == 0 && tid == 0) sh.n_cand = 0;
+
+    // ---- one pass over this CTA's pieces
+    SoftSum t;
+    int batch = 0;
+    for (int i0 = first + tid; i0 - tid < end; i0 += kUnroll * kThreads, ++batch) {
+        uint4 w[kUnroll];
+#pragma unroll
+        for (int q = 0; q < kUnroll; ++q) {
+            const int i = i0 + q * kThreads;
+            w[q] = load_piece<T>(view.base, i, end);
+        }
+        float x[kUnroll * kVec];
+#pragma unroll
+        for (int q = 0; q < kUnroll; ++q) Elem<T>::unpack(w[q], x + q * kVec);
+        const float top = soft_add<kEntropy>(t, x, p.c2);
+        if (kTop) batch_max[batch * kThreads + tid] = top;
+    }
+    const int v_edge = view.edge(tid, rank == 0, rank == size - 1);
+    const float x_edge[2] = {v_edge >= 0 ? view.at(v_edge) : -INFINITY, -INFINITY};
+    soft_add<kEntropy>(t, x_edge, p.c2);
+    if (kTop) sh.maxima[tid] = t.m;
+    // ---- joined over the CTA
+    {
+        SoftSum a = t;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            SoftSum b;
+            b.m = shfl_xor(a.m, o);
+            b.s = shfl_xor(a.s, o);
+            if (kEntropy) b.u = shfl_xor(a.u, o);
+            soft_merge<kEntropy>(a, b, p.c2);
+        }
+        if (lane == 0) sh.part[warp] = a;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        SoftSum a = sh.part[0];
+        for (int w = 1; w < kWarps; ++w) soft_merge<kEntropy>(a, sh.part[w], p.c2);
+        sh.row = a;
+    }
+    if (kTop) {
+        // the thread whose maximum is the K-th largest (of equal ones the later thread is lower)
+        int above = 0;
+        for (int j = 0; j < kThreads; j += 4) {
+            const float4 o = *reinterpret_cast<const float4*>(sh.maxima + j);
+            above += (o.x > t.m || (o.x == t.m && j < tid)) + (o.y > t.m || (o.y == t.m && j + 1 < tid)) +
+                     (o.z > t.m || (o.z == t.m && j + 2 < tid)) + (o.w > t.m || (o.w == t.m && j + 3 < tid));
+        }
+        if (above == p.top_k - 1) sh.bound = t.m;
+    }
+    cluster_sync();
+    // ---- joined over the cluster, by its first CTA; the bound by all
+    SoftSum all = sh.row;
+    if (rank == 0 && size > 1) {
+        for (uint32_t c = 1; c < size; ++c) {
+            const uint32_t a = cluster_map(&sh.row, c);
+            SoftSum b;
+            b.m = cluster_ld_f32(a + offsetof(SoftSum, m));
+            b.s = cluster_ld_f32(a + offsetof(SoftSum, s));
+            b.u = cluster_ld_f32(a + offsetof(SoftSum, u));
+            soft_merge<kEntropy>(all, b, p.c2);
+        }
+    }
+    if (kTop) {
+        float bound = -INFINITY;
+        for (uint32_t c = 0; c < size; ++c) bound = fmaxf(bound, cluster_ld_f32(cluster_map(&sh.bound, c)));
+        const uint32_t list = cluster_map(sh.cand, 0), count = cluster_map(&sh.n_cand, 0);
+        auto offer = [&](float x, int v) {
+            if (x >= bound && x > -INFINITY) {
+                const uint32_t c = cluster_atomic_add(count, 1u);
+                if (c < (uint32_t)kCandidates) cluster_st_u64(list + 8 * c, rank_key(x, v));
+            }
+        };
+        offer(x_edge[0], v_edge);
+        for (int b = 0; b < batch; ++b) {
+            if (!(batch_max[b * kThreads + tid] >= bound)) continue;
+#pragma unroll 1
+            for (int q = 0; q < kUnroll; ++q) {
+                const int i = first + tid + (b * kUnroll + q) * kThreads;
+                if (i >= end) break;
+                float x[kVec];
+                Elem<T>::unpack(__ldcs(view.base + i), x);
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) offer(x[e], view.head + i * kVec + e);
+            }
+        }
+    }
+    if (size > 1 || kTop) cluster_sync();
+    if (rank != 0) return;
+    // ---- the row's outputs
+    if (!(all.s > 0.0f && all.s < INFINITY) || all.m == INFINITY) {
+        // a NaN or +inf in it, or nothing but -inf
+        fill_row(p, n, NAN, NAN);
+        if (tid == 0) report(p.dev_status, DSPARK_ERR_DEVICE_INPUT);
+        return;
+    }
+    const float log_s = logf(all.s);
+    if (tid == 0) {
+        if (p.logprob) p.logprob[n] = p.tokens ? (x_token - all.m) * p.invT - log_s : 0.0f;
+        if (p.lse) p.lse[n] = all.m * p.invT + log_s;
+        if (kEntropy) p.entropy[n] = log_s - kLn2F * (all.u / all.s);
+    }
+    if (kTop) {
+        if (sh.n_cand > (uint32_t)kCandidates) select_by_bits<T>(row, p.V, p.top_k, sh);
+        const int found = (int)sh.n_cand;
+        for (int c = tid; c < found; c += kThreads) {
+            const uint64_t mine = sh.cand[c];
+            int place = 0;
+            for (int o = 0; o < found; ++o) place += sh.cand[o] > mine;
+            if (place < p.top_k) {
+                p.top_ids[n * p.top_k + place] = (int32_t)(0xFFFFFFFFu - (uint32_t)mine);
+                p.top_logprobs[n * p.top_k + place] = (of_order((uint32_t)(mine >> 32)) - all.m) * p.invT - log_s;
+            }
+        }
+        for (int k = found + tid; k < p.top_k; k += kThreads) {
+            p.top_ids[n * p.top_k + k] = -1;
+            p.top_logprobs[n * p.top_k + k] = -INFINITY;
+        }
+    }
+}
+
+template <typename T>
+const void* kernel_of(bool entropy, bool top) {
+    return entropy ? (top ? (const void*)logprobs_kernel<T, true, true> : (const void*)logprobs_kernel<T, true, false>)
+                   : (top ? (const void*)logprobs_kernel<T, false, true> : (const void*)logprobs_kernel<T, false, false>);
+}
+
+}  // namespace
+
+cudaError_t launch_logprobs(const LogprobsParams& p, cudaStream_t stream) {
+    const int vec = p.dtype == DSPARK_F32 ? 4 : 8;
+    const int64_t places = p.cu ? (int64_t)p.R * p.width : p.rows;
+    int ctas = 1;
+    auto smem_of = [&](int c) {
+        const int64_t per = ((int64_t)p.V / vec + c - 1) / c;
+        return (size_t)(p.top_k ? (per + kUnroll * kThreads - 1) / (kUnroll * kThreads) * kThreads * sizeof(float) : 0);
+    };
+    while (ctas < 8 && smem_of(ctas) > 48 * 1024) ctas *= 2;
+    const size_t smem = smem_of(ctas);
+    const void* fn = p.dtype == DSPARK_F32 ? kernel_of<float>(p.entropy, p.top_k > 0)
+                                           : kernel_of<uint16_t>(p.entropy, p.top_k > 0);
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(places * ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void* args[] = {const_cast<LogprobsParams*>(&p)};
+    return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+}  // namespace dspark
