@@ -5,126 +5,437 @@
 //   grad_prev[n] = sum_v g[n][v] W2[v]            (dL / d W1[prev[n]], of this row)
 //   dW1[a]       = sum of grad_prev[n] over the rows with prev[n] = a
 //   dW2[v]       = sum_n g[n][v] W1[prev[n]]
-// Both products are sums of exact products of bf16 values in fp32.
+// Two products of the same gradient, both on the tensor cores (exact products of
+// bf16 values, fp32 sums).  One kernel computes both, tiles of 128 x 256:
+//   grad_prev: rows x rank, summed over V.  Few tiles and a long sum, so it is cut
+//              into parts; the parts of all tiles go through the same stretch of V at the same
+//              time (g and W2 are read from memory about once, then from L2), and
+//              join_kernel adds them in order.
+//   dW2:       V x rank, summed over the rows: many tiles, each written once.  g's tile
+//              is read with V, the contiguous direction, as the product's rows.
+// The tensor cores may cut off what lies below the accumulator's last bit, so a
+// chain of products ends after 64 of them (1024 terms); the epilogue's threads
+// hold the tile in registers and add the chains in fp32.
 #include <algorithm>
 
 #include "kernels.cuh"
+#include "tc_ptx.cuh"
 
 namespace dspark {
 namespace {
 
-constexpr int kTile = 64, kStep = 16, kThreads = 256;
-constexpr int kSplitKeys = 8192;
+constexpr int kTileM = 128, kTileN = 256;
+constexpr int kBlockK = 64;            // terms of a pipeline stage
+constexpr int kChain = 16;             // stages of a chain
+constexpr int kStages = 4;
+constexpr int kGroup = 64 * 64 * 2;    // 64 rows of 128 bytes
+constexpr int kABytes = kTileM * kBlockK * 2, kBBytes = kTileN * kBlockK * 2;
+constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kEpilogueWarps = 8;
+constexpr int kThreads = 32 * (kEpilogueWarps + 2);
+constexpr size_t kSmem = kStages * kStageBytes + 1024;
+constexpr uint32_t kIdescATransposed = 1u << 15;
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kGatherRows = 16;
+constexpr int kGridSms = 152;          // what the parts of a sum are counted for
 
-int splits_of(int V) { return (V + kSplitKeys - 1) / kSplitKeys; }
+struct Product {
+    int M, rank;           // rows and columns of the result
+    int blocks;            // stages of the whole sum
+    int tiles_n, tiles;    // tiles along the columns, in all
+    int parts, per;        // parts of a sum, stages in each
+    float* C;              // [parts][M][rank]
+    int accumulate;
+    const uint64_t* drop;  // a bit per row of g that gives nothing (dW2), a word per stage
+    int32_t* dev_status;
+};
 
-// ---- W1 rows of the previous tokens, zeros where there is none
-__global__ void __launch_bounds__(128) gather_kernel(const MarkovGradParams p, uint16_t* E) {
-    const int n = blockIdx.x;
-    const int a = p.prev[n];
-    if (a >= p.V && threadIdx.x == 0) report(p.dev_status, DSPARK_ERR_DEVICE_INPUT);
-    const bool there = a >= 0 && a < p.V;
-    for (int i = threadIdx.x; i < p.rank; i += 128)
-        E[(size_t)n * p.rank + i] = there ? p.W1[(size_t)a * p.rank + i] : (uint16_t)0;
-}
+struct Barriers {
+    uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], drain;
+    uint32_t tmem;
+    int abort_flag;
+};
 
-// C[m][r] = sum_k A[m][k] B[k][r] over k in [z * per, ...): a tile of 64 x 64 per CTA.
-__global__ void __launch_bounds__(kThreads) product_kernel(const uint16_t* A, int64_t sm, int64_t sk, const uint16_t* B,
-                                                           int M, int K, int rank, int per, float* C, int accumulate) {
-    __shared__ float a[kStep][kTile + 1], b[kStep][kTile + 1];
-    const int m0 = blockIdx.x * kTile, r0 = blockIdx.y * kTile, z = blockIdx.z;
-    const int k_begin = z * per, k_end = min(K, k_begin + per);
-    const int tm = threadIdx.x / 16 * 4, tr = threadIdx.x % 16 * 4;
-    float acc[4][4] = {};
-    for (int k0 = k_begin; k0 < k_end; k0 += kStep) {
-        for (int i = threadIdx.x; i < kStep * kTile; i += kThreads) {
-            // neighbouring threads along the contiguous direction
-            const int ka = sk == 1 ? i % kStep : i / kTile, ma = sk == 1 ? i / kStep : i % kTile;
-            a[ka][ma] = k0 + ka < k_end && m0 + ma < M ? bf16_bits_to_float(A[(m0 + ma) * sm + (k0 + ka) * sk]) : 0.0f;
-            const int kb = i / kTile, rb = i % kTile;
-            b[kb][rb] = k0 + kb < k_end ? bf16_bits_to_float(B[(size_t)(k0 + kb) * rank + r0 + rb]) : 0.0f;
+// tc::mbar_wait for threads whose registers are full: with its slow part called
+// out of line all 128 sums of a thread were spilled around the call.
+__device__ __forceinline__ bool wait_inline(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    for (;;) {
+        if (tc::mbar_try_wait_sleep(bar, parity, 20000)) return true;
+        if (*abort_flag) return false;
+        if (global_ns() - t0 > kWaitNs) {
+            *abort_flag = 1;
+            return false;
         }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kStep; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] += a[k][tm + i] * b[k][tr + j];
-        __syncthreads();
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j)
-            if (m0 + tm + i < M) {
-                float* c = C + ((size_t)z * M + m0 + tm + i) * rank + r0 + tr + j;
-                *c = accumulate ? *c + acc[i][j] : acc[i][j];
-            }
 }
 
-// ---- the splits of grad_prev, in order
-__global__ void __launch_bounds__(128) join_kernel(const MarkovGradParams p, const float* part, int splits) {
-    const int n = blockIdx.x;
-    const int a = p.prev[n];
-    for (int i = threadIdx.x; i < p.rank; i += 128) {
-        float s = 0.0f;
-        for (int z = 0; z < splits; ++z) s += part[((size_t)z * p.rows + n) * p.rank + i];
-        p.grad_prev[(size_t)n * p.rank + i] = a < 0 ? 0.0f : a >= p.V ? NAN : s;
+// kSumRows: the sum runs over g's rows (dW2), else over V (grad_prev).
+template <bool kSumRows>
+__global__ void __launch_bounds__(kThreads, 1)
+    product_kernel(const Product p, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b) {
+    extern __shared__ unsigned char dyn[];
+    __shared__ Barriers sh;
+    unsigned char* ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    volatile int* abort_flag = &sh.abort_flag;
+    if (warp == kEpilogueWarps + 1) {
+        tc::tmem_alloc(&sh.tmem, 512);
+        tc::tmem_relinquish();
+    } else if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            tc::mbar_init(&sh.full[s], 1);
+            tc::mbar_init(&sh.empty[s], 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            tc::mbar_init(&sh.tfull[a], 1);
+            tc::mbar_init(&sh.tempty[a], kEpilogueWarps);
+        }
+        tc::mbar_init(&sh.drain, 1);
+        sh.abort_flag = 0;
+        tc::fence_barrier_init();
     }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    launch_dependents();
+    wait_prior_grid();
+    const int units = p.tiles * p.parts;
+
+    // a unit of work: one tile's sum over the stages [k0, k1)
+    struct Unit {
+        int m0, n0, cols, part, k0, k1;
+    };
+    auto unit_of = [&](int u) {
+        Unit x;
+        x.part = u / p.tiles;
+        const int t = u - x.part * p.tiles;
+        x.m0 = t / p.tiles_n * kTileM;
+        x.n0 = t % p.tiles_n * kTileN;
+        x.cols = min(kTileN, p.rank - x.n0);
+        x.k0 = x.part * p.per;
+        x.k1 = min(p.blocks, x.k0 + p.per);
+        return x;
+    };
+
+    if (warp == kEpilogueWarps) {
+        // ---------------------------------------------------------------- loads
+        if (lane == 0) {
+            tc::prefetch_tmap(&map_a);
+            tc::prefetch_tmap(&map_b);
+            int i = 0;
+            bool go = true;
+            for (int u = blockIdx.x; go && u < units; u += gridDim.x) {
+                const Unit x = unit_of(u);
+                const uint32_t bytes = kABytes + x.cols / 64 * kGroup;
+                for (int k = x.k0; k < x.k1; ++k, ++i) {
+                    const int s = i % kStages;
+                    if (i >= kStages && !(go = tc::mbar_wait(&sh.empty[s], (i / kStages - 1) & 1, abort_flag, kWaitNs))) break;
+                    unsigned char* a = ring + s * kStageBytes;
+                    unsigned char* b = a + kABytes;
+                    tc::mbar_arrive_expect_tx(&sh.full[s], bytes);
+                    if (kSumRows) {
+                        tc::tma_load_2d(a, &map_a, &sh.full[s], x.m0, k * kBlockK);
+                        tc::tma_load_2d(a + kGroup, &map_a, &sh.full[s], x.m0 + 64, k * kBlockK);
+                    } else {
+                        tc::tma_load_2d(a, &map_a, &sh.full[s], k * kBlockK, x.m0);
+                    }
+                    for (int c = 0; c < x.cols; c += 64)
+                        tc::tma_load_2d(b + c / 64 * kGroup, &map_b, &sh.full[s], x.n0 + c, k * kBlockK);
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == kEpilogueWarps + 1) {
+        // ---------------------------------------------------------------- products
+        int i = 0, chain = 0;
+        bool go = true;
+        for (int u = blockIdx.x; go && u < units; u += gridDim.x) {
+            const Unit x = unit_of(u);
+            const uint32_t idesc = tc::idesc_bf16_f32(kTileM, x.cols) | tc::kIdescBTransposed | (kSumRows ? kIdescATransposed : 0u);
+            for (int c0 = x.k0; go && c0 < x.k1; c0 += kChain, ++chain) {
+                const int buf = chain & 1;
+                if (chain >= 2 && !(go = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&sh.tempty[buf], (chain / 2 - 1) & 1, abort_flag, kWaitNs)))) break;
+                tc::tc_fence_after();
+                const uint32_t d = tmem + buf * kTileN;
+                const int c1 = min(x.k1, c0 + kChain);
+                for (int k = c0; k < c1; ++k, ++i) {
+                    const int s = i % kStages;
+                    // rows that give nothing, NaN and infinities in them among it
+                    const uint64_t drop = kSumRows ? __ldcg(p.drop + k) : 0;
+                    if (!(go = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&sh.full[s], (i / kStages) & 1, abort_flag, kWaitNs)))) break;
+                    unsigned char* a = ring + s * kStageBytes;
+                    if (kSumRows && drop) {
+                        for (uint64_t left = drop; left; left &= left - 1) {
+                            const int r = __ffsll((long long)left) - 1;
+                            if (lane < 16)
+                                *reinterpret_cast<uint4*>(a + (lane >> 3) * kGroup + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        tc::fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    tc::tc_fence_after();
+                    const uint32_t sa = tc::smem_u32(a);
+                    const uint64_t ad = kSumRows ? tc::smem_desc_sw128_mn(sa, kGroup) : tc::smem_desc_sw128(sa);
+                    const uint64_t bd = tc::smem_desc_sw128_mn(sa + kABytes, kGroup);
+#pragma unroll
+                    for (int j = 0; j < kBlockK / 16; ++j)
+                        tc::umma_bf16_elect(d, ad + (uint64_t)(j * ((kSumRows ? 2048 : 32) >> 4)), bd + (uint64_t)(j * (2048 >> 4)),
+                                            idesc, k > c0 || j > 0);
+                    tc::umma_commit_elect(&sh.empty[s]);
+                }
+                if (go) tc::umma_commit_elect(&sh.tfull[buf]);
+            }
+        }
+        __syncwarp();
+        // (whatever ended the loop, the products are done before tensor memory is given back)
+        tc::umma_commit_elect(&sh.drain);
+        int never = 0;
+        tc::mbar_wait(&sh.drain, 0, &never, kWaitNs);
+    } else {
+        // ---------------------------------------------------------------- chains added up, tiles written
+        const int quad = warp & 3, half = warp >> 2;
+        int chain = 0;
+        bool go = true;
+        for (int u = blockIdx.x; go && u < units; u += gridDim.x) {
+            const Unit x = unit_of(u);
+            const int cols = min(128, x.cols - half * 128);  // (none: only the barriers)
+            float acc[128];
+#pragma unroll
+            for (int e = 0; e < 128; ++e) acc[e] = 0.0f;
+            for (int c0 = x.k0; c0 < x.k1; c0 += kChain, ++chain) {
+                const int buf = chain & 1;
+                if (!(go = __all_sync(0xFFFFFFFFu, wait_inline(&sh.tfull[buf], (chain / 2) & 1, abort_flag)))) break;
+                tc::tc_fence_after();
+                if (cols > 0) {
+                    const uint32_t t = tmem + ((uint32_t)(quad * 32) << 16) + buf * kTileN + half * 128;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        float v[16];
+                        tc::tmem_ld_32x32b_x16<0>(t + 16 * q, v);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) acc[16 * q + e] += v[e];
+                    }
+                }
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&sh.tempty[buf]);
+            }
+            const int row = x.m0 + quad * 32 + lane;
+            if (go && cols > 0 && row < p.M) {
+                float* c = p.C + ((size_t)x.part * p.M + row) * p.rank + x.n0 + half * 128;
+#pragma unroll
+                for (int e = 0; e < 128; e += 4) {
+                    if (e < cols) {
+                        float4 y = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+                        if (p.accumulate) {
+                            const float4 o = *reinterpret_cast<const float4*>(c + e);
+                            y = make_float4(o.x + y.x, o.y + y.y, o.z + y.z, o.w + y.w);
+                        }
+                        *reinterpret_cast<float4*>(c + e) = y;
+                    }
+                }
+            }
+        }
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    if (sh.abort_flag) {
+        if (tid == 0) report(p.dev_status, DSPARK_ERR_TIMEOUT);
+        const uint64_t t0 = global_ns();  // loads in flight end before their memory goes
+        while (global_ns() - t0 < 1000000) {}
+    }
+    if (warp == kEpilogueWarps + 1) tc::tmem_dealloc(tmem, 512);
+}
+
+// ---- W1 rows of the previous tokens (zeros where there is none), and which rows give nothing
+__global__ void __launch_bounds__(32 * kGatherRows) gather_kernel(const MarkovGradParams p, uint16_t* E, uint16_t* drop) {
+    __shared__ uint32_t off;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int n = blockIdx.x * kGatherRows + warp;
+    wait_prior_grid();
+    if (threadIdx.x == 0) off = 0;
+    __syncthreads();
+    const int a = n < p.rows ? p.prev[n] : -1;
+    const bool there = a >= 0 && a < p.V;
+    if (lane == 0) {
+        if (n < p.rows && !there) atomicOr(&off, 1u << warp);
+        if (a >= p.V) report(p.dev_status, DSPARK_ERR_DEVICE_INPUT);
+    }
+    if (n < p.rows)
+        for (int i = lane; i < p.rank / 8; i += 32)
+            reinterpret_cast<uint4*>(E + (size_t)n * p.rank)[i] =
+                there ? __ldg(reinterpret_cast<const uint4*>(p.W1 + (size_t)a * p.rank) + i) : make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    if (threadIdx.x == 0) drop[blockIdx.x] = (uint16_t)off;
+    launch_dependents();
+}
+
+// ---- the parts of grad_prev, in order
+__global__ void __launch_bounds__(128) join_kernel(const MarkovGradParams p, const float* part, int parts) {
+    const int n = blockIdx.x, i = threadIdx.x;
+    wait_prior_grid();
+    if (4 * i < p.rank) {
+        const int a = p.prev[n];
+        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+        for (int z = 0; z < parts; ++z) {
+            const float4 x = __ldcs(reinterpret_cast<const float4*>(part + ((size_t)z * p.rows + n) * p.rank) + i);
+            s = make_float4(s.x + x.x, s.y + x.y, s.z + x.z, s.w + x.w);
+        }
+        if (a < 0) s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (a >= p.V) s = make_float4(NAN, NAN, NAN, NAN);
+        reinterpret_cast<float4*>(p.grad_prev + (size_t)n * p.rank)[i] = s;
+    }
+    launch_dependents();
 }
 
 // ---- dW1: the first row of each previous token adds up all of them, in order
 __global__ void __launch_bounds__(128) scatter_kernel(const MarkovGradParams p) {
     const int n = blockIdx.x;
+    wait_prior_grid();
     const int a = p.prev[n];
     if (a < 0 || a >= p.V) return;
     int seen = 0;
     for (int m = threadIdx.x; m < n; m += 128) seen |= p.prev[m] == a;
     if (__syncthreads_or(seen)) return;
-    constexpr int kMost = 4;  // rank <= 512
-    float s[kMost] = {};
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const int i = threadIdx.x;
     for (int m0 = n; m0 < p.rows; m0 += 32) {
         const int m = m0 + (threadIdx.x & 31);
         unsigned same = __ballot_sync(0xFFFFFFFFu, m < p.rows && p.prev[m] == a);
         for (; same; same &= same - 1) {
-            const float* g = p.grad_prev + (size_t)(m0 + __ffs(same) - 1) * p.rank;
-#pragma unroll
-            for (int i = 0; i < kMost; ++i)
-                if (threadIdx.x + 128 * i < p.rank) s[i] += g[threadIdx.x + 128 * i];
+            if (4 * i < p.rank) {
+                const float4 x =
+                    reinterpret_cast<const float4*>(p.grad_prev + (size_t)(m0 + __ffs(same) - 1) * p.rank)[i];
+                s = make_float4(s.x + x.x, s.y + x.y, s.z + x.z, s.w + x.w);
+            }
         }
     }
-    float* d = p.dW1 + (size_t)a * p.rank;
-#pragma unroll
-    for (int i = 0; i < kMost; ++i) {
-        const int r = threadIdx.x + 128 * i;
-        if (r < p.rank) d[r] = p.accumulate ? d[r] + s[i] : s[i];
+    if (4 * i >= p.rank) return;
+    float4* d = reinterpret_cast<float4*>(p.dW1 + (size_t)a * p.rank) + i;
+    if (p.accumulate) {
+        const float4 o = *d;
+        s = make_float4(o.x + s.x, o.y + s.y, o.z + s.z, o.w + s.w);
     }
+    *d = s;
 }
 
+// ------------------------------------------------------------------------------- host
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+int up(int a, int b) { return (a + b - 1) / b; }
+
+// How many parts the sum over V is cut into: the fewest steps of the busiest SM,
+// a stage counted as 512 cycles of products and a part's way to memory and back
+// as its bytes at 23 a cycle and SM.
+int parts_of(int rows, int V, int rank) {
+    const int tiles = up(rows, kTileM) * up(rank, kTileN), blocks = up(V, kBlockK);
+    double best = 0;
+    int parts = 1;
+    for (int n = 1; n <= std::min(blocks, 152); ++n) {
+        const double steps = (double)up(tiles * n, kGridSms) * (up(blocks, n) * 512.0 + 3000.0);
+        const double moved = (double)n * rows * rank * 8.0 / (23.0 * kGridSms);
+        if (n == 1 || steps + moved < best) {
+            best = steps + moved;
+            parts = n;
+        }
+    }
+    return up(blocks, up(blocks, parts));
+}
+
+struct Layout {
+    size_t E, drop, part, total;
+};
+Layout layout_of(int rows, int V, int rank) {
+    Layout L;
+    size_t off = 0;
+    L.E = off; off += align256((size_t)rows * rank * 2);
+    L.drop = off; off += align256((size_t)up(rows, kBlockK) * 8);
+    L.part = off; off += align256((size_t)parts_of(rows, V, rank) * rows * rank * 4);
+    L.total = std::max<size_t>(off, 256);
+    return L;
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encoder() {
+    static const EncodeTiled fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                        q == cudaDriverEntryPointSuccess;
+        return ok ? reinterpret_cast<EncodeTiled>(f) : nullptr;
+    }();
+    return fn;
+}
+
+// Boxes of 64 columns and `box_rows` rows of a bf16 matrix; zeros outside it.
+bool encode(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t stride, int box_rows) {
+    const EncodeTiled enc = encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+    const cuuint32_t es[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool kSumRows>
+cudaError_t launch_product(Product p, const CUtensorMap& a, const CUtensorMap& b, int n_sm, cudaStream_t stream) {
+    p.tiles_n = up(p.rank, kTileN);
+    p.tiles = up(p.M, kTileM) * p.tiles_n;
+    p.per = up(p.blocks, p.parts);
+    const cudaError_t e = cudaFuncSetAttribute(product_kernel<kSumRows>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_after(product_kernel<kSumRows>, dim3(std::min(n_sm, p.tiles * p.parts)), kThreads, kSmem, stream, p, a, b);
+}
 
 }  // namespace
 
-size_t markov_grad_workspace(int rows, int V, int rank) {
-    return 256 + align256((size_t)rows * rank * 2) + (size_t)splits_of(V) * rows * rank * 4;
-}
+size_t markov_grad_workspace(int rows, int V, int rank) { return layout_of(rows, V, rank).total; }
 
 cudaError_t launch_markov_grad(const MarkovGradParams& p, cudaStream_t stream) {
     if (p.rows == 0) {
         if (!p.dW2 || p.accumulate) return cudaSuccess;
         return cudaMemsetAsync(p.dW2, 0, (size_t)p.V * p.rank * sizeof(float), stream);
     }
-    uint16_t* E = static_cast<uint16_t*>(p.ws);
-    float* part = reinterpret_cast<float*>(static_cast<unsigned char*>(p.ws) + align256((size_t)p.rows * p.rank * 2));
-    const int splits = splits_of(p.V);
-    gather_kernel<<<p.rows, 128, 0, stream>>>(p, E);
-    product_kernel<<<dim3((p.rows + kTile - 1) / kTile, p.rank / kTile, splits), kThreads, 0, stream>>>(
-        p.grad, p.stride, 1, p.W2, p.rows, p.V, p.rank, kSplitKeys, part, 0);
-    join_kernel<<<p.rows, 128, 0, stream>>>(p, part, splits);
-    if (p.dW1) scatter_kernel<<<p.rows, 128, 0, stream>>>(p);
-    if (p.dW2)
-        product_kernel<<<dim3((p.V + kTile - 1) / kTile, p.rank / kTile, 1), kThreads, 0, stream>>>(
-            p.grad, 1, p.stride, E, p.V, p.rows, p.rank, p.rows, p.dW2, p.accumulate);
-    return cudaGetLastError();
+    int dev = 0, n_sm = 0;
+    cudaError_t e;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    const Layout L = layout_of(p.rows, p.V, p.rank);
+    unsigned char* w = static_cast<unsigned char*>(p.ws);
+    uint16_t* E = reinterpret_cast<uint16_t*>(w + L.E);
+    float* part = reinterpret_cast<float*>(w + L.part);
+    const int parts = parts_of(p.rows, p.V, p.rank);
+    const int64_t stride = p.rows > 1 ? p.stride : p.V;
+    CUtensorMap g_rows, g_cols, w2, before;
+    if (!encode(&g_rows, p.grad, p.V, p.rows, stride, kTileM) || !encode(&g_cols, p.grad, p.V, p.rows, stride, kBlockK) ||
+        !encode(&w2, p.W2, p.rank, p.V, p.rank, kBlockK) || !encode(&before, E, p.rank, p.rows, p.rank, kBlockK))
+        return cudaErrorInvalidValue;
+    if ((e = launch_after(gather_kernel, dim3(up(p.rows, kBlockK) * (kBlockK / kGatherRows)), 32 * kGatherRows, 0, stream, p, E,
+                          reinterpret_cast<uint16_t*>(w + L.drop))) != cudaSuccess)
+        return e;
+    Product q{};
+    q.rank = p.rank;
+    q.dev_status = p.dev_status;
+    q.M = p.rows; q.blocks = up(p.V, kBlockK); q.parts = parts; q.C = part;
+    if ((e = launch_product<false>(q, g_rows, w2, n_sm, stream)) != cudaSuccess) return e;
+    if ((e = launch_after(join_kernel, dim3(p.rows), 128, 0, stream, p, part, parts)) != cudaSuccess) return e;
+    if (p.dW1 && (e = launch_after(scatter_kernel, dim3(p.rows), 128, 0, stream, p)) != cudaSuccess) return e;
+    if (p.dW2) {
+        q.M = p.V; q.blocks = up(p.rows, kBlockK); q.parts = 1; q.C = p.dW2; q.accumulate = p.accumulate;
+        q.drop = reinterpret_cast<const uint64_t*>(w + L.drop);
+        if ((e = launch_product<true>(q, g_cols, before, n_sm, stream)) != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace dspark

@@ -468,13 +468,17 @@ def test_markov_grad_in_part(B, want):
         assert b is None or torch.equal(a, b)
 
 
-def test_markov_grad_bad_token(B):
-    rows, V, rank = 40, 640, 64
+@pytest.mark.parametrize("rows,V,rank", [(40, 640, 64), (150, 4104, 320)])
+def test_markov_grad_bad_token(B, rows, V, rank):
+    """Tokens that are none: their rows give nothing, and what stands in them is not seen."""
     g, prev, W1, W2 = markov_case(7, rows, V, rank)
-    prev[3], prev[17] = V, 2 ** 31 - 1
+    prev[3], prev[17], prev[rows - 1] = V, 2 ** 31 - 1, -5
+    seen = g.clone()
+    seen[[3, 17, rows - 1]] = 0
+    g[3], g[17, 5], g[rows - 1] = NAN, INF, -INF
     gp, d1, d2, status = markov(B, g, prev, W1, W2)
     assert status == DEVICE_INPUT
-    ref, tol = L.markov(g, prev, W1, W2)
+    ref, tol = L.markov(seen, prev, W1, W2)
     close(gp, ref[0], tol[0], "grad_prev")
     close(d1, ref[1], tol[1], "dW1")
     close(d2, ref[2], tol[2], "dW2")
