@@ -33,7 +33,8 @@ constexpr int kABytes = kTileM * kBlockK * 2, kBBytes = kTileN * kBlockK * 2;
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kEpilogueWarps = 8;
 constexpr int kThreads = 32 * (kEpilogueWarps + 2);
-constexpr size_t kSmem = kStages * kStageBytes + 1024;
+constexpr int kPiece = 32 * 32 * 4;    // 32 rows of 32 sums: what a warp hands to one store
+constexpr size_t kSmem = kStages * kStageBytes + kEpilogueWarps * kPiece + 1024;
 constexpr uint32_t kIdescATransposed = 1u << 15;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kGatherRows = 16;
@@ -44,7 +45,6 @@ struct Product {
     int blocks;            // stages of the whole sum
     int tiles_n, tiles;    // tiles along the columns, in all
     int parts, per;        // parts of a sum, stages in each
-    float* C;              // [parts][M][rank]
     int accumulate;
     const uint64_t* drop;  // a bit per row of g that gives nothing (dW2), a word per stage
     int32_t* dev_status;
@@ -55,6 +55,24 @@ struct Barriers {
     uint32_t tmem;
     int abort_flag;
 };
+
+// 32 x 32 sums from shared memory to (or added to) columns x.., rows y.. of part z.
+__device__ __forceinline__ void store_piece(const CUtensorMap* map, const void* src, int x, int y, int z, int add) {
+    if (add)
+        asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                         reinterpret_cast<uint64_t>(map)),
+                     "r"(tc::smem_u32(src)), "r"(x), "r"(y), "r"(z)
+                     : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                         reinterpret_cast<uint64_t>(map)),
+                     "r"(tc::smem_u32(src)), "r"(x), "r"(y), "r"(z)
+                     : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// Until the stores of this thread have read their shared memory; until they are done.
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // tc::mbar_wait for threads whose registers are full: with its slow part called
 // out of line all 128 sums of a thread were spilled around the call.
@@ -74,7 +92,8 @@ __device__ __forceinline__ bool wait_inline(uint64_t* bar, uint32_t parity, vola
 // kSumRows: the sum runs over g's rows (dW2), else over V (grad_prev).
 template <bool kSumRows>
 __global__ void __launch_bounds__(kThreads, 1)
-    product_kernel(const Product p, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b) {
+    product_kernel(const Product p, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                   const __grid_constant__ CUtensorMap map_c) {
     extern __shared__ unsigned char dyn[];
     __shared__ Barriers sh;
     unsigned char* ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
@@ -197,6 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ---------------------------------------------------------------- chains added up, tiles written
         const int quad = warp & 3, half = warp >> 2;
+        unsigned char* piece = ring + kStages * kStageBytes + warp * kPiece;
         int chain = 0;
         bool go = true;
         for (int u = blockIdx.x; go && u < units; u += gridDim.x) {
@@ -224,22 +244,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&sh.tempty[buf]);
             }
-            const int row = x.m0 + quad * 32 + lane;
-            if (go && cols > 0 && row < p.M) {
-                float* c = p.C + ((size_t)x.part * p.M + row) * p.rank + x.n0 + half * 128;
+            // 32 columns at a time through shared memory (16-byte pieces in the order the store's swizzle
+            // undoes), then to memory by one store, which leaves out what lies past the result's rows.  Stores
+            // from registers, a row to a thread, took 210 us of markov_batch's second product.
+            const int row = x.m0 + quad * 32;
+            if (go && row < p.M) {
 #pragma unroll
-                for (int e = 0; e < 128; e += 4) {
-                    if (e < cols) {
-                        float4 y = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
-                        if (p.accumulate) {
-                            const float4 o = *reinterpret_cast<const float4*>(c + e);
-                            y = make_float4(o.x + y.x, o.y + y.y, o.z + y.z, o.w + y.w);
-                        }
-                        *reinterpret_cast<float4*>(c + e) = y;
+                for (int q = 0; q < 4; ++q) {
+                    if (32 * q < cols) {
+                        if (lane == 0) bulk_wait_read();
+                        __syncwarp();
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            *reinterpret_cast<float4*>(piece + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+                                make_float4(acc[32 * q + 4 * e], acc[32 * q + 4 * e + 1], acc[32 * q + 4 * e + 2], acc[32 * q + 4 * e + 3]);
+                        tc::fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) store_piece(&map_c, piece, x.n0 + half * 128 + 32 * q, row, x.part, p.accumulate);
                     }
                 }
             }
         }
+        if (lane == 0) bulk_wait();
+        __syncwarp();
     }
     tc::tc_fence_before();
     __syncthreads();
@@ -274,16 +301,33 @@ __global__ void __launch_bounds__(32 * kGatherRows) gather_kernel(const MarkovGr
     launch_dependents();
 }
 
-// ---- the parts of grad_prev, in order
-__global__ void __launch_bounds__(128) join_kernel(const MarkovGradParams p, const float* part, int parts) {
-    const int n = blockIdx.x, i = threadIdx.x;
+// ---- the parts of grad_prev: every group of threads adds its own in order, then the groups in order
+constexpr int kJoinThreads = 512;
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const MarkovGradParams p, const float* part, int parts) {
+    __shared__ float4 sums[kJoinThreads];
+    const int n = blockIdx.x, quads = p.rank / 4, groups = kJoinThreads / quads;
+    const int i = threadIdx.x % quads, g = threadIdx.x / quads;
     wait_prior_grid();
-    if (4 * i < p.rank) {
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (g < groups) {
+        for (int z0 = g; z0 < parts; z0 += 4 * groups) {
+            float4 x[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int z = z0 + q * groups;
+                x[q] = z < parts ? __ldcs(reinterpret_cast<const float4*>(part + ((size_t)z * p.rows + n) * p.rank) + i)
+                                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) s = make_float4(s.x + x[q].x, s.y + x[q].y, s.z + x[q].z, s.w + x[q].w);
+        }
+    }
+    sums[threadIdx.x] = s;
+    __syncthreads();
+    if (g == 0) {
         const int a = p.prev[n];
-        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-        for (int z = 0; z < parts; ++z) {
-            const float4 x = __ldcs(reinterpret_cast<const float4*>(part + ((size_t)z * p.rows + n) * p.rank) + i);
+        for (int o = 1; o < groups; ++o) {
+            const float4 x = sums[o * quads + i];
             s = make_float4(s.x + x.x, s.y + x.y, s.z + x.z, s.w + x.w);
         }
         if (a < 0) s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -387,14 +431,28 @@ bool encode(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Boxes of 32 columns and 32 rows of [parts][rows][cols] fp32.
+bool encode_sums(CUtensorMap* m, const void* base, int cols, int rows, int parts) {
+    const EncodeTiled enc = encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)parts};
+    const cuuint64_t strides[2] = {(cuuint64_t)cols * 4, (cuuint64_t)cols * 4 * rows};
+    const cuuint32_t box[3] = {32, 32, 1};
+    const cuuint32_t es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <bool kSumRows>
-cudaError_t launch_product(Product p, const CUtensorMap& a, const CUtensorMap& b, int n_sm, cudaStream_t stream) {
+cudaError_t launch_product(Product p, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, int n_sm,
+                           cudaStream_t stream) {
     p.tiles_n = up(p.rank, kTileN);
     p.tiles = up(p.M, kTileM) * p.tiles_n;
     p.per = up(p.blocks, p.parts);
     const cudaError_t e = cudaFuncSetAttribute(product_kernel<kSumRows>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
-    return launch_after(product_kernel<kSumRows>, dim3(std::min(n_sm, p.tiles * p.parts)), kThreads, kSmem, stream, p, a, b);
+    return launch_after(product_kernel<kSumRows>, dim3(std::min(n_sm, p.tiles * p.parts)), kThreads, kSmem, stream, p, a, b, c);
 }
 
 }  // namespace
@@ -416,9 +474,10 @@ cudaError_t launch_markov_grad(const MarkovGradParams& p, cudaStream_t stream) {
     float* part = reinterpret_cast<float*>(w + L.part);
     const int parts = parts_of(p.rows, p.V, p.rank);
     const int64_t stride = p.rows > 1 ? p.stride : p.V;
-    CUtensorMap g_rows, g_cols, w2, before;
+    CUtensorMap g_rows, g_cols, w2, before, sums, dW2;
     if (!encode(&g_rows, p.grad, p.V, p.rows, stride, kTileM) || !encode(&g_cols, p.grad, p.V, p.rows, stride, kBlockK) ||
-        !encode(&w2, p.W2, p.rank, p.V, p.rank, kBlockK) || !encode(&before, E, p.rank, p.rows, p.rank, kBlockK))
+        !encode(&w2, p.W2, p.rank, p.V, p.rank, kBlockK) || !encode(&before, E, p.rank, p.rows, p.rank, kBlockK) ||
+        !encode_sums(&sums, part, p.rank, p.rows, parts) || (p.dW2 && !encode_sums(&dW2, p.dW2, p.rank, p.V, 1)))
         return cudaErrorInvalidValue;
     if ((e = launch_after(gather_kernel, dim3(up(p.rows, kBlockK) * (kBlockK / kGatherRows)), 32 * kGatherRows, 0, stream, p, E,
                           reinterpret_cast<uint16_t*>(w + L.drop))) != cudaSuccess)
@@ -426,14 +485,14 @@ cudaError_t launch_markov_grad(const MarkovGradParams& p, cudaStream_t stream) {
     Product q{};
     q.rank = p.rank;
     q.dev_status = p.dev_status;
-    q.M = p.rows; q.blocks = up(p.V, kBlockK); q.parts = parts; q.C = part;
-    if ((e = launch_product<false>(q, g_rows, w2, n_sm, stream)) != cudaSuccess) return e;
-    if ((e = launch_after(join_kernel, dim3(p.rows), 128, 0, stream, p, part, parts)) != cudaSuccess) return e;
+    q.M = p.rows; q.blocks = up(p.V, kBlockK); q.parts = parts;
+    if ((e = launch_product<false>(q, g_rows, w2, sums, n_sm, stream)) != cudaSuccess) return e;
+    if ((e = launch_after(join_kernel, dim3(p.rows), kJoinThreads, 0, stream, p, part, parts)) != cudaSuccess) return e;
     if (p.dW1 && (e = launch_after(scatter_kernel, dim3(p.rows), 128, 0, stream, p)) != cudaSuccess) return e;
     if (p.dW2) {
-        q.M = p.V; q.blocks = up(p.rows, kBlockK); q.parts = 1; q.C = p.dW2; q.accumulate = p.accumulate;
+        q.M = p.V; q.blocks = up(p.rows, kBlockK); q.parts = 1; q.accumulate = p.accumulate;
         q.drop = reinterpret_cast<const uint64_t*>(w + L.drop);
-        if ((e = launch_product<true>(q, g_cols, before, n_sm, stream)) != cudaSuccess) return e;
+        if ((e = launch_product<true>(q, g_cols, before, dW2, n_sm, stream)) != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
