@@ -279,7 +279,8 @@ struct DistillParams {
     void* grad;
     int64_t grad_stride;
     int grad_dtype;
-    int staged;      // the rows stay in shared memory for their gradient
+    int staged;      // batches of a row that stay in shared memory for their gradient
+    int bit_words;
     int32_t* dev_status;
 };
 

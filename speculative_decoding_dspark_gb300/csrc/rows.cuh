@@ -37,10 +37,14 @@ __device__ __forceinline__ uint32_t cluster_size() {
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
+// The two halves of it; a thread waits before it arrives again.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // All threads of the cluster meet; shared-memory writes before it are visible after it.
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+
 // The address of `p` (this CTA's shared memory) in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t cluster_map(const void* p, uint32_t rank) {
     uint32_t a;
@@ -61,6 +65,9 @@ __device__ __forceinline__ uint32_t cluster_atomic_add(uint32_t a, uint32_t x) {
     uint32_t v;
     asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(v) : "r"(a), "r"(x) : "memory");
     return v;
+}
+__device__ __forceinline__ void cluster_st_f32(uint32_t a, float x) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(x) : "memory");
 }
 __device__ __forceinline__ void cluster_st_u64(uint32_t a, uint64_t x) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(x) : "memory");
@@ -179,8 +186,10 @@ __device__ __forceinline__ float soft_add(SoftSum& t, const float (&x)[N], float
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
         float2 a = mul2(add2(make_float2(x[i], x[i + 1]), minus), scale);
-        a.x = fmaxf(a.x, -200.0f);  // (2^-200 is zero, and so is its product)
-        a.y = fmaxf(a.y, -200.0f);
+        if (kEntropy) {  // (2^-200 is zero, and so is its product)
+            a.x = fmaxf(a.x, -200.0f);
+            a.y = fmaxf(a.y, -200.0f);
+        }
         const float2 e = make_float2(exp2_approx(a.x), exp2_approx(a.y));
         s = add2(s, e);
         if (kEntropy) u = fma2(e, a, u);
