@@ -20,7 +20,7 @@
 // asynchronous copies into the places that the second pass has just emptied (each
 // thread fills and empties places of its own: no barrier).  What a place cannot be
 // found for (rows longer than the cluster's shared memory) is read twice.  One warp
-// keeps the listed tokens and does all that is done once per row.
+// of its own keeps the listed tokens and does all that is done once per row.
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -30,21 +30,24 @@
 namespace dspark {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // that walk through the rows
 constexpr int kWarps = kThreads / 32;
+constexpr int kAllThreads = kThreads + 32;  // and the warp that keeps the listed tokens
 constexpr int kUnroll = 4;     // pieces of a batch
 constexpr int kMaxCtas = 8;    // of a cluster
 constexpr int kPerLane = DSPARK_TOP_MAX / 32;
 
-struct Part {  // the tokens that are not listed, as one CTA sees them
-    float m, s, bad;
+struct Kept {  // what is known of a row's listed tokens before its sums are
+    float x_top, e_sum;  // the largest logit, the sum of 2^((x - x_top) c2)
+    float mass;          // the teacher's: the sum of p (with the rest as a class), or whether there is any
+    float bad;
 };
 
 struct Shared {
-    SoftSum warp_sum[kWarps];
-    Part parts[2][kMaxCtas];  // of all CTAs, by the row's parity
-    float factor, m_ref;      // the gradient of a token that is not listed: factor 2^((x - m_ref) c2)
-    int bad;
+    float2 sums[2][kMaxCtas][kWarps];  // (m, s) of all warps of the cluster, by the row's parity
+    float bad[2][kMaxCtas];            // whether a CTA found fault with the listed tokens
+    Kept kept[2];
+    uint32_t marked[kThreads];         // which batches of a thread hold listed tokens (bit 31: the 32nd or a later one)
 };
 
 __device__ __forceinline__ float warp_max(float a) {
@@ -85,12 +88,17 @@ __device__ __forceinline__ void store_piece(uint16_t* p, const float (&x)[8]) {
                                                    bf16_pair(x[6], x[7])));
 }
 
-// One CTA's part of a gradient row, all of it one value.
+// This CTA's share of a gradient row of weight 0.
 template <typename G>
-__device__ __forceinline__ void fill_grad(G* g, int V, uint32_t rank, uint32_t size, float x) {
-    const G y = grad_of<G>(x);
-    const int64_t a = (int64_t)V * rank / size, b = (int64_t)V * (rank + 1) / size;
-    for (int64_t v = a + threadIdx.x; v < b; v += kThreads) g[v] = y;
+__device__ __forceinline__ void clear_grad(G* g, int V, uint32_t rank, uint32_t size) {
+    constexpr int kVec = 16 / sizeof(G);
+    const int head = min(V, (int)(((16 - (reinterpret_cast<uintptr_t>(g) & 15)) & 15) / sizeof(G)));
+    const int pieces = (V - head) / kVec, first = pieces * rank / size, end = pieces * (rank + 1) / size;
+    uint4* wide = reinterpret_cast<uint4*>(g + head);
+    for (int i = first + threadIdx.x; i < end; i += kAllThreads) __stcs(wide + i, make_uint4(0, 0, 0, 0));
+    if (rank == 0 && threadIdx.x < head) g[threadIdx.x] = G(0);
+    const int tail = head + pieces * kVec + threadIdx.x;
+    if (rank == size - 1 && tail < V) g[tail] = G(0);
 }
 
 // At most `left` (or 7) of this thread's groups of copies still on their way.
@@ -115,8 +123,8 @@ struct Share {
     int v0, v1;        // its elements, the row's edges among them
     __device__ __forceinline__ Share(const DistillParams& p, int64_t row, uint32_t rank, uint32_t size)
         : view(reinterpret_cast<const T*>(p.student) + row * p.stride, p.V) {
-        first = (int)((int64_t)view.pieces * rank / size);
-        const int end = (int)((int64_t)view.pieces * (rank + 1) / size);
+        first = view.pieces * rank / size;
+        const int end = view.pieces * (rank + 1) / size;
         n = end - first;
         v0 = rank == 0 ? 0 : view.head + first * Elem<T>::kVec;
         v1 = rank == size - 1 ? p.V : view.head + end * Elem<T>::kVec;
@@ -127,7 +135,7 @@ struct Share {
     __device__ __forceinline__ int batches() const { return (n + kUnroll * kThreads - 1) / (kUnroll * kThreads); }
 };
 
-// A row's listed tokens, four to a lane of the first warp.
+// A row's listed tokens, four to a lane of the warp that keeps them.
 struct Listed {
     int id[kPerLane];    // -1: none
     float x[kPerLane];   // the drafter's logit
@@ -136,37 +144,40 @@ struct Listed {
 
 // T: the logits' elements, G: the gradient's, kGrad: there is one.
 template <typename T, typename G, bool kGrad>
-__global__ void __launch_bounds__(kThreads) distill_kernel(const DistillParams p) {
+__global__ void __launch_bounds__(kAllThreads, kGrad ? 2 : 3) distill_kernel(const DistillParams p) {
     constexpr int kVec = Elem<T>::kVec;
+    constexpr int kBatch = kUnroll * kThreads;  // pieces
     extern __shared__ uint4 dyn[];
     __shared__ Shared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const bool keeper = warp == kWarps;
     const uint32_t rank = cluster_rank(), size = cluster_size();
     const int clusters = gridDim.x / size;
-    uint4* stage = dyn + tid;                                                     // [p.staged batches][kUnroll][kThreads]
-    uint32_t* bits = reinterpret_cast<uint32_t*>(dyn + p.staged * kUnroll * kThreads);
-    for (int i = tid; i < p.bit_words; i += kThreads) bits[i] = 0;
+    uint4* stage = dyn + tid;  // [p.staged batches][kUnroll][kThreads]
+    uint32_t* bits = reinterpret_cast<uint32_t*>(dyn + p.staged * kBatch);
+    for (int i = tid; i < p.bit_words; i += kAllThreads) bits[i] = 0;
+    if (tid < kThreads) sh.marked[tid] = 0;
 
-    auto weight_of = [&](int64_t n) { return p.weight ? __ldg(p.weight + n) : 1.0f; };
+    auto weight_of = [&](int64_t n) { return p.weight && n < p.rows ? __ldg(p.weight + n) : 1.0f; };
     // The next row from n on that has a weight; those that have none are done with.
     auto active = [&](int64_t n, float& w) {
         while (n < p.rows && w == 0.0f) {
-            if (kGrad) fill_grad(reinterpret_cast<G*>(p.grad) + n * p.grad_stride, p.V, rank, size, 0.0f);
+            if (kGrad) clear_grad(reinterpret_cast<G*>(p.grad) + n * p.grad_stride, p.V, rank, size);
             if (rank == 0 && tid == 0) p.loss[n] = 0.0f;
             n += clusters;
-            if (n < p.rows) w = weight_of(n);
+            w = weight_of(n);
         }
         return n;
     };
     auto copy_batch = [&](const Share<T>& s, int b) {
+        const uint4* from = s.pieces() + b * kBatch + tid;
+        const int left = s.n - b * kBatch - tid;
 #pragma unroll
-        for (int q = 0; q < kUnroll; ++q) {
-            const int i = (b * kUnroll + q) * kThreads + tid;
-            if (i < s.n) tc::cp_async_16(tc::smem_u32(stage + (b * kUnroll + q) * kThreads), s.pieces() + i, 16);
-        }
+        for (int q = 0; q < kUnroll; ++q)
+            if (q * kThreads < left) tc::cp_async_16(tc::smem_u32(stage + b * kBatch + q * kThreads), from + q * kThreads, 16);
         tc::cp_async_commit();
     };
-    // (first warp) a row's listed tokens
+    // (keeper) a row's listed tokens
     auto fetch = [&](int64_t n, Listed& t) {
         const RowView<T> view(reinterpret_cast<const T*>(p.student) + n * p.stride, p.V);
 #pragma unroll
@@ -181,253 +192,268 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const DistillParams p
             t.x[q] = t.id[q] >= 0 && t.id[q] < p.V ? view.at(t.id[q]) : -INFINITY;
         }
     };
-    // (first warp) marks a row's listed tokens; whether something is wrong with them
+    // (keeper) marks a row's listed tokens; whether something is wrong with them
     auto mark = [&](const Share<T>& s, const Listed& t) {
         bool bad = false;
 #pragma unroll
         for (int q = 0; q < kPerLane; ++q) {
             bad |= t.id[q] >= p.V || t.value[q] != t.value[q] || t.value[q] == INFINITY || t.x[q] != t.x[q];
             if (t.id[q] >= s.v0 && t.id[q] < s.v1) {
-                const int b = s.bit(t.id[q]);
+                const int b = s.bit(t.id[q]), piece = (b - 32) / kVec;
                 bad |= (atomicOr(&bits[b >> 5], 1u << (b & 31)) >> (b & 31) & 1u) != 0;  // listed twice
+                if (b >= 32 && piece < s.n) atomicOr(&sh.marked[piece % kThreads], 1u << min(piece / kBatch, 31));
             }
         }
         return __any_sync(0xFFFFFFFFu, bad);
     };
+    auto unmark = [&](const Share<T>& s, const Listed& t) {
+#pragma unroll
+        for (int q = 0; q < kPerLane; ++q)
+            if (t.id[q] >= s.v0 && t.id[q] < s.v1) {
+                const int b = s.bit(t.id[q]), piece = (b - 32) / kVec;
+                bits[b >> 5] = 0;
+                if (b >= 32 && piece < s.n) sh.marked[piece % kThreads] = 0;
+            }
+        __syncwarp();
+    };
+
+    // The row's sums over the cluster (every warp by itself; the lanes agree).
+    struct Joined {
+        SoftSum rest;              // the tokens that are not listed
+        float m_all, f_rest, f_listed, total, p_rest, all_mass;
+        float m_ref, factor;       // the gradient of a token that is not listed: factor 2^((x - m_ref) c2)
+        bool bad;
+    };
+    auto joined = [&](int parity, float weight) {
+        Joined j;
+        const Kept kept = sh.kept[parity];
+        constexpr int kEach = kMaxCtas * kWarps / 32;
+        SoftSum each[kEach], t;
+        const int n_sums = size * kWarps;
+#pragma unroll
+        for (int q = 0; q < kEach; ++q) {
+            const int at = lane + 32 * q;
+            if (at < n_sums) {
+                const float2 a = sh.sums[parity][at / kWarps][at % kWarps];
+                each[q].m = a.x;
+                each[q].s = a.y;
+            }
+            t.m = fmaxf(t.m, each[q].m);
+        }
+#pragma unroll
+        for (int q = 0; q < kEach; ++q)
+            t.s += each[q].m == -INFINITY ? each[q].s : each[q].s * exp2_approx((each[q].m - t.m) * p.c2);
+        j.rest = soft_join<false, 32>(t, p.c2);
+        const float bad_there = (uint32_t)lane < size ? sh.bad[parity][lane] : 0.0f;
+        j.m_all = fmaxf(kept.x_top, j.rest.m);
+        j.f_rest = j.rest.m > -INFINITY ? exp2_approx((j.rest.m - j.m_all) * p.c2) : 0.0f;
+        j.f_listed = kept.x_top > -INFINITY ? exp2_approx((kept.x_top - j.m_all) * p.c2) : 0.0f;
+        j.total = kept.e_sum * j.f_listed + j.rest.s * j.f_rest;
+        j.bad = __any_sync(0xFFFFFFFFu, bad_there != 0.0f) || kept.bad != 0.0f || !(j.total > 0.0f && j.total < INFINITY) ||
+                j.m_all == INFINITY || j.rest.s != j.rest.s;
+        const bool none = j.rest.m == -INFINITY;  // (what is not listed is -inf alone: no class of the rest)
+        j.p_rest = p.rest && !none ? fmaxf(1.0f - kept.mass, 0.0f) : 0.0f;
+        j.all_mass = kept.mass + j.p_rest;
+        j.m_ref = none ? 0.0f : j.rest.m;
+        j.factor = j.bad ? NAN
+                   : none ? 0.0f
+                          : weight * p.invT * (j.all_mass * j.f_rest / j.total - (j.p_rest > 0.0f ? j.p_rest / j.rest.s : 0.0f));
+        return j;
+    };
 
     int64_t row = blockIdx.x / size;
-    if (row >= p.rows) return;  // (the whole cluster)
     float weight = weight_of(row);
     row = active(row, weight);
+    float ahead = weight_of(row + clusters);
     Listed now;
     bool bad_list = false;
     __syncthreads();
     if (row < p.rows) {
         const Share<T> s(p, row, rank, size);
-        if (kGrad)
-            for (int b = 0; b < p.staged; ++b) copy_batch(s, b);
-        if (warp == 0) {
+        if (keeper) {
             fetch(row, now);
             bad_list = mark(s, now);
+        } else if (kGrad) {
+            for (int b = 0; b < p.staged; ++b) copy_batch(s, b);
         }
     }
     __syncthreads();
 
     for (int parity = 0; row < p.rows; parity ^= 1) {
         const Share<T> s(p, row, rank, size);
-        const int n_batches = s.batches();
-        const int v_edge = warp == 1 ? s.view.edge(lane, rank == 0, rank == size - 1) : -1;
-        const float x_edge = v_edge >= 0 ? s.view.at(v_edge) : -INFINITY;
-        int64_t next = row + clusters;
-        float next_weight = next < p.rows ? weight_of(next) : 0.0f;
-
-        // ---- first pass: the tokens that are not listed
-        SoftSum t;
-        for (int b = 0; b < n_batches; ++b) {
-            uint4 w[kUnroll];
-            if (kGrad && b < p.staged) {
-                copies_left(p.staged - 1 - b);
+        float next_weight = ahead;
+        const int64_t next = active(row + clusters, next_weight);
+        ahead = weight_of(next + clusters);
+        const bool more = next < p.rows;
+        if (!keeper) {
+            const int n_batches = s.batches();
+            const int v_edge = warp == 0 ? s.view.edge(lane, rank == 0, rank == size - 1) : -1;
+            const float x_edge = v_edge >= 0 ? s.view.at(v_edge) : -INFINITY;
+            const uint32_t marked = sh.marked[tid];
+            // ---- first pass: the tokens that are not listed
+            SoftSum t;
+            auto add_batch = [&](uint4 (&w)[kUnroll], int b) {
+                if (marked >> min(b, 31) & 1u) {
 #pragma unroll
-                for (int q = 0; q < kUnroll; ++q) {
-                    constexpr uint32_t k = Elem<T>::kMinusInf;
-                    const int i = (b * kUnroll + q) * kThreads + tid;
-                    w[q] = i < s.n ? stage[(b * kUnroll + q) * kThreads] : make_uint4(k, k, k, k);
+                    for (int q = 0; q < kUnroll; ++q) {
+                        const int at = (b * kBatch + q * kThreads + tid) * kVec;
+                        if (at < s.n * kVec) w[q] = Elem<T>::without(w[q], bits[1 + (at >> 5)] >> (at & 31));
+                    }
                 }
-            } else {
+                soft_add<T, false>(t, w, p.c2);
+            };
+            for (int b = 0; b < n_batches; ++b) {
+                constexpr uint32_t k = Elem<T>::kMinusInf;
+                const int left = s.n - b * kBatch - tid;
+                uint4 w[kUnroll];
+                if (kGrad && b < p.staged) {
+                    copies_left(p.staged - 1 - b);
+                    if (left > (kUnroll - 1) * kThreads) {
 #pragma unroll
-                for (int q = 0; q < kUnroll; ++q) w[q] = load_piece<T>(s.pieces(), (b * kUnroll + q) * kThreads + tid, s.n);
-            }
-            float x[kUnroll * kVec];
+                        for (int q = 0; q < kUnroll; ++q) w[q] = stage[b * kBatch + q * kThreads];
+                    } else {
 #pragma unroll
-            for (int q = 0; q < kUnroll; ++q) {
-                const int i = (b * kUnroll + q) * kThreads + tid;
-                Elem<T>::unpack(w[q], x + q * kVec);
-                if (i < s.n) {
-                    const uint32_t m = bits[1 + (i * kVec >> 5)] >> (i * kVec & 31) & ((1u << kVec) - 1u);
-                    if (m)
+                        for (int q = 0; q < kUnroll; ++q)
+                            w[q] = q * kThreads < left ? stage[b * kBatch + q * kThreads] : make_uint4(k, k, k, k);
+                    }
+                } else {
+                    const uint4* from = s.pieces() + b * kBatch + tid;
 #pragma unroll
-                        for (int e = 0; e < kVec; ++e)
-                            if (m >> e & 1u) x[q * kVec + e] = -INFINITY;
+                    for (int q = 0; q < kUnroll; ++q)
+                        w[q] = q * kThreads < left ? __ldcs(from + q * kThreads) : make_uint4(k, k, k, k);
                 }
+                add_batch(w, b);
             }
-            soft_add<false>(t, x, p.c2);
-        }
-        if (warp == 1) {
-            const int b = v_edge >= 0 ? s.bit(v_edge) : 0;
-            const float edge[2] = {v_edge >= 0 && !(bits[b >> 5] >> (b & 31) & 1u) ? x_edge : -INFINITY, -INFINITY};
-            soft_add<false>(t, edge, p.c2);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            SoftSum b;
-            b.m = shfl_xor(t.m, o);
-            b.s = shfl_xor(t.s, o);
-            soft_merge<false>(t, b, p.c2);
-        }
-        if (lane == 0) sh.warp_sum[warp] = t;
-        __syncthreads();
-        // ---- the CTA's sums to all CTAs of the cluster
-        if (warp == 0) {
-            SoftSum a;
-            if (lane < kWarps) a = sh.warp_sum[lane];
-#pragma unroll
-            for (int o = kWarps / 2; o > 0; o >>= 1) {
-                SoftSum b;
-                b.m = shfl_xor(a.m, o);
-                b.s = shfl_xor(a.s, o);
-                soft_merge<false>(a, b, p.c2);
-            }
-            a.m = __shfl_sync(0xFFFFFFFFu, a.m, 0);
-            a.s = __shfl_sync(0xFFFFFFFFu, a.s, 0);
-            if (lane < (int)size) {
-                const uint32_t to = cluster_map(&sh.parts[parity][rank], lane);
-                cluster_st_f32(to + offsetof(Part, m), a.m);
-                cluster_st_f32(to + offsetof(Part, s), a.s);
-                cluster_st_f32(to + offsetof(Part, bad), bad_list ? 1.0f : 0.0f);
+            if (v_edge >= 0) {
+                const int b = s.bit(v_edge);
+                if (!(bits[b >> 5] >> (b & 31) & 1u)) soft_add_one<false>(t, x_edge, p.c2);
             }
             __syncwarp();
-        }
-        cluster_arrive();
-        next = active(next, next_weight);
-        Listed then;
-        if (warp == 0) {
-            // this row's marks go
-#pragma unroll
-            for (int q = 0; q < kPerLane; ++q)
-                if (now.id[q] >= s.v0 && now.id[q] < s.v1) bits[s.bit(now.id[q]) >> 5] = 0;
-            if (next < p.rows) fetch(next, then);
+            // ---- to all CTAs of the cluster
+            t = soft_join<false, 32>(t, p.c2);
+            if ((uint32_t)lane < size) cluster_st_f32x2(cluster_map(&sh.sums[parity][rank][warp], lane), t.m, t.s);
+            __syncwarp();
+            cluster_arrive();
             cluster_wait();
-            SoftSum rest;
-            float bad_f = 0.0f;
-            if (lane < (int)size) {
-                const Part a = sh.parts[parity][lane];
-                rest.m = a.m;
-                rest.s = a.s;
-                bad_f = a.bad;
-            }
+            // ---- second pass: the gradient; the next row's pieces follow this one's
+            if (kGrad) {
+                G* grad = reinterpret_cast<G*>(p.grad) + row * p.grad_stride;
+                const Share<T> after(p, more ? next : row, rank, size);
+                const Joined j = joined(parity, weight);
+                const float m_ref = j.m_ref, factor = j.factor;
+                const float2 scale = make_float2(p.c2, p.c2), f2 = make_float2(factor, factor);
+                const float2 minus = make_float2(-m_ref, -m_ref);
+                G* out = grad + s.view.head + (int64_t)s.first * kVec;
+                const bool wide = reinterpret_cast<uintptr_t>(out) % (kVec * sizeof(G) < 16 ? kVec * sizeof(G) : 16) == 0;
+                const int all_batches = more ? max(n_batches, p.staged) : n_batches;
+                auto write = [&](const uint4& w, int64_t i) {
+                    float x[kVec];
 #pragma unroll
-            for (int o = kMaxCtas / 2; o > 0; o >>= 1) {
-                SoftSum b;
-                b.m = shfl_xor(rest.m, o);
-                b.s = shfl_xor(rest.s, o);
-                soft_merge<false>(rest, b, p.c2);
+                    for (int e = 0; e < kVec; e += 2) {
+                        const float2 y = Elem<T>::pair(w, e / 2);
+                        const float2 a = mul2(add2(y, minus), scale);
+                        const float2 g = mul2(make_float2(exp2_approx(a.x), exp2_approx(a.y)), f2);
+                        x[e] = g.x;
+                        x[e + 1] = g.y;
+                    }
+                    if (wide) {
+                        store_piece(out + i * kVec, x);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < kVec; ++e) out[i * kVec + e] = grad_of<G>(x[e]);
+                    }
+                };
+                for (int b = 0; b < all_batches; ++b) {
+                    const int i0 = b * kBatch + tid, left = s.n - i0;
+                    uint4 w[kUnroll];
+                    if (left > (kUnroll - 1) * kThreads && b < p.staged) {
+#pragma unroll
+                        for (int q = 0; q < kUnroll; ++q) w[q] = stage[b * kBatch + q * kThreads];
+#pragma unroll
+                        for (int q = 0; q < kUnroll; ++q) write(w[q], i0 + q * kThreads);
+                    } else {
+#pragma unroll 1
+                        for (int q = 0; q * kThreads < left && q < kUnroll; ++q)
+                            write(b < p.staged ? stage[b * kBatch + q * kThreads] : __ldcs(s.pieces() + i0 + q * kThreads),
+                                  i0 + q * kThreads);
+                    }
+                    if (more && b < p.staged) copy_batch(after, b);
+                }
+                if (v_edge >= 0) grad[v_edge] = grad_of<G>(factor * exp2_approx((x_edge - m_ref) * p.c2));
             }
-            rest.m = __shfl_sync(0xFFFFFFFFu, rest.m, 0);
-            rest.s = __shfl_sync(0xFFFFFFFFu, rest.s, 0);
-            bool bad = __any_sync(0xFFFFFFFFu, bad_f != 0.0f) || !(fabsf(weight) < INFINITY);
-            // the teacher's classes, and the row's maximum and sum over listed tokens and rest
+            __syncthreads();  // the gradient is written, the next row's tokens are marked
+        } else {
+            // ---- the keeper: what does not wait for this row's sums
+            Listed then;
+            if (more) fetch(next, then);
             float x_top = -INFINITY, v_top = -INFINITY;
 #pragma unroll
             for (int q = 0; q < kPerLane; ++q) {
                 x_top = fmaxf(x_top, now.x[q]);
                 v_top = fmaxf(v_top, now.value[q]);
             }
-            const float m_all = fmaxf(warp_max(x_top), rest.m);
+            x_top = warp_max(x_top);
             v_top = p.rest ? 0.0f : warp_max(v_top);  // (a list of -inf alone has no mass)
             float prob[kPerLane], e_listed[kPerLane], mass = 0.0f, e_sum = 0.0f;
 #pragma unroll
             for (int q = 0; q < kPerLane; ++q) {
                 prob[q] = now.value[q] > -INFINITY ? expf(now.value[q] - v_top) : 0.0f;
-                e_listed[q] = now.x[q] > -INFINITY ? exp2_approx((now.x[q] - m_all) * p.c2) : 0.0f;
+                e_listed[q] = now.x[q] > -INFINITY ? exp2_approx((now.x[q] - x_top) * p.c2) : 0.0f;
                 mass += prob[q];
                 e_sum += e_listed[q];
             }
             mass = warp_sum(mass);
-            const float f_rest = rest.m > -INFINITY ? exp2_approx((rest.m - m_all) * p.c2) : 0.0f;
-            const float total = warp_sum(e_sum) + rest.s * f_rest;
-            bad |= !(total > 0.0f && total < INFINITY) || m_all == INFINITY || rest.s != rest.s || !(mass < INFINITY);
-            const float log_total = logf(total);
-            float p_rest = 0.0f, scale = 1.0f, log_scale = 0.0f, all_mass;
-            if (p.rest) {
-                // (no class of the rest where the drafter has no token left for it)
-                if (rest.m > -INFINITY) p_rest = fmaxf(1.0f - mass, 0.0f);
-                all_mass = mass + p_rest;
-            } else {
-                all_mass = mass > 0.0f ? 1.0f : 0.0f;  // nothing listed: nothing to learn from
-                if (mass > 0.0f) {
-                    scale = 1.0f / mass;
-                    log_scale = -v_top - logf(mass);
-                }
+            e_sum = warp_sum(e_sum);
+            float scale = 1.0f, log_scale = 0.0f;
+            const bool bad_row = !(fabsf(weight) < INFINITY) || !(mass < INFINITY);
+            if (!p.rest && mass > 0.0f) {
+                scale = 1.0f / mass;
+                log_scale = -v_top - logf(mass);
+                mass = 1.0f;  // (nothing listed: nothing to learn from)
             }
+            if (lane == 0) {
+                Kept k;
+                k.x_top = x_top;
+                k.e_sum = e_sum;
+                k.mass = mass;
+                k.bad = bad_row ? 1.0f : 0.0f;
+                sh.kept[parity] = k;
+            }
+            if ((uint32_t)lane < size) cluster_st_f32(cluster_map(&sh.bad[parity][rank], lane), bad_list ? 1.0f : 0.0f);
+            __syncwarp();
+            cluster_arrive();
+            cluster_wait();
+            const Joined j = joined(parity, weight);
             const float w = weight * p.invT;
             if (rank == 0) {
+                const float log_total = logf(j.total);
                 float term = 0.0f;
 #pragma unroll
                 for (int q = 0; q < kPerLane; ++q)
                     if (prob[q] > 0.0f)
-                        term += prob[q] * scale * ((now.value[q] + log_scale) - ((now.x[q] - m_all) * p.invT - log_total));
+                        term += prob[q] * scale *
+                                ((now.value[q] + log_scale) - ((now.x[q] - j.m_all) * p.invT - log_total));
                 term = warp_sum(term);
-                if (p_rest > 0.0f) term += p_rest * (logf(p_rest) - ((rest.m - m_all) * p.invT + logf(rest.s) - log_total));
+                if (j.p_rest > 0.0f)
+                    term += j.p_rest * (logf(j.p_rest) - ((j.rest.m - j.m_all) * p.invT + logf(j.rest.s) - log_total));
                 if (lane == 0) {
-                    p.loss[row] = bad ? NAN : weight * term;
-                    if (bad) report(p.dev_status, DSPARK_ERR_DEVICE_INPUT);
+                    p.loss[row] = j.bad ? NAN : weight * term;
+                    if (j.bad) report(p.dev_status, DSPARK_ERR_DEVICE_INPUT);
                 }
             }
-            if (lane == 0) {
-                sh.bad = bad;
-                sh.m_ref = rest.m;
-                sh.factor = rest.m > -INFINITY ? w * (all_mass * f_rest / total - (p_rest > 0.0f ? p_rest / rest.s : 0.0f)) : 0.0f;
-            }
-            // the listed tokens' gradients, to be written over those of the second pass
-            if (kGrad)
-#pragma unroll
-                for (int q = 0; q < kPerLane; ++q) now.x[q] = w * (all_mass * (e_listed[q] / total) - prob[q] * scale);
-        } else {
-            cluster_wait();
-        }
-        __syncthreads();
-        // ---- second pass: the gradient; the next row's pieces follow this one's
-        if (kGrad) {
-            G* grad = reinterpret_cast<G*>(p.grad) + row * p.grad_stride;
-            const Share<T> after(p, next < p.rows ? next : row, rank, size);
-            const bool bad = sh.bad, more = next < p.rows;
-            const float m_ref = bad ? NAN : sh.m_ref, factor = sh.factor;
-            const bool none = !bad && m_ref == -INFINITY;  // (-inf alone is not listed)
-            const float2 minus = make_float2(-m_ref, -m_ref), c2 = make_float2(p.c2, p.c2), f2 = make_float2(factor, factor);
-            G* out = grad + s.view.head + (int64_t)s.first * kVec;
-            const bool wide = reinterpret_cast<uintptr_t>(out) % (kVec * sizeof(G) < 16 ? kVec * sizeof(G) : 16) == 0;
-            const int all_batches = more ? max(n_batches, p.staged) : n_batches;
-            for (int b = 0; b < all_batches; ++b) {
-                uint4 w[kUnroll];
-#pragma unroll
-                for (int q = 0; q < kUnroll; ++q) {
-                    const int i = (b * kUnroll + q) * kThreads + tid;
-                    if (i < s.n) w[q] = b < p.staged ? stage[(b * kUnroll + q) * kThreads] : __ldcs(s.pieces() + i);
-                }
-#pragma unroll
-                for (int q = 0; q < kUnroll; ++q) {
-                    const int i = (b * kUnroll + q) * kThreads + tid;
-                    if (i >= s.n) continue;
-                    float x[kVec];
-                    Elem<T>::unpack(w[q], x);
-#pragma unroll
-                    for (int e = 0; e < kVec; e += 2) {
-                        const float2 a = mul2(add2(make_float2(x[e], x[e + 1]), minus), c2);
-                        const float2 y = mul2(make_float2(exp2_approx(a.x), exp2_approx(a.y)), f2);
-                        x[e] = none ? 0.0f : y.x;
-                        x[e + 1] = none ? 0.0f : y.y;
-                    }
-                    if (wide) {
-                        store_piece(out + (int64_t)i * kVec, x);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < kVec; ++e) out[(int64_t)i * kVec + e] = grad_of<G>(x[e]);
-                    }
-                }
-                if (more && b < p.staged) copy_batch(after, b);
-            }
-            if (v_edge >= 0) grad[v_edge] = grad_of<G>(none ? 0.0f : factor * exp2_approx((x_edge - m_ref) * p.c2));
-            if (warp == 0 && more) bad_list = mark(after, then);
+            unmark(s, now);
+            if (more) bad_list = mark(Share<T>(p, next, rank, size), then);
             __syncthreads();
-            if (warp == 0 && !bad)
+            // the listed tokens' own gradients over those of the second pass
+            if (kGrad && !j.bad) {
+                G* grad = reinterpret_cast<G*>(p.grad) + row * p.grad_stride;
 #pragma unroll
                 for (int q = 0; q < kPerLane; ++q)
-                    if (now.id[q] >= s.v0 && now.id[q] < s.v1) grad[now.id[q]] = grad_of<G>(now.x[q]);
-        } else {
-            if (warp == 0 && next < p.rows) bad_list = mark(Share<T>(p, next, rank, size), then);
-            __syncthreads();
+                    if (now.id[q] >= s.v0 && now.id[q] < s.v1)
+                        grad[now.id[q]] = grad_of<G>(w * (j.all_mass * (e_listed[q] * j.f_listed / j.total) - prob[q] * scale));
+            }
+            now = then;
         }
-        now = then;
         row = next;
         weight = next_weight;
     }
@@ -463,7 +489,7 @@ cudaError_t launch_distill(DistillParams p, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kAllThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -472,14 +498,11 @@ cudaError_t launch_distill(DistillParams p, cudaStream_t stream) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    int clusters = p.rows;
-    if (p.grad) {  // as many as there is room for at a time: they walk down the rows
-        cfg.gridDim = dim3((unsigned)ctas);
-        int room = 0;
-        if ((e = cudaOccupancyMaxActiveClusters(&room, fn, &cfg)) != cudaSuccess) return e;
-        clusters = std::min(clusters, std::max(1, room));
-    }
-    cfg.gridDim = dim3((unsigned)(clusters * (int64_t)ctas));
+    // as many clusters as there is room for at a time: they walk down the rows
+    cfg.gridDim = dim3((unsigned)ctas);
+    int room = 0;
+    if ((e = cudaOccupancyMaxActiveClusters(&room, fn, &cfg)) != cudaSuccess) return e;
+    cfg.gridDim = dim3((unsigned)(std::min(p.rows, std::max(1, room)) * ctas));
     void* args[] = {&p};
     return cudaLaunchKernelExC(&cfg, fn, args);
 }

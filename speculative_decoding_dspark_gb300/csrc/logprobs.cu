@@ -183,34 +183,22 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsParams
             const int i = i0 + q * kThreads;
             w[q] = load_piece<T>(view.base, i, end);
         }
-        float x[kUnroll * kVec];
-#pragma unroll
-        for (int q = 0; q < kUnroll; ++q) Elem<T>::unpack(w[q], x + q * kVec);
-        const float top = soft_add<kEntropy>(t, x, p.c2);
+        const float top = soft_add<T, kEntropy>(t, w, p.c2);
         if (kTop) batch_max[batch * kThreads + tid] = top;
     }
     const int v_edge = view.edge(tid, rank == 0, rank == size - 1);
-    const float x_edge[2] = {v_edge >= 0 ? view.at(v_edge) : -INFINITY, -INFINITY};
-    soft_add<kEntropy>(t, x_edge, p.c2);
+    const float x_edge = v_edge >= 0 ? view.at(v_edge) : -INFINITY;
+    soft_add_one<kEntropy>(t, x_edge, p.c2);
     if (kTop) sh.maxima[tid] = t.m;
     // ---- joined over the CTA
     {
-        SoftSum a = t;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            SoftSum b;
-            b.m = shfl_xor(a.m, o);
-            b.s = shfl_xor(a.s, o);
-            if (kEntropy) b.u = shfl_xor(a.u, o);
-            soft_merge<kEntropy>(a, b, p.c2);
-        }
+        const SoftSum a = soft_join<kEntropy, 32>(t, p.c2);
         if (lane == 0) sh.part[warp] = a;
     }
     __syncthreads();
-    if (tid == 0) {
-        SoftSum a = sh.part[0];
-        for (int w = 1; w < kWarps; ++w) soft_merge<kEntropy>(a, sh.part[w], p.c2);
-        sh.row = a;
+    if (warp == 0) {
+        const SoftSum a = soft_join<kEntropy, kWarps>(lane < kWarps ? sh.part[lane] : SoftSum(), p.c2);
+        if (lane == 0) sh.row = a;
     }
     if (kTop) {
         // the thread whose maximum is the K-th largest (of equal ones the later thread is lower)
@@ -224,16 +212,15 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsParams
     }
     cluster_sync();
     // ---- joined over the cluster, by its first CTA; the bound by all
-    SoftSum all = sh.row;
-    if (rank == 0 && size > 1) {
-        for (uint32_t c = 1; c < size; ++c) {
-            const uint32_t a = cluster_map(&sh.row, c);
-            SoftSum b;
-            b.m = cluster_ld_f32(a + offsetof(SoftSum, m));
-            b.s = cluster_ld_f32(a + offsetof(SoftSum, s));
-            b.u = cluster_ld_f32(a + offsetof(SoftSum, u));
-            soft_merge<kEntropy>(all, b, p.c2);
+    SoftSum all;
+    if (rank == 0) {
+        if ((uint32_t)lane < size) {
+            const uint32_t a = cluster_map(&sh.row, lane);
+            all.m = cluster_ld_f32(a + offsetof(SoftSum, m));
+            all.s = cluster_ld_f32(a + offsetof(SoftSum, s));
+            all.u = cluster_ld_f32(a + offsetof(SoftSum, u));
         }
+        all = soft_join<kEntropy, 32>(all, p.c2);
     }
     if (kTop) {
         float bound = -INFINITY;
@@ -245,17 +232,20 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsParams
                 if (c < (uint32_t)kCandidates) cluster_st_u64(list + 8 * c, rank_key(x, v));
             }
         };
-        offer(x_edge[0], v_edge);
+        offer(x_edge, v_edge);
         for (int b = 0; b < batch; ++b) {
             if (!(batch_max[b * kThreads + tid] >= bound)) continue;
 #pragma unroll 1
             for (int q = 0; q < kUnroll; ++q) {
                 const int i = first + tid + (b * kUnroll + q) * kThreads;
                 if (i >= end) break;
-                float x[kVec];
-                Elem<T>::unpack(__ldcs(view.base + i), x);
+                const uint4 w = __ldcs(view.base + i);
 #pragma unroll
-                for (int e = 0; e < kVec; ++e) offer(x[e], view.head + i * kVec + e);
+                for (int e = 0; e < kVec; e += 2) {
+                    const float2 x = Elem<T>::pair(w, e / 2);
+                    offer(x.x, view.head + i * kVec + e);
+                    offer(x.y, view.head + i * kVec + e + 1);
+                }
             }
         }
     }
@@ -283,7 +273,8 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsParams
             for (int o = 0; o < found; ++o) place += sh.cand[o] > mine;
             if (place < p.top_k) {
                 p.top_ids[n * p.top_k + place] = (int32_t)(0xFFFFFFFFu - (uint32_t)mine);
-                p.top_logprobs[n * p.top_k + place] = (of_order((uint32_t)(mine >> 32)) - all.m) * p.invT - log_s;
+                p.top_logprobs[n * p.top_k + place] = 
+                    (of_order((uint32_t)(mine >> 32)) - all.m) * p.invT - log_s;
             }
         }
         for (int k = found + tid; k < p.top_k; k += kThreads) {

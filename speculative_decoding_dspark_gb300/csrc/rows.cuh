@@ -26,6 +26,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return y;
 }
 
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
 // ---- clusters ---------------------------------------------------------------
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -69,6 +75,9 @@ __device__ __forceinline__ uint32_t cluster_atomic_add(uint32_t a, uint32_t x) {
 __device__ __forceinline__ void cluster_st_f32(uint32_t a, float x) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(x) : "memory");
 }
+__device__ __forceinline__ void cluster_st_f32x2(uint32_t a, float x, float y) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(x), "f"(y) : "memory");
+}
 __device__ __forceinline__ void cluster_st_u64(uint32_t a, uint64_t x) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(x) : "memory");
 }
@@ -79,22 +88,52 @@ template <> struct Elem<float> {
     static constexpr int kVec = 4;
     static constexpr uint32_t kMinusInf = 0xFF800000u;  // a 32-bit word of them
     static __device__ __forceinline__ float to_float(float x) { return x; }
-    static __device__ __forceinline__ void unpack(const uint4& w, float* f) {
-        f[0] = __uint_as_float(w.x); f[1] = __uint_as_float(w.y);
-        f[2] = __uint_as_float(w.z); f[3] = __uint_as_float(w.w);
+    // Elements 2 i and 2 i + 1 of a piece.
+    static __device__ __forceinline__ float2 pair(const uint4& w, int i) {
+        return i == 0 ? make_float2(__uint_as_float(w.x), __uint_as_float(w.y))
+                      : make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
+    }
+    static __device__ __forceinline__ uint4 without(const uint4& w, uint32_t mask) {  // -inf where mask has a bit
+        return make_uint4(mask & 1 ? kMinusInf : w.x, mask & 2 ? kMinusInf : w.y, mask & 4 ? kMinusInf : w.z,
+                          mask & 8 ? kMinusInf : w.w);
+    }
+    template <int N>
+    static __device__ __forceinline__ float largest(const uint4 (&w)[N]) {
+        float m = __uint_as_float(w[0].x);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            m = max3_nan(m, __uint_as_float(w[i].x), __uint_as_float(w[i].y));
+            m = max3_nan(m, __uint_as_float(w[i].z), __uint_as_float(w[i].w));
+        }
+        return m;
     }
 };
 template <> struct Elem<uint16_t> {
     static constexpr int kVec = 8;
     static constexpr uint32_t kMinusInf = 0xFF80FF80u;
     static __device__ __forceinline__ float to_float(uint16_t x) { return bf16_bits_to_float(x); }
-    static __device__ __forceinline__ void unpack(const uint4& w, float* f) {
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    static __device__ __forceinline__ float2 pair(const uint4& w, int i) {
+        const uint32_t u = i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
+        return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+    }
+    static __device__ __forceinline__ uint32_t without(uint32_t u, uint32_t mask) {
+        const uint32_t off = (mask & 1 ? 0xFFFFu : 0u) | (mask & 2 ? 0xFFFF0000u : 0u);
+        return (u & ~off) | (kMinusInf & off);
+    }
+    static __device__ __forceinline__ uint4 without(const uint4& w, uint32_t mask) {
+        return make_uint4(without(w.x, mask), without(w.y, mask >> 2), without(w.z, mask >> 4), without(w.w, mask >> 6));
+    }
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+        uint32_t y;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+        return y;
+    }
+    template <int N>
+    static __device__ __forceinline__ float largest(const uint4 (&w)[N]) {
+        uint32_t m = max2(max2(w[0].x, w[0].y), max2(w[0].z, w[0].w));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(u[i] << 16);
-            f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-        }
+        for (int i = 1; i < N; ++i) m = max2(m, max2(max2(w[i].x, w[i].y), max2(w[i].z, w[i].w)));
+        return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
     }
 };
 
@@ -131,72 +170,84 @@ __device__ __forceinline__ uint4 load_piece(const uint4* base, int i, int end) {
 
 // ---- the running softmax sums of a row --------------------------------------------
 // m the largest x, s = sum 2^a and u = sum a 2^a over the x seen, a = (x - m) c2.
-// The difference comes first: rows whose values are all near the type's lowest
-// keep their sums (x c2 alone would overflow).  A NaN makes s a NaN.
+// The difference comes first: the largest value's a is 0, and rows whose values are
+// all near the type's lowest keep their sums (x c2 alone would overflow).  A NaN
+// makes s a NaN.
 struct SoftSum {
     float m = -INFINITY, s = 0.0f, u = 0.0f;
 };
 
-template <bool kEntropy>
-__device__ __forceinline__ void soft_merge(SoftSum& a, const SoftSum& b, float c2) {
-    if (b.m == -INFINITY) {
-        a.s += b.s;  // nothing, or a NaN
-        return;
+// The sums of kWidth neighbouring lanes, in each of them: the maximum first, then
+// each lane's sums brought to it.
+template <bool kEntropy, int kWidth>
+__device__ __forceinline__ SoftSum soft_join(const SoftSum& t, float c2) {
+    SoftSum a;
+    a.m = t.m;
+#pragma unroll
+    for (int o = kWidth / 2; o > 0; o >>= 1) a.m = fmaxf(a.m, shfl_xor(a.m, o));
+    const bool none = t.m == -INFINITY;  // (s is 0, or a NaN)
+    const float d = none ? 0.0f : fmaxf((t.m - a.m) * c2, -200.0f), f = exp2_approx(d);
+    a.s = f * t.s;
+    if (kEntropy) a.u = f * (t.u + d * t.s);
+#pragma unroll
+    for (int o = kWidth / 2; o > 0; o >>= 1) {
+        a.s += shfl_xor(a.s, o);
+        if (kEntropy) a.u += shfl_xor(a.u, o);
     }
-    if (a.m == -INFINITY) {
-        const float s = a.s;
-        a = b;
-        a.s += s;
-        return;
-    }
-    const float m = fmaxf(a.m, b.m);
-    const float da = fmaxf((a.m - m) * c2, -200.0f), db = fmaxf((b.m - m) * c2, -200.0f);
-    const float fa = exp2_approx(da), fb = exp2_approx(db);
-    if (kEntropy) a.u = fa * (a.u + da * a.s) + fb * (b.u + db * b.s);
-    a.s = fa * a.s + fb * b.s;
-    a.m = m;
+    return a;
 }
 
-// N more values.  Their largest comes first, so that one rescaling serves all.
-template <bool kEntropy, int N>
-__device__ __forceinline__ float soft_add(SoftSum& t, const float (&x)[N], float c2) {
-    float g[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) g[i] = x[i];
-#pragma unroll
-    for (int o = N / 2; o > 0; o /= 2)
-#pragma unroll
-        for (int i = 0; i < o; ++i) g[i] = max_nan(g[i], g[i + o]);
-    const float top = g[0];
-    if (!(top <= t.m)) {
-        if (top != top) {
-            t.s = top;
-        } else {
-            if (t.m != -INFINITY) {
-                const float d = fmaxf((t.m - top) * c2, -200.0f), f = exp2_approx(d);
-                if (kEntropy) t.u = f * (t.u + d * t.s);
-                t.s *= f;
-            }
-            t.m = top;
-        }
+// `top`, a new value or the largest of several, may be the new maximum.
+template <bool kEntropy>
+__device__ __forceinline__ void soft_raise(SoftSum& t, float top, float c2) {
+    if (top <= t.m) return;
+    if (top != top) {
+        t.s = top;
+        return;
     }
+    if (t.m != -INFINITY) {
+        const float d = fmaxf((t.m - top) * c2, -200.0f), f = exp2_approx(d);
+        if (kEntropy) t.u = f * (t.u + d * t.s);
+        t.s *= f;
+    }
+    t.m = top;
+}
+
+// N more pieces; returns their largest value.  It comes first, so that one rescaling serves all.
+template <typename T, bool kEntropy, int N>
+__device__ __forceinline__ float soft_add(SoftSum& t, const uint4 (&w)[N], float c2) {
+    const float top = Elem<T>::largest(w);
+    soft_raise<kEntropy>(t, top, c2);
     if (t.m == -INFINITY) return top;
-    const float2 minus = make_float2(-t.m, -t.m), scale = make_float2(c2, c2);
-    float2 s = make_float2(0.0f, 0.0f), u = make_float2(0.0f, 0.0f);
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-        float2 a = mul2(add2(make_float2(x[i], x[i + 1]), minus), scale);
+    float2 s0 = make_float2(0.0f, 0.0f), s1 = s0, u0 = s0;
+    auto add = [&](float2 a, float2& s) {
         if (kEntropy) {  // (2^-200 is zero, and so is its product)
             a.x = fmaxf(a.x, -200.0f);
             a.y = fmaxf(a.y, -200.0f);
         }
         const float2 e = make_float2(exp2_approx(a.x), exp2_approx(a.y));
         s = add2(s, e);
-        if (kEntropy) u = fma2(e, a, u);
-    }
-    t.s += s.x + s.y;
-    if (kEntropy) t.u += u.x + u.y;
+        if (kEntropy) u0 = fma2(e, a, u0);
+    };
+    const float2 scale = make_float2(c2, c2), minus = make_float2(-t.m, -t.m);
+#pragma unroll
+    for (int q = 0; q < N; ++q)
+#pragma unroll
+        for (int i = 0; i < Elem<T>::kVec / 2; ++i) add(mul2(add2(Elem<T>::pair(w[q], i), minus), scale), i & 1 ? s1 : s0);
+    s0 = add2(s0, s1);
+    t.s += s0.x + s0.y;
+    if (kEntropy) t.u += u0.x + u0.y;
     return top;
+}
+
+// One more value.
+template <bool kEntropy>
+__device__ __forceinline__ void soft_add_one(SoftSum& t, float x, float c2) {
+    soft_raise<kEntropy>(t, x, c2);
+    if (t.m == -INFINITY) return;
+    const float a = fmaxf((x - t.m) * c2, -200.0f), e = exp2_approx(a);
+    t.s += e;
+    if (kEntropy) t.u += e * a;
 }
 
 }  // namespace dspark
