@@ -5,14 +5,17 @@
 //   lse = t_m + log s,  logprob = t_token - lse,  entropy = log s - sum (t - t_m) exp(t - t_m) / s
 // in one pass with the running maximum and sums of each thread, joined at the end.
 //
-// The K best: a thread's largest value is one of the row's values, so the K-th
-// largest of the threads' maxima is a bound that at least K values reach, and
-// few more do.  The pass leaves the maximum of every batch of 64 bytes in shared
-// memory; only batches whose maximum reaches the bound are looked at again, and
-// their values that reach it (the candidates) are ranked by counting: the value
-// falls, then the place rises.  A row with more candidates than the list holds
-// (equal values in their hundreds) has its bound found by counting the values'
-// bits from the top, and equal values taken in the order of their places.
+// The K best: a thread's largest value is one of the row's values, so whatever K
+// of the threads' maxima reach, at least K values reach: a bound found by bisecting
+// the values' bits until K maxima or few more reach it (one warp, the maxima in its
+// registers).  In a cluster of C CTAs each finds the bound that K / C of its own
+// maxima reach, and the lowest serves.  The pass leaves the maximum of every batch
+// of 64 bytes in shared memory; only batches whose maximum reaches the bound are
+// read again (from L2, by as many threads as there are pieces), and the values that
+// reach it, the candidates, are ranked by counting: the value falls, then the place
+// rises.  A row with more candidates than the list holds (equal values in their
+// hundreds) has its bound found by counting the values' bits from the top, and
+// equal values taken in the order of their places.
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -25,6 +28,8 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 4;       // pieces of a batch
 constexpr int kCandidates = 1024;
+constexpr int kHits = 1024;
+constexpr int kSms = 152;
 
 __device__ __forceinline__ uint32_t order_of(float x) {
     const uint32_t b = __float_as_uint(x + 0.0f);  // (-0 is 0)
@@ -42,13 +47,43 @@ struct Shared {
     float maxima[kThreads];
     SoftSum part[kWarps];
     SoftSum row;      // this CTA's part of the row
-    float bound;      // its K-th largest thread maximum
+    float bound;      // what at least K / C of its threads' maxima reach
     uint32_t n_cand;  // leader: candidates of all CTAs
+    uint32_t n_hits;  // batches whose maximum reaches the bound
+    uint32_t hits[kHits];
     uint32_t hist[256];
     uint32_t found;
     uint32_t count[kWarps];
     uint32_t prefix, need;
 };
+
+// (one warp) A value that at least `want` of the CTA's maxima reach, and not many
+// more: found when at most a quarter more do, or when no bit is left.
+__device__ __forceinline__ float bound_of(const float* maxima, int want) {
+    uint32_t k[kWarps], low = 0xFFFFFFFFu, high = 0;
+#pragma unroll
+    for (int q = 0; q < kWarps; ++q) {
+        k[q] = order_of(maxima[q * 32 + (threadIdx.x & 31)]);
+        low = min(low, k[q]);
+        high = max(high, k[q]);
+    }
+    low = __reduce_min_sync(0xFFFFFFFFu, low);    // (all reach it)
+    high = __reduce_max_sync(0xFFFFFFFFu, high) + 1;  // (none does)
+    while (high - low > 1) {
+        const uint32_t mid = low + (high - low) / 2;
+        int n = 0;
+#pragma unroll
+        for (int q = 0; q < kWarps; ++q) n += k[q] >= mid;
+        n = __reduce_add_sync(0xFFFFFFFFu, n);
+        if (n >= want) {
+            low = mid;
+            if (n <= want + 1 + want / 4) break;
+        } else {
+            high = mid;
+        }
+    }
+    return of_order(low);
+}
 
 // The K best when the list was too short; leaves exactly K of them in sh.cand.
 template <typename T>
@@ -170,8 +205,8 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsParams
     const T* row = reinterpret_cast<const T*>(p.logits) + n * p.stride;
     const float x_token = Elem<T>::to_float(row[token]);
     const RowView<T> view(row, p.V);
-    const int first = (int)((int64_t)view.pieces * rank / size), end = (int)((int64_t)view.pieces * (rank + 1) / size);
-    if (kTop && rank == 0 && tid == 0) sh.n_cand = 0;
+    const int first = (int)(view.pieces * rank / size), end = (int)(view.pieces * (rank + 1) / size);
+    if (kTop && tid == 0) sh.n_cand = sh.n_hits = 0;
 
     // ---- one pass over this CTA's pieces
     SoftSum t;
@@ -200,17 +235,14 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsParams
         const SoftSum a = soft_join<kEntropy, kWarps>(lane < kWarps ? sh.part[lane] : SoftSum(), p.c2);
         if (lane == 0) sh.row = a;
     }
-    if (kTop) {
-        // the thread whose maximum is the K-th largest (of equal ones the later thread is lower)
-        int above = 0;
-        for (int j = 0; j < kThreads; j += 4) {
-            const float4 o = *reinterpret_cast<const float4*>(sh.maxima + j);
-            above += (o.x > t.m || (o.x == t.m && j < tid)) + (o.y > t.m || (o.y == t.m && j + 1 < tid)) +
-                     (o.z > t.m || (o.z == t.m && j + 2 < tid)) + (o.w > t.m || (o.w == t.m && j + 3 < tid));
-        }
-        if (above == p.top_k - 1) sh.bound = t.m;
+    if (kTop && warp == 1) {
+        const float bound = bound_of(sh.maxima, (p.top_k + size - 1) / size);
+        if (lane == 0) sh.bound = bound;
     }
-    cluster_sync();
+    if (size > 1)
+        cluster_sync();
+    else
+        __syncthreads();
     // ---- joined over the cluster, by its first CTA; the bound by all
     SoftSum all;
     if (rank == 0) {
@@ -223,33 +255,51 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsParams
         all = soft_join<kEntropy, 32>(all, p.c2);
     }
     if (kTop) {
-        float bound = -INFINITY;
-        for (uint32_t c = 0; c < size; ++c) bound = fmaxf(bound, cluster_ld_f32(cluster_map(&sh.bound, c)));
+        float bound = sh.bound;
+        for (uint32_t c = 0; c < size; ++c) bound = fminf(bound, cluster_ld_f32(cluster_map(&sh.bound, c)));
         const uint32_t list = cluster_map(sh.cand, 0), count = cluster_map(&sh.n_cand, 0);
         auto offer = [&](float x, int v) {
-            if (x >= bound && x > -INFINITY) {
-                const uint32_t c = cluster_atomic_add(count, 1u);
-                if (c < (uint32_t)kCandidates) cluster_st_u64(list + 8 * c, rank_key(x, v));
-            }
+            const uint32_t c = size > 1 ? cluster_atomic_add(count, 1u) : atomicAdd(&sh.n_cand, 1u);
+            if (c < (uint32_t)kCandidates) cluster_st_u64(list + 8 * c, rank_key(x, v));
         };
-        offer(x_edge, v_edge);
-        for (int b = 0; b < batch; ++b) {
-            if (!(batch_max[b * kThreads + tid] >= bound)) continue;
-#pragma unroll 1
-            for (int q = 0; q < kUnroll; ++q) {
-                const int i = first + tid + (b * kUnroll + q) * kThreads;
-                if (i >= end) break;
+        if (x_edge >= bound && x_edge > -INFINITY) offer(x_edge, v_edge);
+        if (t.m >= bound)
+            for (int b = 0; b < batch; ++b) {
+                const float top = batch_max[b * kThreads + tid];
+                if (top >= bound && top > -INFINITY) {
+                    const uint32_t h = atomicAdd(&sh.n_hits, 1u);
+                    if (h < (uint32_t)kHits) sh.hits[h] = first + b * kUnroll * kThreads + tid;
+                }
+            }
+        __syncthreads();
+        const int n_hits = (int)sh.n_hits;
+        if (n_hits > kHits) {  // (as many candidates, then)
+            if (tid == 0) cluster_atomic_add(count, (uint32_t)kCandidates + 1);
+        } else {
+            for (int h = tid; h < n_hits * kUnroll; h += kThreads) {
+                const int i = (int)sh.hits[h / kUnroll] + h % kUnroll * kThreads;
+                if (i >= end) continue;
                 const uint4 w = __ldcs(view.base + i);
+                uint32_t reach = 0;
 #pragma unroll
                 for (int e = 0; e < kVec; e += 2) {
                     const float2 x = Elem<T>::pair(w, e / 2);
-                    offer(x.x, view.head + i * kVec + e);
-                    offer(x.y, view.head + i * kVec + e + 1);
+                    reach |= (x.x >= bound ? 1u << e : 0u) | (x.y >= bound ? 2u << e : 0u);
+                }
+                for (; reach; reach &= reach - 1) {
+                    const int e = __ffs(reach) - 1, v = view.head + i * kVec + e;
+                    const float x = view.at(v);
+                    if (x > -INFINITY) offer(x, v);
                 }
             }
         }
+        if (size > 1)
+            cluster_sync();
+        else
+            __syncthreads();
+    } else if (size > 1) {
+        cluster_sync();
     }
-    if (size > 1 || kTop) cluster_sync();
     if (rank != 0) return;
     // ---- the row's outputs
     if (!(all.s > 0.0f && all.s < INFINITY) || all.m == INFINITY) {
@@ -267,14 +317,18 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsParams
     if (kTop) {
         if (sh.n_cand > (uint32_t)kCandidates) select_by_bits<T>(row, p.V, p.top_k, sh);
         const int found = (int)sh.n_cand;
-        for (int c = tid; c < found; c += kThreads) {
-            const uint64_t mine = sh.cand[c];
+        // four threads to a candidate, each against a quarter of the others
+        for (int c0 = 0; c0 < found; c0 += kThreads / 4) {
+            const int c = c0 + tid / 4;
+            const uint64_t mine = c < found ? sh.cand[c] : 0;
             int place = 0;
-            for (int o = 0; o < found; ++o) place += sh.cand[o] > mine;
-            if (place < p.top_k) {
+#pragma unroll 4
+            for (int o = tid & 3; o < found; o += 4) place += sh.cand[o] > mine;
+            place += shfl_xor(place, 1);
+            place += shfl_xor(place, 2);
+            if ((tid & 3) == 0 && c < found && place < p.top_k) {
                 p.top_ids[n * p.top_k + place] = (int32_t)(0xFFFFFFFFu - (uint32_t)mine);
-                p.top_logprobs[n * p.top_k + place] = 
-                    (of_order((uint32_t)(mine >> 32)) - all.m) * p.invT - log_s;
+                p.top_logprobs[n * p.top_k + place] = (of_order((uint32_t)(mine >> 32)) - all.m) * p.invT - log_s;
             }
         }
         for (int k = found + tid; k < p.top_k; k += kThreads) {
@@ -296,11 +350,18 @@ cudaError_t launch_logprobs(const LogprobsParams& p, cudaStream_t stream) {
     const int vec = p.dtype == DSPARK_F32 ? 4 : 8;
     const int64_t places = p.cu ? (int64_t)p.R * p.width : p.rows;
     int ctas = 1;
+    const int64_t pieces = p.V / vec;
     auto smem_of = [&](int c) {
-        const int64_t per = ((int64_t)p.V / vec + c - 1) / c;
+        const int64_t per = (pieces + c - 1) / c;
         return (size_t)(p.top_k ? (per + kUnroll * kThreads - 1) / (kUnroll * kThreads) * kThreads * sizeof(float) : 0);
     };
-    while (ctas < 8 && smem_of(ctas) > 48 * 1024) ctas *= 2;
+    // Rows are shared by more CTAs until there are eight to an SM (of a packed batch's places about half have a token),
+    // as long as a CTA keeps 4096 pieces, or 1024 where an SM would have none.
+    const int64_t likely = p.cu ? (places + 1) / 2 : places;
+    auto larger = [&](int c) {
+        return smem_of(c) > 48 * 1024 || (likely * c < 8 * kSms && pieces / (2 * c) >= (likely * c < kSms ? 1024 : 4096));
+    };
+    while (ctas < 8 && larger(ctas)) ctas *= 2;
     const size_t smem = smem_of(ctas);
     const void* fn = p.dtype == DSPARK_F32 ? kernel_of<float>(p.entropy, p.top_k > 0)
                                            : kernel_of<uint16_t>(p.entropy, p.top_k > 0);
