@@ -10,7 +10,7 @@
 // the values' bits until K maxima or few more reach it (one warp, the maxima in its
 // registers).  In a cluster of C CTAs each finds the bound that K / C of its own
 // maxima reach, and the lowest serves.  The pass leaves the maximum of every batch
-// of 64 bytes in shared memory; only batches whose maximum reaches the bound are
+// of 32 elements in shared memory; only batches whose maximum reaches the bound are
 // read again (from L2, by as many threads as there are pieces), and the values that
 // reach it, the candidates, are ranked by counting: the value falls, then the place
 // rises.  A row with more candidates than the list holds (equal values in their
@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 4;       // pieces of a batch
+constexpr int kBatch = 32;       // elements of a batch (a thread's, of as many pieces)
 constexpr int kCandidates = 1024;
 constexpr int kHits = 1024;
 constexpr int kSms = 152;
@@ -167,7 +167,7 @@ __device__ __forceinline__ void fill_row(const LogprobsParams& p, int64_t n, flo
 
 template <typename T, bool kEntropy, bool kTop>
 __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsParams p) {
-    constexpr int kVec = Elem<T>::kVec;
+    constexpr int kVec = Elem<T>::kVec, kUnroll = kBatch / kVec;
     extern __shared__ float batch_max[];  // [batches of this CTA][thread]
     __shared__ Shared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -353,7 +353,7 @@ cudaError_t launch_logprobs(const LogprobsParams& p, cudaStream_t stream) {
     const int64_t pieces = p.V / vec;
     auto smem_of = [&](int c) {
         const int64_t per = (pieces + c - 1) / c;
-        return (size_t)(p.top_k ? (per + kUnroll * kThreads - 1) / (kUnroll * kThreads) * kThreads * sizeof(float) : 0);
+        return (size_t)(p.top_k ? (per * vec + kBatch * kThreads - 1) / (kBatch * kThreads) * kThreads * sizeof(float) : 0);
     };
     // Rows are shared by more CTAs until there are eight to an SM (of a packed batch's places about half have a token),
     // as long as a CTA keeps 4096 pieces, or 1024 where an SM would have none.
