@@ -90,14 +90,14 @@ __device__ __forceinline__ void store_piece(uint16_t* p, const float (&x)[8]) {
 
 // This CTA's share of a gradient row of weight 0.
 template <typename G>
-__device__ __forceinline__ void clear_grad(G* g, int V, uint32_t rank, uint32_t size) {
+__device__ __forceinline__ void clear_grad(G* g, int V, int rank, int size) {
     constexpr int kVec = 16 / sizeof(G);
     const int head = min(V, (int)(((16 - (reinterpret_cast<uintptr_t>(g) & 15)) & 15) / sizeof(G)));
     const int pieces = (V - head) / kVec, first = pieces * rank / size, end = pieces * (rank + 1) / size;
     uint4* wide = reinterpret_cast<uint4*>(g + head);
     for (int i = first + threadIdx.x; i < end; i += kAllThreads) __stcs(wide + i, make_uint4(0, 0, 0, 0));
-    if (rank == 0 && threadIdx.x < head) g[threadIdx.x] = G(0);
-    const int tail = head + pieces * kVec + threadIdx.x;
+    if (rank == 0 && (int)threadIdx.x < head) g[threadIdx.x] = G(0);
+    const int tail = head + pieces * kVec + (int)threadIdx.x;
     if (rank == size - 1 && tail < V) g[tail] = G(0);
 }
 
@@ -121,13 +121,13 @@ struct Share {
     RowView<T> view;
     int first, n;      // its pieces
     int v0, v1;        // its elements, the row's edges among them
-    __device__ __forceinline__ Share(const DistillParams& p, int64_t row, uint32_t rank, uint32_t size)
+    __device__ __forceinline__ Share(const DistillParams& p, int64_t row, int rank)
         : view(reinterpret_cast<const T*>(p.student) + row * p.stride, p.V) {
-        first = view.pieces * rank / size;
-        const int end = view.pieces * (rank + 1) / size;
+        first = view.pieces * rank >> p.log_ctas;
+        const int end = view.pieces * (rank + 1) >> p.log_ctas;
         n = end - first;
         v0 = rank == 0 ? 0 : view.head + first * Elem<T>::kVec;
-        v1 = rank == size - 1 ? p.V : view.head + end * Elem<T>::kVec;
+        v1 = rank + 1 == 1 << p.log_ctas ? p.V : view.head + end * Elem<T>::kVec;
     }
     __device__ __forceinline__ const uint4* pieces() const { return view.base + first; }
     // The bit of its element v (a word is kept for the edges on either side).
@@ -151,8 +151,8 @@ __global__ void __launch_bounds__(kAllThreads, kGrad ? 2 : 3) distill_kernel(con
     __shared__ Shared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const bool keeper = warp == kWarps;
-    const uint32_t rank = cluster_rank(), size = cluster_size();
-    const int clusters = gridDim.x / size;
+    const int rank = (int)cluster_rank(), size = 1 << p.log_ctas;
+    const int clusters = gridDim.x >> p.log_ctas;
     uint4* stage = dyn + tid;  // [p.staged batches][kUnroll][kThreads]
     uint32_t* bits = reinterpret_cast<uint32_t*>(dyn + p.staged * kBatch);
     for (int i = tid; i < p.bit_words; i += kAllThreads) bits[i] = 0;
@@ -169,12 +169,18 @@ __global__ void __launch_bounds__(kAllThreads, kGrad ? 2 : 3) distill_kernel(con
         }
         return n;
     };
-    auto copy_batch = [&](const Share<T>& s, int b) {
-        const uint4* from = s.pieces() + b * kBatch + tid;
-        const int left = s.n - b * kBatch - tid;
+    auto copy_batch = [&](const uint4* from, int n, int b) {  // of a row's n pieces from `from` on
+        const uint32_t to = tc::smem_u32(stage + b * kBatch);
+        const int left = n - b * kBatch - tid;
+        from += b * kBatch + tid;
+        if (left > (kUnroll - 1) * kThreads) {
 #pragma unroll
-        for (int q = 0; q < kUnroll; ++q)
-            if (q * kThreads < left) tc::cp_async_16(tc::smem_u32(stage + b * kBatch + q * kThreads), from + q * kThreads, 16);
+            for (int q = 0; q < kUnroll; ++q) tc::cp_async_16(to + q * kThreads * 16, from + q * kThreads, 16);
+        } else {
+#pragma unroll
+            for (int q = 0; q < kUnroll; ++q)
+                if (q * kThreads < left) tc::cp_async_16(to + q * kThreads * 16, from + q * kThreads, 16);
+        }
         tc::cp_async_commit();
     };
     // (keeper) a row's listed tokens
@@ -244,7 +250,7 @@ __global__ void __launch_bounds__(kAllThreads, kGrad ? 2 : 3) distill_kernel(con
         for (int q = 0; q < kEach; ++q)
             t.s += each[q].m == -INFINITY ? each[q].s : each[q].s * exp2_approx((each[q].m - t.m) * p.c2);
         j.rest = soft_join<false, 32>(t, p.c2);
-        const float bad_there = (uint32_t)lane < size ? sh.bad[parity][lane] : 0.0f;
+        const float bad_there = lane < size ? sh.bad[parity][lane] : 0.0f;
         j.m_all = fmaxf(kept.x_top, j.rest.m);
         j.f_rest = j.rest.m > -INFINITY ? exp2_approx((j.rest.m - j.m_all) * p.c2) : 0.0f;
         j.f_listed = kept.x_top > -INFINITY ? exp2_approx((kept.x_top - j.m_all) * p.c2) : 0.0f;
@@ -257,11 +263,11 @@ __global__ void __launch_bounds__(kAllThreads, kGrad ? 2 : 3) distill_kernel(con
         j.m_ref = none ? 0.0f : j.rest.m;
         j.factor = j.bad ? NAN
                    : none ? 0.0f
-                          : weight * p.invT * (j.all_mass * j.f_rest / j.total - (j.p_rest > 0.0f ? j.p_rest / j.rest.s : 0.0f));
+                          : weight * p.invT * (__fdividef(j.all_mass * j.f_rest, j.total) - (j.p_rest > 0.0f ? __fdividef(j.p_rest, j.rest.s) : 0.0f));
         return j;
     };
 
-    int64_t row = blockIdx.x / size;
+    int64_t row = blockIdx.x >> p.log_ctas;
     float weight = weight_of(row);
     row = active(row, weight);
     float ahead = weight_of(row + clusters);
@@ -269,22 +275,23 @@ __global__ void __launch_bounds__(kAllThreads, kGrad ? 2 : 3) distill_kernel(con
     bool bad_list = false;
     __syncthreads();
     if (row < p.rows) {
-        const Share<T> s(p, row, rank, size);
+        const Share<T> s(p, row, rank);
         if (keeper) {
             fetch(row, now);
             bad_list = mark(s, now);
         } else if (kGrad) {
-            for (int b = 0; b < p.staged; ++b) copy_batch(s, b);
+            for (int b = 0; b < p.staged; ++b) copy_batch(s.pieces(), s.n, b);
         }
     }
     __syncthreads();
 
+    Share<T> s(p, min(row, (int64_t)p.rows - 1), rank);
     for (int parity = 0; row < p.rows; parity ^= 1) {
-        const Share<T> s(p, row, rank, size);
         float next_weight = ahead;
         const int64_t next = active(row + clusters, next_weight);
         ahead = weight_of(next + clusters);
         const bool more = next < p.rows;
+        const Share<T> after(p, more ? next : row, rank);
         if (!keeper) {
             const int n_batches = s.batches();
             const int v_edge = warp == 0 ? s.view.edge(lane, rank == 0, rank == size - 1) : -1;
@@ -331,53 +338,55 @@ __global__ void __launch_bounds__(kAllThreads, kGrad ? 2 : 3) distill_kernel(con
             __syncwarp();
             // ---- to all CTAs of the cluster
             t = soft_join<false, 32>(t, p.c2);
-            if ((uint32_t)lane < size) cluster_st_f32x2(cluster_map(&sh.sums[parity][rank][warp], lane), t.m, t.s);
+            if (lane < size) cluster_st_f32x2(cluster_map(&sh.sums[parity][rank][warp], lane), t.m, t.s);
             __syncwarp();
             cluster_arrive();
             cluster_wait();
             // ---- second pass: the gradient; the next row's pieces follow this one's
             if (kGrad) {
                 G* grad = reinterpret_cast<G*>(p.grad) + row * p.grad_stride;
-                const Share<T> after(p, more ? next : row, rank, size);
                 const Joined j = joined(parity, weight);
                 const float m_ref = j.m_ref, factor = j.factor;
-                const float2 scale = make_float2(p.c2, p.c2), f2 = make_float2(factor, factor);
-                const float2 minus = make_float2(-m_ref, -m_ref);
+                const Two scale = two(p.c2, p.c2), f2 = two(factor, factor), minus = two(-m_ref, -m_ref);
                 G* out = grad + s.view.head + (int64_t)s.first * kVec;
+                const uint4* next_pieces = after.pieces();
                 const bool wide = reinterpret_cast<uintptr_t>(out) % (kVec * sizeof(G) < 16 ? kVec * sizeof(G) : 16) == 0;
                 const int all_batches = more ? max(n_batches, p.staged) : n_batches;
-                auto write = [&](const uint4& w, int64_t i) {
+                auto write = [&](const uint4& w, G* to) {
                     float x[kVec];
 #pragma unroll
                     for (int e = 0; e < kVec; e += 2) {
-                        const float2 y = Elem<T>::pair(w, e / 2);
-                        const float2 a = mul2(add2(y, minus), scale);
-                        const float2 g = mul2(make_float2(exp2_approx(a.x), exp2_approx(a.y)), f2);
+                        const float2 a = split(mul_two(add_two(Elem<T>::pair(w, e / 2), minus), scale));
+                        const float2 g = split(mul_two(two(exp2_approx(a.x), exp2_approx(a.y)), f2));
                         x[e] = g.x;
                         x[e + 1] = g.y;
                     }
                     if (wide) {
-                        store_piece(out + i * kVec, x);
+                        store_piece(to, x);
                     } else {
 #pragma unroll
-                        for (int e = 0; e < kVec; ++e) out[i * kVec + e] = grad_of<G>(x[e]);
+                        for (int e = 0; e < kVec; ++e) to[e] = grad_of<G>(x[e]);
                     }
                 };
                 for (int b = 0; b < all_batches; ++b) {
                     const int i0 = b * kBatch + tid, left = s.n - i0;
+                    G* to = out + (int64_t)i0 * kVec;
                     uint4 w[kUnroll];
                     if (left > (kUnroll - 1) * kThreads && b < p.staged) {
 #pragma unroll
                         for (int q = 0; q < kUnroll; ++q) w[q] = stage[b * kBatch + q * kThreads];
 #pragma unroll
-                        for (int q = 0; q < kUnroll; ++q) write(w[q], i0 + q * kThreads);
+                        for (int q = 0; q < kUnroll; ++q) write(w[q], to + q * kThreads * kVec);
                     } else {
-#pragma unroll 1
-                        for (int q = 0; q * kThreads < left && q < kUnroll; ++q)
-                            write(b < p.staged ? stage[b * kBatch + q * kThreads] : __ldcs(s.pieces() + i0 + q * kThreads),
-                                  i0 + q * kThreads);
+#pragma unroll
+                        for (int q = 0; q < kUnroll; ++q)
+                            if (q * kThreads < left)
+                                w[q] = b < p.staged ? stage[b * kBatch + q * kThreads] : __ldcs(s.pieces() + i0 + q * kThreads);
+#pragma unroll
+                        for (int q = 0; q < kUnroll; ++q)
+                            if (q * kThreads < left) write(w[q], to + q * kThreads * kVec);
                     }
-                    if (more && b < p.staged) copy_batch(after, b);
+                    if (more && b < p.staged) copy_batch(next_pieces, after.n, b);
                 }
                 if (v_edge >= 0) grad[v_edge] = grad_of<G>(factor * exp2_approx((x_edge - m_ref) * p.c2));
             }
@@ -419,7 +428,7 @@ __global__ void __launch_bounds__(kAllThreads, kGrad ? 2 : 3) distill_kernel(con
                 k.bad = bad_row ? 1.0f : 0.0f;
                 sh.kept[parity] = k;
             }
-            if ((uint32_t)lane < size) cluster_st_f32(cluster_map(&sh.bad[parity][rank], lane), bad_list ? 1.0f : 0.0f);
+            if (lane < size) cluster_st_f32(cluster_map(&sh.bad[parity][rank], lane), bad_list ? 1.0f : 0.0f);
             __syncwarp();
             cluster_arrive();
             cluster_wait();
@@ -442,7 +451,7 @@ __global__ void __launch_bounds__(kAllThreads, kGrad ? 2 : 3) distill_kernel(con
                 }
             }
             unmark(s, now);
-            if (more) bad_list = mark(Share<T>(p, next, rank, size), then);
+            if (more) bad_list = mark(after, then);
             __syncthreads();
             // the listed tokens' own gradients over those of the second pass
             if (kGrad && !j.bad) {
@@ -456,6 +465,7 @@ __global__ void __launch_bounds__(kAllThreads, kGrad ? 2 : 3) distill_kernel(con
         }
         row = next;
         weight = next_weight;
+        s = after;
     }
     cluster_sync();  // (no CTA ends while another may still write to its shared memory)
 }
@@ -483,6 +493,7 @@ cudaError_t launch_distill(DistillParams p, cudaStream_t stream) {
     while (ctas < kMaxCtas && larger(ctas)) ctas *= 2;
     p.staged = p.grad ? std::min<int64_t>(batches_of(ctas), (int64_t)((kShare - std::min(kShare, smem_of(ctas, 0))) / (kUnroll * kThreads * 16))) : 0;
     p.bit_words = bits_of(ctas);
+    p.log_ctas = ctas == 1 ? 0 : ctas == 2 ? 1 : ctas == 4 ? 2 : 3;
     const size_t smem = smem_of(ctas, p.staged);
     const void* fn = p.dtype == DSPARK_F32 ? kernel_of<float>(p.grad != nullptr, p.grad_dtype)
                                            : kernel_of<uint16_t>(p.grad != nullptr, p.grad_dtype);

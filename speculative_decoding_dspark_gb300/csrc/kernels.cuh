@@ -280,7 +280,7 @@ struct DistillParams {
     int64_t grad_stride;
     int grad_dtype;
     int staged;      // batches of a row that stay in shared memory for their gradient
-    int bit_words;
+    int bit_words, log_ctas;
     int32_t* dev_status;
 };
 

@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsParams
                 uint32_t reach = 0;
 #pragma unroll
                 for (int e = 0; e < kVec; e += 2) {
-                    const float2 x = Elem<T>::pair(w, e / 2);
+                    const float2 x = split(Elem<T>::pair(w, e / 2));
                     reach |= (x.x >= bound ? 1u << e : 0u) | (x.y >= bound ? 2u << e : 0u);
                 }
                 for (; reach; reach &= reach - 1) {

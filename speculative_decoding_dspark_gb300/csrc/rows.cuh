@@ -32,6 +32,34 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
     return y;
 }
 
+// Two floats in one 64-bit register, and the operations on both at once.
+using Two = unsigned long long;
+__device__ __forceinline__ Two two(float lo, float hi) {
+    Two y;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(lo), "f"(hi));
+    return y;
+}
+__device__ __forceinline__ float2 split(Two x) {
+    float2 y;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(y.x), "=f"(y.y) : "l"(x));
+    return y;
+}
+__device__ __forceinline__ Two add_two(Two a, Two b) {
+    Two y;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+    return y;
+}
+__device__ __forceinline__ Two mul_two(Two a, Two b) {
+    Two y;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+    return y;
+}
+__device__ __forceinline__ Two fma_two(Two a, Two b, Two c) {
+    Two y;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(a), "l"(b), "l"(c));
+    return y;
+}
+
 // ---- clusters ---------------------------------------------------------------
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -89,9 +117,8 @@ template <> struct Elem<float> {
     static constexpr uint32_t kMinusInf = 0xFF800000u;  // a 32-bit word of them
     static __device__ __forceinline__ float to_float(float x) { return x; }
     // Elements 2 i and 2 i + 1 of a piece.
-    static __device__ __forceinline__ float2 pair(const uint4& w, int i) {
-        return i == 0 ? make_float2(__uint_as_float(w.x), __uint_as_float(w.y))
-                      : make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
+    static __device__ __forceinline__ Two pair(const uint4& w, int i) {
+        return i == 0 ? two(__uint_as_float(w.x), __uint_as_float(w.y)) : two(__uint_as_float(w.z), __uint_as_float(w.w));
     }
     static __device__ __forceinline__ uint4 without(const uint4& w, uint32_t mask) {  // -inf where mask has a bit
         return make_uint4(mask & 1 ? kMinusInf : w.x, mask & 2 ? kMinusInf : w.y, mask & 4 ? kMinusInf : w.z,
@@ -112,9 +139,9 @@ template <> struct Elem<uint16_t> {
     static constexpr int kVec = 8;
     static constexpr uint32_t kMinusInf = 0xFF80FF80u;
     static __device__ __forceinline__ float to_float(uint16_t x) { return bf16_bits_to_float(x); }
-    static __device__ __forceinline__ float2 pair(const uint4& w, int i) {
+    static __device__ __forceinline__ Two pair(const uint4& w, int i) {
         const uint32_t u = i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
-        return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+        return two(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
     }
     static __device__ __forceinline__ uint32_t without(uint32_t u, uint32_t mask) {
         const uint32_t off = (mask & 1 ? 0xFFFFu : 0u) | (mask & 2 ? 0xFFFF0000u : 0u);
@@ -219,24 +246,28 @@ __device__ __forceinline__ float soft_add(SoftSum& t, const uint4 (&w)[N], float
     const float top = Elem<T>::largest(w);
     soft_raise<kEntropy>(t, top, c2);
     if (t.m == -INFINITY) return top;
-    float2 s0 = make_float2(0.0f, 0.0f), s1 = s0, u0 = s0;
-    auto add = [&](float2 a, float2& s) {
-        if (kEntropy) {  // (2^-200 is zero, and so is its product)
-            a.x = fmaxf(a.x, -200.0f);
-            a.y = fmaxf(a.y, -200.0f);
-        }
-        const float2 e = make_float2(exp2_approx(a.x), exp2_approx(a.y));
-        s = add2(s, e);
-        if (kEntropy) u0 = fma2(e, a, u0);
-    };
-    const float2 scale = make_float2(c2, c2), minus = make_float2(-t.m, -t.m);
+    Two s0 = two(0.0f, 0.0f), s1 = s0, u0 = s0;
+    const Two scale = two(c2, c2), minus = two(-t.m, -t.m);
 #pragma unroll
     for (int q = 0; q < N; ++q)
 #pragma unroll
-        for (int i = 0; i < Elem<T>::kVec / 2; ++i) add(mul2(add2(Elem<T>::pair(w[q], i), minus), scale), i & 1 ? s1 : s0);
-    s0 = add2(s0, s1);
-    t.s += s0.x + s0.y;
-    if (kEntropy) t.u += u0.x + u0.y;
+        for (int i = 0; i < Elem<T>::kVec / 2; ++i) {
+            float2 a = split(mul_two(add_two(Elem<T>::pair(w[q], i), minus), scale));
+            if (kEntropy) {  // (2^-200 is zero, and so is its product)
+                a.x = fmaxf(a.x, -200.0f);
+                a.y = fmaxf(a.y, -200.0f);
+            }
+            const Two e = two(exp2_approx(a.x), exp2_approx(a.y));
+            if (i & 1) s1 = add_two(s1, e);
+            else s0 = add_two(s0, e);
+            if (kEntropy) u0 = fma_two(e, two(a.x, a.y), u0);
+        }
+    const float2 s = split(add_two(s0, s1));
+    t.s += s.x + s.y;
+    if (kEntropy) {
+        const float2 u = split(u0);
+        t.u += u.x + u.y;
+    }
     return top;
 }
 
