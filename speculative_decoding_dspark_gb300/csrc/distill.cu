@@ -309,12 +309,16 @@ __global__ void __launch_bounds__(kAllThreads, kGrad ? 2 : 3) distill_kernel(con
                 }
                 soft_add<T, false>(t, w, p.c2);
             };
+            const int half = p.staged / 2;  // (two waits a row: one for each batch cost 2 %)
             for (int b = 0; b < n_batches; ++b) {
                 constexpr uint32_t k = Elem<T>::kMinusInf;
                 const int left = s.n - b * kBatch - tid;
                 uint4 w[kUnroll];
                 if (kGrad && b < p.staged) {
-                    copies_left(p.staged - 1 - b);
+                    if (b == 0)
+                        copies_left(half);
+                    else if (b == p.staged - half)
+                        copies_left(0);
                     if (left > (kUnroll - 1) * kThreads) {
 #pragma unroll
                         for (int q = 0; q < kUnroll; ++q) w[q] = stage[b * kBatch + q * kThreads];
@@ -352,7 +356,7 @@ __global__ void __launch_bounds__(kAllThreads, kGrad ? 2 : 3) distill_kernel(con
                 const uint4* next_pieces = after.pieces();
                 const bool wide = reinterpret_cast<uintptr_t>(out) % (kVec * sizeof(G) < 16 ? kVec * sizeof(G) : 16) == 0;
                 const int all_batches = more ? max(n_batches, p.staged) : n_batches;
-                auto write = [&](const uint4& w, G* to) {
+                auto write = [&](const uint4& w, G* to, bool whole) {
                     float x[kVec];
 #pragma unroll
                     for (int e = 0; e < kVec; e += 2) {
@@ -361,7 +365,7 @@ __global__ void __launch_bounds__(kAllThreads, kGrad ? 2 : 3) distill_kernel(con
                         x[e] = g.x;
                         x[e + 1] = g.y;
                     }
-                    if (wide) {
+                    if (whole) {
                         store_piece(to, x);
                     } else {
 #pragma unroll
@@ -372,11 +376,11 @@ __global__ void __launch_bounds__(kAllThreads, kGrad ? 2 : 3) distill_kernel(con
                     const int i0 = b * kBatch + tid, left = s.n - i0;
                     G* to = out + (int64_t)i0 * kVec;
                     uint4 w[kUnroll];
-                    if (left > (kUnroll - 1) * kThreads && b < p.staged) {
+                    if (wide && left > (kUnroll - 1) * kThreads && b < p.staged) {
 #pragma unroll
                         for (int q = 0; q < kUnroll; ++q) w[q] = stage[b * kBatch + q * kThreads];
 #pragma unroll
-                        for (int q = 0; q < kUnroll; ++q) write(w[q], to + q * kThreads * kVec);
+                        for (int q = 0; q < kUnroll; ++q) write(w[q], to + q * kThreads * kVec, true);
                     } else {
 #pragma unroll
                         for (int q = 0; q < kUnroll; ++q)
@@ -384,7 +388,7 @@ __global__ void __launch_bounds__(kAllThreads, kGrad ? 2 : 3) distill_kernel(con
                                 w[q] = b < p.staged ? stage[b * kBatch + q * kThreads] : __ldcs(s.pieces() + i0 + q * kThreads);
 #pragma unroll
                         for (int q = 0; q < kUnroll; ++q)
-                            if (q * kThreads < left) write(w[q], to + q * kThreads * kVec);
+                            if (q * kThreads < left) write(w[q], to + q * kThreads * kVec, wide);
                     }
                     if (more && b < p.staged) copy_batch(next_pieces, after.n, b);
                 }
