@@ -27,18 +27,27 @@ namespace {
 constexpr int kTileM = 128, kTileN = 256;
 constexpr int kBlockK = 64;            // terms of a pipeline stage
 constexpr int kChain = 16;             // stages of a chain
-constexpr int kStages = 4;
 constexpr int kGroup = 64 * 64 * 2;    // 64 rows of 128 bytes
-constexpr int kABytes = kTileM * kBlockK * 2, kBBytes = kTileN * kBlockK * 2;
-constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kABytes = kTileM * kBlockK * 2;
 constexpr int kEpilogueWarps = 8;
 constexpr int kThreads = 32 * (kEpilogueWarps + 2);
 constexpr int kPiece = 32 * 32 * 4;    // 32 rows of 32 sums: what a warp hands to one store
-constexpr size_t kSmem = kStages * kStageBytes + kEpilogueWarps * kPiece + 1024;
 constexpr uint32_t kIdescATransposed = 1u << 15;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kGatherRows = 16;
+constexpr int kKnown = 2560;           // stages (of rows) whose words are looked at once; a multiple of kThreads
 constexpr int kGridSms = 152;          // what the parts of a sum are counted for
+
+// A tile of kCtas x 128 rows and 256 columns by kCtas CTAs: each holds its rows of A and
+// its part of B's columns.  A CTA of a pair takes 32 KB to a stage where one by itself takes 48
+// (512 cycles of products either way, and the way into an SM gives about 62 bytes a cycle).
+template <int kCtas>
+struct Ring {
+    static constexpr int kBBytes = kTileN / kCtas * kBlockK * 2;
+    static constexpr int kStageBytes = kABytes + kBBytes;
+    static constexpr int kStages = kCtas == 1 ? 4 : 6;
+    static constexpr size_t kSmem = kStages * kStageBytes + kEpilogueWarps * kPiece + 1024;
+};
 
 struct Product {
     int M, rank;           // rows and columns of the result
@@ -46,15 +55,75 @@ struct Product {
     int tiles_n, tiles;    // tiles along the columns, in all
     int parts, per;        // parts of a sum, stages in each
     int accumulate;
-    const uint64_t* drop;  // a bit per row of g that gives nothing (dW2), a word per stage
+    const uint64_t* drop;  // a bit per row of g that is to be cleared (dW2), a word per stage
     int32_t* dev_status;
 };
 
 struct Barriers {
-    uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], drain;
+    uint64_t full[6], empty[6], land[6], tfull[2], tempty[2], drain;
     uint32_t tmem;
     int abort_flag;
+    uint32_t has_drop[kKnown / 32];  // a bit per stage: some of its rows are to be cleared
 };
+
+// ---- what a pair of CTAs does together (a pair's first CTA issues the products of both)
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc::smem_u32(dst)), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols) : "memory");
+}
+// As tc::tma_load_2d into this CTA's memory, counted on a barrier of either CTA (a cluster address).
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(tc::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+// (nothing is published by it; as a release in the cluster it took 700 cycles)
+__device__ __forceinline__ void expect_at(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void arrive_at(uint32_t bar) {  // (what this thread has written is visible to either CTA)
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void arrive_read(uint32_t bar) {  // (for what it has read alone)
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_address(const void* p, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(tc::smem_u32(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ uint32_t pair_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void pair_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void umma_pair_elect(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// As tc::umma_commit_elect, on the barrier at this place in both CTAs.
+__device__ __forceinline__ void commit_pair_elect(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+            tc::smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
 
 // 32 x 32 sums from shared memory to (or added to) columns x.., rows y.. of part z.
 __device__ __forceinline__ void store_piece(const CUtensorMap* map, const void* src, int x, int y, int z, int add) {
@@ -74,13 +143,42 @@ __device__ __forceinline__ void store_piece(const CUtensorMap* map, const void* 
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// tc::mbar_wait for threads whose registers are full: with its slow part called
-// out of line all 128 sums of a thread were spilled around the call.
-__device__ __forceinline__ bool wait_inline(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-    if (tc::mbar_try_wait(bar, parity)) return true;
+// (acquires what either CTA of a pair has released)
+__device__ __forceinline__ bool try_wait(uint64_t* bar, uint32_t parity, uint32_t hint_ns) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(tc::smem_u32(bar)), "r"(parity), "r"(hint_ns)
+        : "memory");
+    return ok != 0;
+}
+// At most 2 s, or until another thread of the CTA has given up.
+static __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
     const uint64_t t0 = global_ns();
     for (;;) {
-        if (tc::mbar_try_wait_sleep(bar, parity, 20000)) return true;
+        if (try_wait(bar, parity, 20000)) return true;
+        if (*abort_flag) return false;
+        if (global_ns() - t0 > kWaitNs) {
+            *abort_flag = 1;
+            return false;
+        }
+    }
+}
+// (the slow part out of line: in line it took the issue of the products from 100 to 370 cycles each)
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    if (__builtin_expect(try_wait(bar, parity, 0), 1)) return true;
+    return wait_slow(bar, parity, abort_flag);
+}
+// The same for threads whose registers are full (in line: all 128 sums of an epilogue's
+// thread were spilled around the call).
+__device__ __forceinline__ bool wait_held(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    if (try_wait(bar, parity, 0)) return true;
+    const uint64_t t0 = global_ns();
+    for (;;) {
+        if (try_wait(bar, parity, 20000)) return true;
         if (*abort_flag) return false;
         if (global_ns() - t0 > kWaitNs) {
             *abort_flag = 1;
@@ -90,26 +188,34 @@ __device__ __forceinline__ bool wait_inline(uint64_t* bar, uint32_t parity, vola
 }
 
 // kSumRows: the sum runs over g's rows (dW2), else over V (grad_prev).
-template <bool kSumRows>
+template <bool kSumRows, int kCtas>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const Product p, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                    const __grid_constant__ CUtensorMap map_c) {
+    using R = Ring<kCtas>;
+    constexpr int kStages = R::kStages;
     extern __shared__ unsigned char dyn[];
     __shared__ Barriers sh;
     unsigned char* ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int cta = kCtas == 1 ? 0 : (int)pair_rank();
     volatile int* abort_flag = &sh.abort_flag;
     if (warp == kEpilogueWarps + 1) {
-        tc::tmem_alloc(&sh.tmem, 512);
-        tc::tmem_relinquish();
+        if (kCtas == 1) {
+            tc::tmem_alloc(&sh.tmem, 512);
+            tc::tmem_relinquish();
+        } else {
+            tmem_alloc_pair(&sh.tmem, 512);
+        }
     } else if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
-            tc::mbar_init(&sh.full[s], 1);
+            tc::mbar_init(&sh.full[s], kCtas);
             tc::mbar_init(&sh.empty[s], 1);
+            tc::mbar_init(&sh.land[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
             tc::mbar_init(&sh.tfull[a], 1);
-            tc::mbar_init(&sh.tempty[a], kEpilogueWarps);
+            tc::mbar_init(&sh.tempty[a], kEpilogueWarps * kCtas);
         }
         tc::mbar_init(&sh.drain, 1);
         sh.abort_flag = 0;
@@ -117,11 +223,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc::tc_fence_before();
     __syncthreads();
+    if (kCtas > 1) pair_sync();
     tc::tc_fence_after();
     const uint32_t tmem = sh.tmem;
     launch_dependents();
     wait_prior_grid();
-    const int units = p.tiles * p.parts;
+    if (kSumRows) {
+        for (int k = tid; k < kKnown; k += kThreads) {
+            const unsigned any = __ballot_sync(0xFFFFFFFFu, k < p.blocks && __ldcg(p.drop + k) != 0);
+            if (lane == 0) sh.has_drop[k >> 5] = any;
+        }
+        __syncthreads();
+    }
+    const int units = p.tiles * p.parts, stride = gridDim.x / kCtas;
 
     // a unit of work: one tile's sum over the stages [k0, k1)
     struct Unit {
@@ -131,12 +245,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         Unit x;
         x.part = u / p.tiles;
         const int t = u - x.part * p.tiles;
-        x.m0 = t / p.tiles_n * kTileM;
+        x.m0 = (t / p.tiles_n * kCtas + cta) * kTileM;
         x.n0 = t % p.tiles_n * kTileN;
-        x.cols = min(kTileN, p.rank - x.n0);
+        // (whole groups of 64 for each CTA; what lies past the rank is zeros, and not written)
+        x.cols = min(kTileN, (p.rank - x.n0 + 64 * kCtas - 1) / (64 * kCtas) * (64 * kCtas));
         x.k0 = x.part * p.per;
         x.k1 = min(p.blocks, x.k0 + p.per);
         return x;
+    };
+    // rows that give nothing and hold a NaN or an infinity: cleared once they have landed.  (Clearing every row without a
+    // token instead made markov_step's dW2 309 us where it is 264.)
+    auto dropped = [&](int k) -> uint64_t {
+        if (!kSumRows || (k < kKnown && !(sh.has_drop[k >> 5] >> (k & 31) & 1u))) return 0;
+        return __ldcg(p.drop + k);
+    };
+    uint32_t landed = 0;  // parities
+    auto clear = [&](uint64_t drop, int s) {
+        const bool go = __all_sync(0xFFFFFFFFu, wait_bounded(&sh.land[s], landed >> s & 1u, abort_flag));
+        landed ^= 1u << s;
+        if (go) {
+            unsigned char* a = ring + s * R::kStageBytes;
+            for (; drop; drop &= drop - 1) {
+                const int r = __ffsll((long long)drop) - 1;
+                if (lane < 16) *reinterpret_cast<uint4*>(a + (lane >> 3) * kGroup + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive_at(cluster_address(&sh.full[s], 0));
+        }
+        return go;
     };
 
     if (warp == kEpilogueWarps) {
@@ -146,23 +283,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::prefetch_tmap(&map_b);
             int i = 0;
             bool go = true;
-            for (int u = blockIdx.x; go && u < units; u += gridDim.x) {
+            for (int u = blockIdx.x / kCtas; go && u < units; u += stride) {
                 const Unit x = unit_of(u);
-                const uint32_t bytes = kABytes + x.cols / 64 * kGroup;
+                const int cols = x.cols / kCtas;  // this CTA's
+                const uint32_t bytes = kABytes + cols / 64 * kGroup;
                 for (int k = x.k0; k < x.k1; ++k, ++i) {
                     const int s = i % kStages;
-                    if (i >= kStages && !(go = tc::mbar_wait(&sh.empty[s], (i / kStages - 1) & 1, abort_flag, kWaitNs))) break;
-                    unsigned char* a = ring + s * kStageBytes;
+                    const bool fix = dropped(k) != 0;
+                    if (i >= kStages && !(go = wait_bounded(&sh.empty[s], (i / kStages - 1) & 1, abort_flag))) break;
+                    unsigned char* a = ring + s * R::kStageBytes;
                     unsigned char* b = a + kABytes;
-                    tc::mbar_arrive_expect_tx(&sh.full[s], bytes);
+                    // (of a pair, both CTAs' loads are counted by the first, which issues the products)
+                    const uint32_t bar = fix ? cluster_address(&sh.land[s], cta) : cluster_address(&sh.full[s], 0);
+                    expect_at(bar, bytes);
+                    auto load = [&](void* dst, const CUtensorMap* map, int c, int r) {
+                        if (kCtas == 1)
+                            tc::tma_load_2d(dst, map, fix ? &sh.land[s] : &sh.full[s], c, r);
+                        else
+                            tma_load_pair(dst, map, bar, c, r);
+                    };
                     if (kSumRows) {
-                        tc::tma_load_2d(a, &map_a, &sh.full[s], x.m0, k * kBlockK);
-                        tc::tma_load_2d(a + kGroup, &map_a, &sh.full[s], x.m0 + 64, k * kBlockK);
+                        load(a, &map_a, x.m0, k * kBlockK);
+                        load(a + kGroup, &map_a, x.m0 + 64, k * kBlockK);
                     } else {
-                        tc::tma_load_2d(a, &map_a, &sh.full[s], k * kBlockK, x.m0);
+                        load(a, &map_a, k * kBlockK, x.m0);
                     }
-                    for (int c = 0; c < x.cols; c += 64)
-                        tc::tma_load_2d(b + c / 64 * kGroup, &map_b, &sh.full[s], x.n0 + c, k * kBlockK);
+                    for (int c = 0; c < cols; c += 64) load(b + c / 64 * kGroup, &map_b, x.n0 + cta * cols + c, k * kBlockK);
                 }
             }
         }
@@ -171,63 +317,78 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------------------------------------------------------- products
         int i = 0, chain = 0;
         bool go = true;
-        for (int u = blockIdx.x; go && u < units; u += gridDim.x) {
+        for (int u = blockIdx.x / kCtas; go && u < units; u += stride) {
             const Unit x = unit_of(u);
-            const uint32_t idesc = tc::idesc_bf16_f32(kTileM, x.cols) | tc::kIdescBTransposed | (kSumRows ? kIdescATransposed : 0u);
+            if (cta != 0) {  // the other CTA of a pair has rows to clear, at most
+                for (int k = x.k0; go && k < x.k1; ++k, ++i) {
+                    const uint64_t drop = dropped(k);
+                    if (drop) go = clear(drop, i % kStages);
+                }
+                continue;
+            }
+            const uint32_t idesc =
+                tc::idesc_bf16_f32(kTileM * kCtas, x.cols) | tc::kIdescBTransposed | (kSumRows ? kIdescATransposed : 0u);
             for (int c0 = x.k0; go && c0 < x.k1; c0 += kChain, ++chain) {
                 const int buf = chain & 1;
-                if (chain >= 2 && !(go = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&sh.tempty[buf], (chain / 2 - 1) & 1, abort_flag, kWaitNs)))) break;
+                if (chain >= 2 && !(go = __all_sync(0xFFFFFFFFu, wait_bounded(&sh.tempty[buf], (chain / 2 - 1) & 1, abort_flag)))) break;
                 tc::tc_fence_after();
                 const uint32_t d = tmem + buf * kTileN;
                 const int c1 = min(x.k1, c0 + kChain);
                 for (int k = c0; k < c1; ++k, ++i) {
                     const int s = i % kStages;
-                    // rows that give nothing, NaN and infinities in them among it
-                    const uint64_t drop = kSumRows ? __ldcg(p.drop + k) : 0;
-                    if (!(go = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&sh.full[s], (i / kStages) & 1, abort_flag, kWaitNs)))) break;
-                    unsigned char* a = ring + s * kStageBytes;
-                    if (kSumRows && drop) {
-                        for (uint64_t left = drop; left; left &= left - 1) {
-                            const int r = __ffsll((long long)left) - 1;
-                            if (lane < 16)
-                                *reinterpret_cast<uint4*>(a + (lane >> 3) * kGroup + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
-                        }
-                        tc::fence_proxy_async_smem();
-                        __syncwarp();
-                    }
+                    const uint64_t drop = dropped(k);
+                    if (drop && !(go = clear(drop, s))) break;
+                    if (!(go = __all_sync(0xFFFFFFFFu, wait_bounded(&sh.full[s], (i / kStages) & 1, abort_flag)))) break;
                     tc::tc_fence_after();
-                    const uint32_t sa = tc::smem_u32(a);
+                    const uint32_t sa = tc::smem_u32(ring + s * R::kStageBytes);
                     const uint64_t ad = kSumRows ? tc::smem_desc_sw128_mn(sa, kGroup) : tc::smem_desc_sw128(sa);
                     const uint64_t bd = tc::smem_desc_sw128_mn(sa + kABytes, kGroup);
 #pragma unroll
-                    for (int j = 0; j < kBlockK / 16; ++j)
-                        tc::umma_bf16_elect(d, ad + (uint64_t)(j * ((kSumRows ? 2048 : 32) >> 4)), bd + (uint64_t)(j * (2048 >> 4)),
-                                            idesc, k > c0 || j > 0);
-                    tc::umma_commit_elect(&sh.empty[s]);
+                    for (int j = 0; j < kBlockK / 16; ++j) {
+                        const uint64_t aj = ad + (uint64_t)(j * ((kSumRows ? 2048 : 32) >> 4)), bj = bd + (uint64_t)(j * (2048 >> 4));
+                        if (kCtas == 1)
+                            tc::umma_bf16_elect(d, aj, bj, idesc, k > c0 || j > 0);
+                        else
+                            umma_pair_elect(d, aj, bj, idesc, k > c0 || j > 0);
+                    }
+                    if (kCtas == 1)
+                        tc::umma_commit_elect(&sh.empty[s]);
+                    else
+                        commit_pair_elect(&sh.empty[s]);
                 }
-                if (go) tc::umma_commit_elect(&sh.tfull[buf]);
+                if (go) {
+                    if (kCtas == 1)
+                        tc::umma_commit_elect(&sh.tfull[buf]);
+                    else
+                        commit_pair_elect(&sh.tfull[buf]);
+                }
             }
         }
         __syncwarp();
-        // (whatever ended the loop, the products are done before tensor memory is given back)
-        tc::umma_commit_elect(&sh.drain);
+        if (cta == 0) {
+            // (whatever ended the loop, the products are done before tensor memory is given back)
+            if (kCtas == 1)
+                tc::umma_commit_elect(&sh.drain);
+            else
+                commit_pair_elect(&sh.drain);
+        }
         int never = 0;
-        tc::mbar_wait(&sh.drain, 0, &never, kWaitNs);
+        wait_bounded(&sh.drain, 0, &never);
     } else {
         // ---------------------------------------------------------------- chains added up, tiles written
         const int quad = warp & 3, half = warp >> 2;
-        unsigned char* piece = ring + kStages * kStageBytes + warp * kPiece;
+        unsigned char* piece = ring + kStages * R::kStageBytes + warp * kPiece;
         int chain = 0;
         bool go = true;
-        for (int u = blockIdx.x; go && u < units; u += gridDim.x) {
+        for (int u = blockIdx.x / kCtas; go && u < units; u += stride) {
             const Unit x = unit_of(u);
-            const int cols = min(128, x.cols - half * 128);  // (none: only the barriers)
+            const int cols = min(128, min(x.cols, p.rank - x.n0) - half * 128);  // (none: only the barriers)
             float acc[128];
 #pragma unroll
             for (int e = 0; e < 128; ++e) acc[e] = 0.0f;
             for (int c0 = x.k0; c0 < x.k1; c0 += kChain, ++chain) {
                 const int buf = chain & 1;
-                if (!(go = __all_sync(0xFFFFFFFFu, wait_inline(&sh.tfull[buf], (chain / 2) & 1, abort_flag)))) break;
+                if (!(go = __all_sync(0xFFFFFFFFu, wait_held(&sh.tfull[buf], (chain / 2) & 1, abort_flag)))) break;
                 tc::tc_fence_after();
                 if (cols > 0) {
                     const uint32_t t = tmem + ((uint32_t)(quad * 32) << 16) + buf * kTileN + half * 128;
@@ -242,11 +403,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&sh.tempty[buf]);
+                if (lane == 0) arrive_read(cluster_address(&sh.tempty[buf], 0));
             }
             // 32 columns at a time through shared memory (16-byte pieces in the order the store's swizzle
             // undoes), then to memory by one store, which leaves out what lies past the result's rows.  Stores
-            // from registers, a row to a thread, took 210 us of markov_batch's second product.
+            // from registers, a row to a thread, took 210 us of markov_batch's second product where these take 136.
             const int row = x.m0 + quad * 32;
             if (go && row < p.M) {
 #pragma unroll
@@ -275,35 +436,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t t0 = global_ns();  // loads in flight end before their memory goes
         while (global_ns() - t0 < 1000000) {}
     }
-    if (warp == kEpilogueWarps + 1) tc::tmem_dealloc(tmem, 512);
+    if (kCtas > 1) pair_sync();  // (neither CTA's memory goes while the other's products or arrivals use it)
+    tc::tc_fence_after();
+    if (warp == kEpilogueWarps + 1) {
+        if (kCtas == 1)
+            tc::tmem_dealloc(tmem, 512);
+        else
+            tmem_dealloc_pair(tmem, 512);
+    }
 }
 
-// ---- W1 rows of the previous tokens (zeros where there is none), and which rows give nothing
-__global__ void __launch_bounds__(32 * kGatherRows) gather_kernel(const MarkovGradParams p, uint16_t* E, uint16_t* drop) {
-    __shared__ uint32_t off;
+// ---- W1 rows of the previous tokens (zeros where there is none); no row marked yet
+__global__ void __launch_bounds__(32 * kGatherRows) gather_kernel(const MarkovGradParams p, uint16_t* E, uint64_t* drop) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int n = blockIdx.x * kGatherRows + warp;
     wait_prior_grid();
-    if (threadIdx.x == 0) off = 0;
-    __syncthreads();
-    const int a = n < p.rows ? p.prev[n] : -1;
-    const bool there = a >= 0 && a < p.V;
-    if (lane == 0) {
-        if (n < p.rows && !there) atomicOr(&off, 1u << warp);
-        if (a >= p.V) report(p.dev_status, DSPARK_ERR_DEVICE_INPUT);
-    }
-    if (n < p.rows)
+    if (n < p.rows) {
+        const int a = p.prev[n];
+        const bool there = a >= 0 && a < p.V;
+        if (lane == 0) {
+            if (a >= p.V) report(p.dev_status, DSPARK_ERR_DEVICE_INPUT);
+            if (n % kBlockK == 0) drop[n / kBlockK] = 0;
+        }
         for (int i = lane; i < p.rank / 8; i += 32)
             reinterpret_cast<uint4*>(E + (size_t)n * p.rank)[i] =
                 there ? __ldg(reinterpret_cast<const uint4*>(p.W1 + (size_t)a * p.rank) + i) : make_uint4(0, 0, 0, 0);
-    __syncthreads();
-    if (threadIdx.x == 0) drop[blockIdx.x] = (uint16_t)off;
+    }
     launch_dependents();
 }
 
-// ---- the parts of grad_prev: every group of threads adds its own in order, then the groups in order
+// ---- the parts of grad_prev: every group of threads adds its own in order, then the groups in order.
+// A row without a token gives nothing, and its sums are not all finite if a NaN or an infinity stands in
+// it: such rows are marked, to be cleared on their way into dW2's products (where their W1 row is zeros,
+// which would do for any others).
 constexpr int kJoinThreads = 512;
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const MarkovGradParams p, const float* part, int parts) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const MarkovGradParams p, const float* part, int parts,
+                                                            unsigned long long* drop) {
     __shared__ float4 sums[kJoinThreads];
     const int n = blockIdx.x, quads = p.rank / 4, groups = kJoinThreads / quads;
     const int i = threadIdx.x % quads, g = threadIdx.x / quads;
@@ -330,6 +498,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const MarkovGradPara
             const float4 x = sums[o * quads + i];
             s = make_float4(s.x + x.x, s.y + x.y, s.z + x.z, s.w + x.w);
         }
+        if ((a < 0 || a >= p.V) && !(fabsf(s.x) < INFINITY && fabsf(s.y) < INFINITY && fabsf(s.z) < INFINITY && fabsf(s.w) < INFINITY))
+            atomicOr(drop + n / kBlockK, 1ull << (n % kBlockK));
         if (a < 0) s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (a >= p.V) s = make_float4(NAN, NAN, NAN, NAN);
         reinterpret_cast<float4*>(p.grad_prev + (size_t)n * p.rank)[i] = s;
@@ -372,15 +542,19 @@ __global__ void __launch_bounds__(128) scatter_kernel(const MarkovGradParams p) 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 int up(int a, int b) { return (a + b - 1) / b; }
 
-// How many parts the sum over V is cut into: the fewest steps of the busiest SM,
-// a stage counted as 512 cycles of products and a part's way to memory and back
+// CTAs to a tile of grad_prev: a pair where there are rows for both.
+int ctas_of(int rows) { return rows > kTileM ? 2 : 1; }
+
+// How many parts the sum over V is cut into: the fewest cycles of the busiest SM,
+// a stage counted as 540 cycles (of a pair) or 775, and a part's way to memory and back
 // as its bytes at 23 a cycle and SM.
 int parts_of(int rows, int V, int rank) {
-    const int tiles = up(rows, kTileM) * up(rank, kTileN), blocks = up(V, kBlockK);
+    const int ctas = ctas_of(rows), slots = kGridSms / ctas;
+    const int tiles = up(rows, kTileM * ctas) * up(rank, kTileN), blocks = up(V, kBlockK);
     double best = 0;
     int parts = 1;
-    for (int n = 1; n <= std::min(blocks, 152); ++n) {
-        const double steps = (double)up(tiles * n, kGridSms) * (up(blocks, n) * 512.0 + 3000.0);
+    for (int n = 1; n <= std::min(blocks, kGridSms); ++n) {
+        const double steps = (double)up(tiles * n, slots) * (up(blocks, n) * (ctas == 2 ? 540.0 : 775.0) + 3000.0);
         const double moved = (double)n * rows * rank * 8.0 / (23.0 * kGridSms);
         if (n == 1 || steps + moved < best) {
             best = steps + moved;
@@ -444,15 +618,29 @@ bool encode_sums(CUtensorMap* m, const void* base, int cols, int rows, int parts
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool kSumRows>
+template <bool kSumRows, int kCtas>
 cudaError_t launch_product(Product p, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, int n_sm,
                            cudaStream_t stream) {
     p.tiles_n = up(p.rank, kTileN);
-    p.tiles = up(p.M, kTileM) * p.tiles_n;
+    p.tiles = up(p.M, kTileM * kCtas) * p.tiles_n;
     p.per = up(p.blocks, p.parts);
-    const cudaError_t e = cudaFuncSetAttribute(product_kernel<kSumRows>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    const auto kernel = product_kernel<kSumRows, kCtas>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Ring<kCtas>::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_after(product_kernel<kSumRows>, dim3(std::min(n_sm, p.tiles * p.parts)), kThreads, kSmem, stream, p, a, b, c);
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = kCtas;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(std::min(n_sm / kCtas, p.tiles * p.parts) * kCtas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Ring<kCtas>::kSmem;
+    cfg.stream = stream;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, p, a, b, c);
 }
 
 }  // namespace
@@ -479,20 +667,23 @@ cudaError_t launch_markov_grad(const MarkovGradParams& p, cudaStream_t stream) {
         !encode(&w2, p.W2, p.rank, p.V, p.rank, kBlockK) || !encode(&before, E, p.rank, p.rows, p.rank, kBlockK) ||
         !encode_sums(&sums, part, p.rank, p.rows, parts) || (p.dW2 && !encode_sums(&dW2, p.dW2, p.rank, p.V, 1)))
         return cudaErrorInvalidValue;
-    if ((e = launch_after(gather_kernel, dim3(up(p.rows, kBlockK) * (kBlockK / kGatherRows)), 32 * kGatherRows, 0, stream, p, E,
-                          reinterpret_cast<uint16_t*>(w + L.drop))) != cudaSuccess)
+    if ((e = launch_after(gather_kernel, dim3(up(p.rows, kGatherRows)), 32 * kGatherRows, 0, stream, p, E,
+                          reinterpret_cast<uint64_t*>(w + L.drop))) != cudaSuccess)
         return e;
     Product q{};
     q.rank = p.rank;
     q.dev_status = p.dev_status;
     q.M = p.rows; q.blocks = up(p.V, kBlockK); q.parts = parts;
-    if ((e = launch_product<false>(q, g_rows, w2, sums, n_sm, stream)) != cudaSuccess) return e;
-    if ((e = launch_after(join_kernel, dim3(p.rows), kJoinThreads, 0, stream, p, part, parts)) != cudaSuccess) return e;
+    e = ctas_of(p.rows) == 2 ? launch_product<false, 2>(q, g_rows, w2, sums, n_sm, stream)
+                            : launch_product<false, 1>(q, g_rows, w2, sums, n_sm, stream);
+    if (e != cudaSuccess) return e;
+    if ((e = launch_after(join_kernel, dim3(p.rows), kJoinThreads, 0, stream, p, part, parts,
+                          reinterpret_cast<unsigned long long*>(w + L.drop))) != cudaSuccess) return e;
     if (p.dW1 && (e = launch_after(scatter_kernel, dim3(p.rows), 128, 0, stream, p)) != cudaSuccess) return e;
     if (p.dW2) {
         q.M = p.V; q.blocks = up(p.rows, kBlockK); q.parts = 1; q.accumulate = p.accumulate;
         q.drop = reinterpret_cast<const uint64_t*>(w + L.drop);
-        if ((e = launch_product<true>(q, g_cols, before, dW2, n_sm, stream)) != cudaSuccess) return e;
+        if ((e = launch_product<true, 2>(q, g_cols, before, dW2, n_sm, stream)) != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
