@@ -469,26 +469,24 @@ __global__ void __launch_bounds__(32 * kGatherRows) gather_kernel(const MarkovGr
 // A row without a token gives nothing, and its sums are not all finite if a NaN or an infinity stands in
 // it: such rows are marked, to be cleared on their way into dW2's products (where their W1 row is zeros,
 // which would do for any others).
-constexpr int kJoinThreads = 512;
+constexpr int kJoinThreads = 512;  // at most
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const MarkovGradParams p, const float* part, int parts,
                                                             unsigned long long* drop) {
     __shared__ float4 sums[kJoinThreads];
-    const int n = blockIdx.x, quads = p.rank / 4, groups = kJoinThreads / quads;
+    const int n = blockIdx.x, quads = p.rank / 4, groups = blockDim.x / quads;
     const int i = threadIdx.x % quads, g = threadIdx.x / quads;
     wait_prior_grid();
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (g < groups) {
-        for (int z0 = g; z0 < parts; z0 += 4 * groups) {
-            float4 x[4];
+    for (int z0 = g; z0 < parts; z0 += 4 * groups) {
+        float4 x[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int z = z0 + q * groups;
-                x[q] = z < parts ? __ldcs(reinterpret_cast<const float4*>(part + ((size_t)z * p.rows + n) * p.rank) + i)
-                                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) s = make_float4(s.x + x[q].x, s.y + x[q].y, s.z + x[q].z, s.w + x[q].w);
+        for (int q = 0; q < 4; ++q) {
+            const int z = z0 + q * groups;
+            x[q] = z < parts ? __ldcs(reinterpret_cast<const float4*>(part + ((size_t)z * p.rows + n) * p.rank) + i)
+                             : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) s = make_float4(s.x + x[q].x, s.y + x[q].y, s.z + x[q].z, s.w + x[q].w);
     }
     sums[threadIdx.x] = s;
     __syncthreads();
@@ -677,8 +675,11 @@ cudaError_t launch_markov_grad(const MarkovGradParams& p, cudaStream_t stream) {
     e = ctas_of(p.rows) == 2 ? launch_product<false, 2>(q, g_rows, w2, sums, n_sm, stream)
                             : launch_product<false, 1>(q, g_rows, w2, sums, n_sm, stream);
     if (e != cudaSuccess) return e;
-    if ((e = launch_after(join_kernel, dim3(p.rows), kJoinThreads, 0, stream, p, part, parts,
-                          reinterpret_cast<unsigned long long*>(w + L.drop))) != cudaSuccess) return e;
+    // (groups of threads, four parts each)
+    const int quads = p.rank / 4, groups = std::min(std::max(parts / 4, 1), kJoinThreads / quads);
+    if ((e = launch_after(join_kernel, dim3(p.rows), quads * groups, 0, stream, p, part, parts,
+                          reinterpret_cast<unsigned long long*>(w + L.drop))) != cudaSuccess)
+        return e;
     if (p.dW1 && (e = launch_after(scatter_kernel, dim3(p.rows), 128, 0, stream, p)) != cudaSuccess) return e;
     if (p.dW2) {
         q.M = p.V; q.blocks = up(p.rows, kBlockK); q.parts = 1; q.accumulate = p.accumulate;
