@@ -380,8 +380,8 @@ int dspark_verify_static_scratch(const float* target_logits, const int32_t* cu_s
  * reported DSPARK_ERR_TIMEOUT are invalid (requests decided before the wait
  * ran out may have been written; the others are left untouched).  The waits
  * of a CTA on its own asynchronous copies (mbarriers) keep a fixed 2 s limit,
- * and so do the waits of the attention kernels' warps on one another: when one
- * runs out, all warps of that CTA stop (those that run ahead of the others wait
+ * and so do the waits of the attention kernels' and dspark_markov_grad's warps on
+ * one another: when one runs out, all warps of that CTA stop (those that run ahead of the others wait
  * as long as these work), and DSPARK_ERR_TIMEOUT is reported in the same way.
  *
  * dspark_set_wait_limit_ns sets the limit of the grid-wide waits for every
@@ -394,12 +394,14 @@ int dspark_verify_static_scratch(const float* target_logits, const int32_t* cu_s
  * arrival more than the grid has, so that no CTA is ever released and every
  * wait runs out after the limit above; with DSPARK_INJECT_ATTENTION_QUERIES the
  * attention kernels' queries are never complete, and the wait for them runs out
- * after 2 s.  Returns the previous mask; 0 turns
+ * after 2 s; with DSPARK_INJECT_MARKOV_OPERANDS those of dspark_markov_grad's
+ * products, likewise.  Returns the previous mask; 0 turns
  * injection off.  Both settings are read when a call is enqueued.
  */
 #define DSPARK_INJECT_VERIFY_BARRIER 1u
 #define DSPARK_INJECT_DRAFT_BARRIER 2u
 #define DSPARK_INJECT_ATTENTION_QUERIES 4u
+#define DSPARK_INJECT_MARKOV_OPERANDS 8u
 
 uint64_t dspark_set_wait_limit_ns(uint64_t limit_ns);
 unsigned dspark_set_fault_injection(unsigned mask);
@@ -766,8 +768,8 @@ int dspark_distill_loss(const void* student, int64_t student_stride, int student
  *   ws, ws_bytes dspark_workspace_size(DSPARK_OP_MARKOV_GRAD, 0, 0, V, rank, rows, DSPARK_BF16, 0)
  * A row with prev >= V is reported (DSPARK_ERR_DEVICE_INPUT), gives nothing to dW1 and dW2, and
  * its grad_prev is NaN.  rows == 0 gives zeros (dW2) without DSPARK_GRAD_ACCUMULATE.
- * Limits (DSPARK_ERR_UNSUPPORTED): rank % 64 == 0 up to 512, V % 8 == 0, rows < 2^24; grad, W1, W2, grad_prev, dW1
- * and dW2 16-byte aligned, grad_stride a multiple of 8.
+ * Limits (DSPARK_ERR_UNSUPPORTED): rank % 64 == 0 up to 512, V % 8 == 0, rows <= 2^20 (dW1
+ * compares every row's token with every other's); grad, W1, W2, grad_prev, dW1 and dW2 16-byte aligned, grad_stride a multiple of 8.
  */
 int dspark_markov_grad(const void* grad, int64_t grad_stride, const int32_t* prev, const void* W1,
                        const void* W2, int rows, int V, int rank, float* grad_prev, float* dW1,

@@ -141,7 +141,7 @@ bool valid_rows(const void* x, int64_t stride, int dtype, int V) {
 }
 
 bool markov_grad_supported(int rows, int V, int rank) {
-    return rows >= 0 && V > 0 && rank > 0 && rank % 64 == 0 && rank <= 512 && V % 8 == 0 && rows < (1 << 24);
+    return rows >= 0 && V > 0 && rank > 0 && rank % 64 == 0 && rank <= 512 && V % 8 == 0 && rows <= (1 << 20);
 }
 
 // Process-wide settings of the grid-wide waits (see dspark_set_wait_limit_ns).
@@ -164,7 +164,8 @@ uint64_t dspark_set_wait_limit_ns(uint64_t limit_ns) {
 }
 
 unsigned dspark_set_fault_injection(unsigned mask) {
-    return g_inject.exchange(mask & (DSPARK_INJECT_VERIFY_BARRIER | DSPARK_INJECT_DRAFT_BARRIER | DSPARK_INJECT_ATTENTION_QUERIES));
+    return g_inject.exchange(mask & (DSPARK_INJECT_VERIFY_BARRIER | DSPARK_INJECT_DRAFT_BARRIER | DSPARK_INJECT_ATTENTION_QUERIES |
+                                     DSPARK_INJECT_MARKOV_OPERANDS));
 }
 
 const char* dspark_status_string(int status) {
@@ -626,6 +627,7 @@ int dspark_markov_grad(const void* grad, int64_t grad_stride, const int32_t* pre
     p.W1 = static_cast<const uint16_t*>(W1); p.W2 = static_cast<const uint16_t*>(W2);
     p.rows = rows; p.V = V; p.rank = rank; p.accumulate = (flags & DSPARK_GRAD_ACCUMULATE) != 0;
     p.grad_prev = grad_prev; p.dW1 = dW1; p.dW2 = dW2; p.dev_status = dev_status; p.ws = ws;
+    p.inject = (fault_injection_mask() & DSPARK_INJECT_MARKOV_OPERANDS) != 0;
     return cuda_status(launch_markov_grad(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -206,6 +206,7 @@ __global__ void __launch_bounds__(kAllThreads, kGrad ? 2 : 3) distill_kernel(con
             bad |= t.id[q] >= p.V || t.value[q] != t.value[q] || t.value[q] == INFINITY || t.x[q] != t.x[q];
             if (t.id[q] >= s.v0 && t.id[q] < s.v1) {
                 const int b = s.bit(t.id[q]), piece = (b - 32) / kVec;
+                if (!IN_BOUNDS(b >= 0 && b >> 5 < p.bit_words, p.dev_status)) continue;
                 bad |= (atomicOr(&bits[b >> 5], 1u << (b & 31)) >> (b & 31) & 1u) != 0;  // listed twice
                 if (b >= 32 && piece < s.n) atomicOr(&sh.marked[piece % kThreads], 1u << min(piece / kBatch, 31));
             }
@@ -217,6 +218,7 @@ __global__ void __launch_bounds__(kAllThreads, kGrad ? 2 : 3) distill_kernel(con
         for (int q = 0; q < kPerLane; ++q)
             if (t.id[q] >= s.v0 && t.id[q] < s.v1) {
                 const int b = s.bit(t.id[q]), piece = (b - 32) / kVec;
+                if (!IN_BOUNDS(b >= 0 && b >> 5 < p.bit_words, p.dev_status)) continue;
                 bits[b >> 5] = 0;
                 if (b >= 32 && piece < s.n) sh.marked[piece % kThreads] = 0;
             }

@@ -292,6 +292,7 @@ struct MarkovGradParams {
     const int32_t* prev;
     const uint16_t *W1, *W2;
     int rows, V, rank, accumulate;
+    int inject;  // 1 (tests): no operand is ever complete
     float *grad_prev, *dW1, *dW2;
     int32_t* dev_status;
     void* ws;

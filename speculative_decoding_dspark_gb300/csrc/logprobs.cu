@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsParams
         }
         return;
     }
+    if (!IN_BOUNDS(n >= 0 && n < p.rows, p.dev_status)) return;  // (the same for all CTAs of the cluster)
     const T* row = reinterpret_cast<const T*>(p.logits) + n * p.stride;
     const float x_token = Elem<T>::to_float(row[token]);
     const RowView<T> view(row, p.V);
@@ -278,7 +279,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsParams
         } else {
             for (int h = tid; h < n_hits * kUnroll; h += kThreads) {
                 const int i = (int)sh.hits[h / kUnroll] + h % kUnroll * kThreads;
-                if (i >= end) continue;
+                if (i >= end || !IN_BOUNDS(i >= first, p.dev_status)) continue;
                 const uint4 w = __ldcs(view.base + i);
                 uint32_t reach = 0;
 #pragma unroll

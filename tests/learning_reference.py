@@ -19,8 +19,9 @@ error, 2^-22 each, with the roundings of their arguments' constants):
 * a gradient: q M (3u|a| + v + e_s + 8u) + p e_p + the rest's share likewise and with p_rest's error; then the
   rounding of the type, u or 2^-9.
 * a product's sum (the Markov factors): the tensor cores add 16 products at a time to an accumulator and may cut off
-  what lies below it: 2^-22 of the sum of magnitudes for each of the at most 64 steps of a chain, K / 1024 chains and
-  up to 152 parts added in fp32: (64 + K / 1024 + 152) 2^-22 of sum |a b| is never passed.
+  what lies below it: 2^-22 of the sum of magnitudes for each of the 32 steps of a chain, and likewise for the chains
+  of a part and the parts, at most 152, added in fp32: (64 + K / 1024 + 152) 2^-22 of sum |a b| is never passed (K / 512
+  chains in all, of which a part has K / 512 over the number of parts; up to K = 180000 in one part).
 """
 from __future__ import annotations
 

@@ -1,5 +1,7 @@
 """GPU parity of dspark_token_logprobs, dspark_distill_loss and dspark_markov_grad against their 64-bit definitions
 (learning_reference.py, whose docstring derives the tolerances).  Outputs and workspaces lie between guard bytes."""
+import time
+
 import numpy as np
 import pytest
 
@@ -389,6 +391,38 @@ def test_distill_rows_without_a_value(B):
     assert status == DEVICE_INPUT and loss.isnan().all() and g.isnan().all()
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_distill_rows_without_weight(B, in_place):
+    """Rows of weight 0, alone and among others, at every alignment: not read, their gradient zero and nothing beside it."""
+    for V in (1, 5, 1027, 40003):
+        for weights in ([0.0] * 6, [0.0, 1.0, 0.0, 0.0, 2.0, -0.0]):
+            for dtype in (F32, BF16):
+                x = rows_of(normal(V, (6, V)), dtype, 3, 5)
+                weight = torch.tensor(weights, device="cuda")
+                ids, value = teacher_of(1, x, 1)
+                ref, tol = L.distill(x, ids, value, 1.0, weight, False, dtype)
+                x[weight == 0] = NAN
+                loss, g, status = distill(B, x, ids, value, 1.0, dtype, weight, False, in_place, gap=0 if in_place else 5, offset=3)
+                assert status == 0
+                close(loss, ref[0], tol[0], "loss")
+                close(g, ref[1], tol[1], "grad")
+
+
+def test_distill_more_places_than_tokens(B):
+    x = normal(19, (3, 3), 2.0)
+    ids = i32([[2, -1, -7, 0, -1, -1, -1, 1], [-1] * 8, [-1] * 7 + [1]])
+    value = torch.full((3, 8), NAN, device="cuda")  # (beside no token a value says nothing)
+    value[0, [0, 3, 7]] = torch.tensor([0.2, 0.3, 0.5], device="cuda").log()
+    value[2, 7] = -0.1
+    for rest in (False, True):
+        clean = torch.where(ids >= 0, value, torch.zeros_like(value))
+        ref, tol = L.distill(x, ids, clean, 1.0, None, rest, F32)
+        loss, g, status = distill(B, x, ids, value, 1.0, F32, None, rest)
+        assert status == 0
+        close(loss, ref[0], tol[0], "loss")
+        close(g, ref[1], tol[1], "grad")
+
+
 def test_distill_gradient_is_the_slope(B):
     """Against differences of the operator's own loss, in steps that the loss resolves."""
     V, h = 40, 0.05
@@ -492,6 +526,49 @@ def test_markov_grad_no_rows(B):
     assert (d1 == 3).all() and (d2 == 0).all()
     _, d1, d2, _ = markov(B, g, prev, W, W, True, start=(3.0, 3.0))
     assert (d1 == 3).all() and (d2 == 3).all()
+
+
+@pytest.mark.parametrize("rows,V,rank", [(5, 640, 64), (300, 4104, 512)])
+def test_markov_grad_wait_that_runs_out(B, rows, V, rank):
+    """Operands that are never complete: the call ends soon after the limit of 2 s for each of its two products, reports the
+    timeout, and the next call is as good as ever."""
+    g, prev, W1, W2 = markov_case(8, rows, V, rank)
+    want = markov(B, g, prev, W1, W2)
+    assert want[3] == 0
+    assert B.dspark_set_fault_injection(B.DSPARK_INJECT_MARKOV_OPERANDS) == 0
+    try:
+        start = time.monotonic()
+        _, _, _, status = markov(B, g, prev, W1, W2)
+        took = time.monotonic() - start
+    finally:
+        assert B.dspark_set_fault_injection(0) == B.DSPARK_INJECT_MARKOV_OPERANDS
+    assert status == B.DSPARK_ERR_TIMEOUT and 4.0 <= took < 6.0
+    again = markov(B, g, prev, W1, W2)
+    assert again[3] == 0 and all(torch.equal(a, b) for a, b in zip(again[:3], want[:3]))
+
+
+@pytest.mark.parametrize("same", [True, False])
+def test_markov_grad_equal_tokens(B, same):
+    """One token before every row; the rows' sums go to one row of dW1."""
+    rows, V, rank = 700, 264, 128
+    g, prev, W1, W2 = markov_case(9, rows, V, rank)
+    prev.fill_(V - 1) if same else prev.copy_(torch.arange(rows, device="cuda") % 3 * 100)
+    gp, d1, d2, status = markov(B, g, prev, W1, W2)
+    assert status == 0
+    ref, tol = L.markov(g, prev, W1, W2)
+    close(gp, ref[0], tol[0], "grad_prev")
+    close(d1, ref[1], tol[1], "dW1")
+    close(d2, ref[2], tol[2], "dW2")
+
+
+def test_markov_grad_no_tokens(B):
+    """No row has a token before it: nothing to learn, whatever stands in the rows."""
+    rows, V, rank = 200, 1000, 64
+    g, prev, W1, W2 = markov_case(10, rows, V, rank)
+    prev.fill_(-1)
+    g[:130] = NAN
+    gp, d1, d2, status = markov(B, g, prev, W1, W2, start=(3.0, 3.0))
+    assert status == 0 and (gp == 0).all() and (d1 == 3).all() and (d2 == 0).all()
 
 
 # ------------------------------------------------------------------------------------------- all of them
