@@ -43,7 +43,17 @@ struct Kept {  // what is known of a row's listed tokens before its sums are
     float bad;
 };
 
+// A row's listed tokens.  (In shared memory: held by the lanes, 24 registers, they kept every
+// thread of the kernel above 72, at which three CTAs fit on an SM.)
+struct Listed {
+    int id[DSPARK_TOP_MAX];      // -1: none
+    float x[DSPARK_TOP_MAX];     // the drafter's logit
+    float value[DSPARK_TOP_MAX];
+    float p[DSPARK_TOP_MAX];     // exp(value - its reference)
+};
+
 struct Shared {
+    Listed list[2];                    // by the row's parity
     float2 sums[2][kMaxCtas][kWarps];  // (m, s) of all warps of the cluster, by the row's parity
     float bad[2][kMaxCtas];            // whether a CTA found fault with the listed tokens
     Kept kept[2];
@@ -101,6 +111,9 @@ __device__ __forceinline__ void clear_grad(G* g, int V, int rank, int size) {
     if (rank == size - 1 && tail < V) g[tail] = G(0);
 }
 
+__device__ __forceinline__ void copy_word(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
+}
 // At most `left` (or 7) of this thread's groups of copies still on their way.
 __device__ __forceinline__ void copies_left(int left) {
     switch (left) {
@@ -135,16 +148,9 @@ struct Share {
     __device__ __forceinline__ int batches() const { return (n + kUnroll * kThreads - 1) / (kUnroll * kThreads); }
 };
 
-// A row's listed tokens, four to a lane of the warp that keeps them.
-struct Listed {
-    int id[kPerLane];    // -1: none
-    float x[kPerLane];   // the drafter's logit
-    float value[kPerLane];
-};
-
 // T: the logits' elements, G: the gradient's, kGrad: there is one.
 template <typename T, typename G, bool kGrad>
-__global__ void __launch_bounds__(kAllThreads, kGrad ? 2 : 3) distill_kernel(const DistillParams p) {
+__global__ void __launch_bounds__(kAllThreads, kGrad && sizeof(T) == 4 ? 2 : 3) distill_kernel(const DistillParams p) {
     constexpr int kVec = Elem<T>::kVec;
     constexpr int kBatch = kUnroll * kThreads;  // pieces
     extern __shared__ uint4 dyn[];
@@ -183,29 +189,31 @@ __global__ void __launch_bounds__(kAllThreads, kGrad ? 2 : 3) distill_kernel(con
         }
         tc::cp_async_commit();
     };
-    // (keeper) a row's listed tokens
+    // (keeper) a row's listed tokens and their values on their way
+    const int n_list = (p.top_k + 31) / 32 * 32;
     auto fetch = [&](int64_t n, Listed& t) {
-        const RowView<T> view(reinterpret_cast<const T*>(p.student) + n * p.stride, p.V);
-#pragma unroll
-        for (int q = 0; q < kPerLane; ++q) {
-            const int k = lane + 32 * q;
-            t.id[q] = k < p.top_k ? __ldg(p.ids + n * p.top_k + k) : -1;
-            t.value[q] = k < p.top_k ? __ldg(p.teacher + n * p.top_k + k) : -INFINITY;
+        for (int k = lane; k < p.top_k; k += 32) {
+            copy_word(&t.id[k], p.ids + n * p.top_k + k);
+            copy_word(&t.value[k], p.teacher + n * p.top_k + k);
         }
-#pragma unroll
-        for (int q = 0; q < kPerLane; ++q) {
-            if (t.id[q] < 0) t.value[q] = -INFINITY;
-            t.x[q] = t.id[q] >= 0 && t.id[q] < p.V ? view.at(t.id[q]) : -INFINITY;
+        tc::cp_async_commit();
+    };
+    auto fetched = [&](Listed& t) {
+        tc::cp_async_wait<0>();
+        for (int k = lane; k < n_list; k += 32) {
+            if (k >= p.top_k) t.id[k] = -1;
+            if (t.id[k] < 0) t.value[k] = -INFINITY;
         }
+        __syncwarp();
     };
     // (keeper) marks a row's listed tokens; whether something is wrong with them
     auto mark = [&](const Share<T>& s, const Listed& t) {
         bool bad = false;
-#pragma unroll
-        for (int q = 0; q < kPerLane; ++q) {
-            bad |= t.id[q] >= p.V || t.value[q] != t.value[q] || t.value[q] == INFINITY || t.x[q] != t.x[q];
-            if (t.id[q] >= s.v0 && t.id[q] < s.v1) {
-                const int b = s.bit(t.id[q]), piece = (b - 32) / kVec;
+        for (int k = lane; k < n_list; k += 32) {
+            const int id = t.id[k];
+            bad |= id >= p.V || t.value[k] != t.value[k] || t.value[k] == INFINITY;
+            if (id >= s.v0 && id < s.v1) {
+                const int b = s.bit(id), piece = (b - 32) / kVec;
                 if (!IN_BOUNDS(b >= 0 && b >> 5 < p.bit_words, p.dev_status)) continue;
                 bad |= (atomicOr(&bits[b >> 5], 1u << (b & 31)) >> (b & 31) & 1u) != 0;  // listed twice
                 if (b >= 32 && piece < s.n) atomicOr(&sh.marked[piece % kThreads], 1u << min(piece / kBatch, 31));
@@ -214,10 +222,9 @@ __global__ void __launch_bounds__(kAllThreads, kGrad ? 2 : 3) distill_kernel(con
         return __any_sync(0xFFFFFFFFu, bad);
     };
     auto unmark = [&](const Share<T>& s, const Listed& t) {
-#pragma unroll
-        for (int q = 0; q < kPerLane; ++q)
-            if (t.id[q] >= s.v0 && t.id[q] < s.v1) {
-                const int b = s.bit(t.id[q]), piece = (b - 32) / kVec;
+        for (int k = lane; k < n_list; k += 32)
+            if (t.id[k] >= s.v0 && t.id[k] < s.v1) {
+                const int b = s.bit(t.id[k]), piece = (b - 32) / kVec;
                 if (!IN_BOUNDS(b >= 0 && b >> 5 < p.bit_words, p.dev_status)) continue;
                 bits[b >> 5] = 0;
                 if (b >= 32 && piece < s.n) sh.marked[piece % kThreads] = 0;
@@ -273,14 +280,14 @@ __global__ void __launch_bounds__(kAllThreads, kGrad ? 2 : 3) distill_kernel(con
     float weight = weight_of(row);
     row = active(row, weight);
     float ahead = weight_of(row + clusters);
-    Listed now;
     bool bad_list = false;
     __syncthreads();
     if (row < p.rows) {
         const Share<T> s(p, row, rank);
         if (keeper) {
-            fetch(row, now);
-            bad_list = mark(s, now);
+            fetch(row, sh.list[0]);
+            fetched(sh.list[0]);
+            bad_list = mark(s, sh.list[0]);
         } else if (kGrad) {
             for (int b = 0; b < p.staged; ++b) copy_batch(s.pieces(), s.n, b);
         }
@@ -399,23 +406,31 @@ __global__ void __launch_bounds__(kAllThreads, kGrad ? 2 : 3) distill_kernel(con
             __syncthreads();  // the gradient is written, the next row's tokens are marked
         } else {
             // ---- the keeper: what does not wait for this row's sums
-            Listed then;
+            Listed &now = sh.list[parity], &then = sh.list[parity ^ 1];
             if (more) fetch(next, then);
-            float x_top = -INFINITY, v_top = -INFINITY;
+            const T* student = reinterpret_cast<const T*>(p.student) + row * p.stride;
+            float x[kPerLane], x_top = -INFINITY, v_top = -INFINITY;
 #pragma unroll
             for (int q = 0; q < kPerLane; ++q) {
-                x_top = fmaxf(x_top, now.x[q]);
-                v_top = fmaxf(v_top, now.value[q]);
+                const int id = 32 * q < n_list ? now.id[lane + 32 * q] : -1;
+                x[q] = id >= 0 && id < p.V ? Elem<T>::to_float(student[id]) : -INFINITY;
             }
+#pragma unroll
+            for (int q = 0; q < kPerLane; ++q) {
+                now.x[lane + 32 * q] = x[q];
+                bad_list |= x[q] != x[q];
+                x_top = fmaxf(x_top, x[q]);
+                if (32 * q < n_list) v_top = fmaxf(v_top, now.value[lane + 32 * q]);
+            }
+            bad_list = __any_sync(0xFFFFFFFFu, bad_list);
             x_top = warp_max(x_top);
             v_top = p.rest ? 0.0f : warp_max(v_top);  // (a list of -inf alone has no mass)
-            float prob[kPerLane], e_listed[kPerLane], mass = 0.0f, e_sum = 0.0f;
-#pragma unroll
-            for (int q = 0; q < kPerLane; ++q) {
-                prob[q] = now.value[q] > -INFINITY ? expf(now.value[q] - v_top) : 0.0f;
-                e_listed[q] = now.x[q] > -INFINITY ? exp2_approx((now.x[q] - x_top) * p.c2) : 0.0f;
-                mass += prob[q];
-                e_sum += e_listed[q];
+            float mass = 0.0f, e_sum = 0.0f;
+            for (int k = lane; k < n_list; k += 32) {
+                const float prob = now.value[k] > -INFINITY ? expf(now.value[k] - v_top) : 0.0f;
+                now.p[k] = prob;
+                mass += prob;
+                if (now.x[k] > -INFINITY) e_sum += exp2_approx((now.x[k] - x_top) * p.c2);
             }
             mass = warp_sum(mass);
             e_sum = warp_sum(e_sum);
@@ -440,14 +455,19 @@ __global__ void __launch_bounds__(kAllThreads, kGrad ? 2 : 3) distill_kernel(con
             cluster_wait();
             const Joined j = joined(parity, weight);
             const float w = weight * p.invT;
+            unmark(s, now);
+            if (more) {
+                fetched(then);
+                bad_list = mark(after, then);
+            }
+            __syncthreads();
             if (rank == 0) {
                 const float log_total = logf(j.total);
                 float term = 0.0f;
-#pragma unroll
-                for (int q = 0; q < kPerLane; ++q)
-                    if (prob[q] > 0.0f)
-                        term += prob[q] * scale *
-                                ((now.value[q] + log_scale) - ((now.x[q] - j.m_all) * p.invT - log_total));
+                for (int k = lane; k < n_list; k += 32)
+                    if (now.p[k] > 0.0f)
+                        term += now.p[k] * scale *
+                                ((now.value[k] + log_scale) - ((now.x[k] - j.m_all) * p.invT - log_total));
                 term = warp_sum(term);
                 if (j.p_rest > 0.0f)
                     term += j.p_rest * (logf(j.p_rest) - ((j.rest.m - j.m_all) * p.invT + logf(j.rest.s) - log_total));
@@ -456,18 +476,18 @@ __global__ void __launch_bounds__(kAllThreads, kGrad ? 2 : 3) distill_kernel(con
                     if (j.bad) report(p.dev_status, DSPARK_ERR_DEVICE_INPUT);
                 }
             }
-            unmark(s, now);
-            if (more) bad_list = mark(after, then);
-            __syncthreads();
             // the listed tokens' own gradients over those of the second pass
             if (kGrad && !j.bad) {
                 G* grad = reinterpret_cast<G*>(p.grad) + row * p.grad_stride;
-#pragma unroll
-                for (int q = 0; q < kPerLane; ++q)
-                    if (now.id[q] >= s.v0 && now.id[q] < s.v1)
-                        grad[now.id[q]] = grad_of<G>(w * (j.all_mass * (e_listed[q] * j.f_listed / j.total) - prob[q] * scale));
+                const float of_x = j.all_mass * j.f_listed / j.total;
+                for (int k = lane; k < n_list; k += 32) {
+                    const int id = now.id[k];
+                    if (id < s.v0 || id >= s.v1) continue;
+                    const float e = now.x[k] > -INFINITY ? exp2_approx((now.x[k] - x_top) * p.c2) : 0.0f;
+                    grad[id] = grad_of<G>(w * (of_x * e - now.p[k] * scale));
+                }
+                __syncwarp();
             }
-            now = then;
         }
         row = next;
         weight = next_weight;
