@@ -109,7 +109,7 @@ typedef struct CUstream_st* dspark_stream_t;
 #define DSPARK_GRAD_ACCUMULATE 1u   /* add to dW1 and dW2 instead of writing them        */
 
 /* Most alternatives of dspark_token_logprobs and listed tokens of dspark_distill_loss,
- * and the longest row (V) of either. */
+ * and the longest row (V) of either and of dspark_markov_grad. */
 #define DSPARK_TOP_MAX 128
 #define DSPARK_ROWS_MAX_V 4194304
 
@@ -768,7 +768,8 @@ int dspark_distill_loss(const void* student, int64_t student_stride, int student
  *   ws, ws_bytes dspark_workspace_size(DSPARK_OP_MARKOV_GRAD, 0, 0, V, rank, rows, DSPARK_BF16, 0)
  * A row with prev >= V is reported (DSPARK_ERR_DEVICE_INPUT), gives nothing to dW1 and dW2, and
  * its grad_prev is NaN.  rows == 0 gives zeros (dW2) without DSPARK_GRAD_ACCUMULATE.
- * Limits (DSPARK_ERR_UNSUPPORTED): rank % 64 == 0 up to 512, V % 8 == 0, rows <= 2^20 (dW1
+ * Limits (DSPARK_ERR_UNSUPPORTED): rank % 64 == 0 up to 512, V % 8 == 0 up to
+ * DSPARK_ROWS_MAX_V, rows <= 2^20 (dW1
  * compares every row's token with every other's); grad, W1, W2, grad_prev, dW1 and dW2 16-byte aligned, grad_stride a multiple of 8.
  */
 int dspark_markov_grad(const void* grad, int64_t grad_stride, const int32_t* prev, const void* W1,

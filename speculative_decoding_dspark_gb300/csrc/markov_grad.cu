@@ -566,13 +566,15 @@ int parts_of(int rows, int V, int rank) {
 
 struct Layout {
     size_t E, drop, part, total;
+    int parts;
 };
 Layout layout_of(int rows, int V, int rank) {
     Layout L;
     size_t off = 0;
     L.E = off; off += align256((size_t)rows * rank * 2);
     L.drop = off; off += align256((size_t)up(rows, kBlockK) * 8);
-    L.part = off; off += align256((size_t)parts_of(rows, V, rank) * rows * rank * 4);
+    L.parts = parts_of(rows, V, rank);
+    L.part = off; off += align256((size_t)L.parts * rows * rank * 4);
     L.total = std::max<size_t>(off, 256);
     return L;
 }
@@ -660,7 +662,7 @@ cudaError_t launch_markov_grad(const MarkovGradParams& p, cudaStream_t stream) {
     unsigned char* w = static_cast<unsigned char*>(p.ws);
     uint16_t* E = reinterpret_cast<uint16_t*>(w + L.E);
     float* part = reinterpret_cast<float*>(w + L.part);
-    const int parts = parts_of(p.rows, p.V, p.rank);
+    const int parts = L.parts;
     const int64_t stride = p.rows > 1 ? p.stride : p.V;
     CUtensorMap g_rows, g_cols, w2, before, sums, dW2;
     if (!encode(&g_rows, p.grad, p.V, p.rows, stride, kTileM) || !encode(&g_cols, p.grad, p.V, p.rows, stride, kBlockK) ||
