@@ -30,12 +30,16 @@
 namespace dspark {
 namespace {
 
-constexpr int kThreads = 256;  // that walk through the rows
-constexpr int kWarps = kThreads / 32;
-constexpr int kAllThreads = kThreads + 32;  // and the warp that keeps the listed tokens
+// kThreads walk through the rows, and a warp more keeps the listed tokens: the large CTA,
+// or the small one where a row has few pieces and what is done once per row counts.
+constexpr int kLarge = 256, kSmall = 64;
 constexpr int kUnroll = 4;     // pieces of a batch
 constexpr int kMaxCtas = 8;    // of a cluster
 constexpr int kPerLane = DSPARK_TOP_MAX / 32;
+// Rows of at most this many pieces take the small CTA, of which nine fit on an SM.  4096 rows, large and small, us: of 500,
+// 4096, 8192 and 16384 fp32 37 and 18, 44 and 30, 53 and 57, 76 and 132; of 4096, 16384 and 32000 bf16 57 and 29, 75 and
+// 76, 109 and 177.
+constexpr int kSmallPieces = 1792;
 
 struct Kept {  // what is known of a row's listed tokens before its sums are
     float x_top, e_sum;  // the largest logit, the sum of 2^((x - x_top) c2)
@@ -52,9 +56,10 @@ struct Listed {
     float p[DSPARK_TOP_MAX];     // exp(value - its reference)
 };
 
+template <int kThreads>
 struct Shared {
     Listed list[2];                    // by the row's parity
-    float2 sums[2][kMaxCtas][kWarps];  // (m, s) of all warps of the cluster, by the row's parity
+    float2 sums[2][kMaxCtas][kThreads / 32];  // (m, s) of all warps of the cluster, by the row's parity
     float bad[2][kMaxCtas];            // whether a CTA found fault with the listed tokens
     Kept kept[2];
     uint32_t marked[kThreads];         // which batches of a thread hold listed tokens (bit 31: the 32nd or a later one)
@@ -99,7 +104,7 @@ __device__ __forceinline__ void store_piece(uint16_t* p, const float (&x)[8]) {
 }
 
 // This CTA's share of a gradient row of weight 0.
-template <typename G>
+template <typename G, int kAllThreads>
 __device__ __forceinline__ void clear_grad(G* g, int V, int rank, int size) {
     constexpr int kVec = 16 / sizeof(G);
     const int head = min(V, (int)(((16 - (reinterpret_cast<uintptr_t>(g) & 15)) & 15) / sizeof(G)));
@@ -145,16 +150,15 @@ struct Share {
     __device__ __forceinline__ const uint4* pieces() const { return view.base + first; }
     // The bit of its element v (a word is kept for the edges on either side).
     __device__ __forceinline__ int bit(int v) const { return v - view.head - first * Elem<T>::kVec + 32; }
-    __device__ __forceinline__ int batches() const { return (n + kUnroll * kThreads - 1) / (kUnroll * kThreads); }
 };
 
 // T: the logits' elements, G: the gradient's, kGrad: there is one.
-template <typename T, typename G, bool kGrad>
-__global__ void __launch_bounds__(kAllThreads, kGrad && sizeof(T) == 4 ? 2 : 3) distill_kernel(const DistillParams p) {
-    constexpr int kVec = Elem<T>::kVec;
+template <typename T, typename G, bool kGrad, int kThreads>
+__global__ void __launch_bounds__(kThreads + 32, kThreads == kLarge ? 3 : 9) distill_kernel(const DistillParams p) {
+    constexpr int kVec = Elem<T>::kVec, kWarps = kThreads / 32, kAllThreads = kThreads + 32;
     constexpr int kBatch = kUnroll * kThreads;  // pieces
     extern __shared__ uint4 dyn[];
-    __shared__ Shared sh;
+    __shared__ Shared<kThreads> sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const bool keeper = warp == kWarps;
     const int rank = (int)cluster_rank(), size = 1 << p.log_ctas;
@@ -168,7 +172,7 @@ __global__ void __launch_bounds__(kAllThreads, kGrad && sizeof(T) == 4 ? 2 : 3) 
     // The next row from n on that has a weight; those that have none are done with.
     auto active = [&](int64_t n, float& w) {
         while (n < p.rows && w == 0.0f) {
-            if (kGrad) clear_grad(reinterpret_cast<G*>(p.grad) + n * p.grad_stride, p.V, rank, size);
+            if (kGrad) clear_grad<G, kAllThreads>(reinterpret_cast<G*>(p.grad) + n * p.grad_stride, p.V, rank, size);
             if (rank == 0 && tid == 0) p.loss[n] = 0.0f;
             n += clusters;
             w = weight_of(n);
@@ -242,7 +246,7 @@ __global__ void __launch_bounds__(kAllThreads, kGrad && sizeof(T) == 4 ? 2 : 3) 
     auto joined = [&](int parity, float weight) {
         Joined j;
         const Kept kept = sh.kept[parity];
-        constexpr int kEach = kMaxCtas * kWarps / 32;
+        constexpr int kEach = (kMaxCtas * kWarps + 31) / 32;
         SoftSum each[kEach], t;
         const int n_sums = size * kWarps;
 #pragma unroll
@@ -302,7 +306,7 @@ __global__ void __launch_bounds__(kAllThreads, kGrad && sizeof(T) == 4 ? 2 : 3) 
         const bool more = next < p.rows;
         const Share<T> after(p, more ? next : row, rank);
         if (!keeper) {
-            const int n_batches = s.batches();
+            const int n_batches = (s.n + kBatch - 1) / kBatch;
             const int v_edge = warp == 0 ? s.view.edge(lane, rank == 0, rank == size - 1) : -1;
             const float x_edge = v_edge >= 0 ? s.view.at(v_edge) : -INFINITY;
             const uint32_t marked = sh.marked[tid];
@@ -496,37 +500,45 @@ __global__ void __launch_bounds__(kAllThreads, kGrad && sizeof(T) == 4 ? 2 : 3) 
     cluster_sync();  // (no CTA ends while another may still write to its shared memory)
 }
 
-template <typename T>
+template <typename T, int kThreads>
 const void* kernel_of(bool grad, int grad_dtype) {
-    if (!grad) return (const void*)distill_kernel<T, float, false>;
-    return grad_dtype == DSPARK_F32 ? (const void*)distill_kernel<T, float, true>
-                                    : (const void*)distill_kernel<T, uint16_t, true>;
+    if (!grad) return (const void*)distill_kernel<T, float, false, kThreads>;
+    return grad_dtype == DSPARK_F32 ? (const void*)distill_kernel<T, float, true, kThreads>
+                                    : (const void*)distill_kernel<T, uint16_t, true, kThreads>;
+}
+template <typename T>
+const void* kernel_of(bool grad, int grad_dtype, bool small) {
+    return small ? kernel_of<T, kSmall>(grad, grad_dtype) : kernel_of<T, kLarge>(grad, grad_dtype);
 }
 
 }  // namespace
 
 cudaError_t launch_distill(DistillParams p, cudaStream_t stream) {
-    constexpr size_t kShare = 104 * 1024;  // shared memory of a CTA, so that two fit on an SM
     const int vec = p.dtype == DSPARK_F32 ? 4 : 8;
     const int64_t pieces = p.V / vec;
+    const bool small = pieces <= kSmallPieces;
+    const int threads = small ? kSmall : kLarge;
+    // Shared memory of a CTA, so that three large ones fit on an SM (a row's last batch is read again then, of 151936 fp32
+    // over eight CTAs the fifth).  Three with all but that, two with all of it: 170 and 174 us for 896 rows of 151936 fp32.
+    const size_t kShare = 68 * 1024;
     int ctas = 1;
-    auto batches_of = [&](int c) { return (int)(((pieces + c - 1) / c + kUnroll * kThreads - 1) / (kUnroll * kThreads)); };
+    auto batches_of = [&](int c) { return (int)(((pieces + c - 1) / c + kUnroll * threads - 1) / (kUnroll * threads)); };
     auto bits_of = [&](int c) { return (int)(((pieces + c - 1) / c * vec + 31) / 32 + 2); };
-    auto smem_of = [&](int c, int batches) { return (size_t)batches * kUnroll * kThreads * 16 + (size_t)bits_of(c) * 4; };
+    auto smem_of = [&](int c, int batches) { return (size_t)batches * kUnroll * threads * 16 + (size_t)bits_of(c) * 4; };
     auto larger = [&](int c) {
-        return smem_of(c, p.grad ? batches_of(c) : 0) > kShare || ((int64_t)p.rows * c < 152 && pieces / c > 2 * kThreads);
+        return smem_of(c, p.grad ? batches_of(c) : 0) > kShare || ((int64_t)p.rows * c < 152 && pieces / c > 2 * kLarge);
     };
     while (ctas < kMaxCtas && larger(ctas)) ctas *= 2;
-    p.staged = p.grad ? std::min<int64_t>(batches_of(ctas), (int64_t)((kShare - std::min(kShare, smem_of(ctas, 0))) / (kUnroll * kThreads * 16))) : 0;
+    p.staged = p.grad ? std::min<int64_t>(batches_of(ctas), (int64_t)((kShare - std::min(kShare, smem_of(ctas, 0))) / (kUnroll * threads * 16))) : 0;
     p.bit_words = bits_of(ctas);
     p.log_ctas = ctas == 1 ? 0 : ctas == 2 ? 1 : ctas == 4 ? 2 : 3;
     const size_t smem = smem_of(ctas, p.staged);
-    const void* fn = p.dtype == DSPARK_F32 ? kernel_of<float>(p.grad != nullptr, p.grad_dtype)
-                                           : kernel_of<uint16_t>(p.grad != nullptr, p.grad_dtype);
+    const void* fn = p.dtype == DSPARK_F32 ? kernel_of<float>(p.grad != nullptr, p.grad_dtype, small)
+                                           : kernel_of<uint16_t>(p.grad != nullptr, p.grad_dtype, small);
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.blockDim = dim3(kAllThreads);
+    cfg.blockDim = dim3(threads + 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
