@@ -85,6 +85,61 @@ __device__ __forceinline__ float bound_of(const float* maxima, int want) {
     return of_order(low);
 }
 
+// Leaves of a long list those that reach a bound which K of them do, and not many
+// more (as bound_of, by all threads): ranking costs the square of the list's length.
+__device__ __noinline__ void shorten(Shared& sh, int K) {
+    constexpr int kEach = kCandidates / kThreads;
+    const int tid = threadIdx.x, found = (int)sh.n_cand;
+    uint64_t mine[kEach];
+    uint32_t low = 0xFFFFFFFFu, high = 0;
+#pragma unroll
+    for (int q = 0; q < kEach; ++q) {
+        const int c = tid + q * kThreads;
+        mine[q] = c < found ? sh.cand[c] : 0;  // (0: below every candidate)
+        if (c < found) {
+            low = min(low, (uint32_t)(mine[q] >> 32));
+            high = max(high, (uint32_t)(mine[q] >> 32));
+        }
+    }
+    low = __reduce_min_sync(0xFFFFFFFFu, low);
+    high = __reduce_max_sync(0xFFFFFFFFu, high);
+    if ((tid & 31) == 0) {
+        sh.hist[tid >> 5] = low;
+        sh.hist[kWarps + (tid >> 5)] = high;
+    }
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) {
+        low = min(low, sh.hist[w]);
+        high = max(high, sh.hist[kWarps + w]);
+    }
+    ++high;
+    while (high - low > 1) {
+        const uint32_t mid = low + (high - low) / 2;
+        int n = 0;
+#pragma unroll
+        for (int q = 0; q < kEach; ++q) n += (uint32_t)(mine[q] >> 32) >= mid;
+        n = __reduce_add_sync(0xFFFFFFFFu, n);
+        __syncthreads();
+        if ((tid & 31) == 0) sh.count[tid >> 5] = (uint32_t)n;
+        __syncthreads();
+        n = 0;
+        for (int w = 0; w < kWarps; ++w) n += (int)sh.count[w];
+        if (n >= K) {
+            low = mid;
+            if (n <= K + 1 + K / 4) break;
+        } else {
+            high = mid;
+        }
+    }
+    __syncthreads();
+    if (tid == 0) sh.n_cand = 0;
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kEach; ++q)
+        if (mine[q] != 0 && (uint32_t)(mine[q] >> 32) >= low) sh.cand[atomicAdd(&sh.n_cand, 1u)] = mine[q];
+    __syncthreads();
+}
+
 // The K best when the list was too short; leaves exactly K of them in sh.cand.
 template <typename T>
 __device__ __noinline__ void select_by_bits(const T* row, int V, int K, Shared& sh) {
@@ -313,7 +368,10 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsParams
         if (kEntropy) p.entropy[n] = log_s - kLn2F * (all.u / all.s);
     }
     if (kTop) {
-        if (sh.n_cand > (uint32_t)kCandidates) select_by_bits<T>(row, p.V, p.top_k, sh);
+        if (sh.n_cand > (uint32_t)kCandidates)
+            select_by_bits<T>(row, p.V, p.top_k, sh);
+        else if (sh.n_cand > (uint32_t)(2 * p.top_k + 64))
+            shorten(sh, p.top_k);
         const int found = (int)sh.n_cand;
         // four threads to a candidate, each against a quarter of the others
         for (int c0 = 0; c0 < found; c0 += kThreads / 4) {
