@@ -731,7 +731,8 @@ int dspark_token_logprobs(const void* logits, int64_t row_stride, int dtype, con
  * token a row has loss and gradient 0.
  *
  *   student      [rows, V] student_dtype (F32 or BF16), student_stride elements from row to row
- *                (for instance dspark_markov_draft's q_logits, which are scaled already: temperature 1)
+ *                (for instance dspark_markov_draft's q_logits, which are scaled already: temperature 1,
+ *                and row weights times invT where the gradient is to be that of U + W2 . W1[prev])
  *   teacher_ids [rows, top_k] int32, teacher_logprobs [rows, top_k] fp32, 1 <= top_k <= DSPARK_TOP_MAX
  *   row_weight   [rows] fp32, or NULL: all 1
  *   loss         [rows] fp32 out
