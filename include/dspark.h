@@ -770,7 +770,7 @@ int dspark_distill_loss(const void* student, int64_t student_stride, int student
  * A row with prev >= V is reported (DSPARK_ERR_DEVICE_INPUT), gives nothing to dW1 and dW2, and
  * its grad_prev is NaN.  rows == 0 gives zeros (dW2) without DSPARK_GRAD_ACCUMULATE.
  * Limits (DSPARK_ERR_UNSUPPORTED): rank % 64 == 0 up to 512, V % 8 == 0 up to
- * DSPARK_ROWS_MAX_V, rows <= 2^20 (dW1
+ * DSPARK_ROWS_MAX_V, rows <= 2^19 (dW1
  * compares every row's token with every other's); grad, W1, W2, grad_prev, dW1 and dW2 16-byte aligned, grad_stride a multiple of 8.
  */
 int dspark_markov_grad(const void* grad, int64_t grad_stride, const int32_t* prev, const void* W1,

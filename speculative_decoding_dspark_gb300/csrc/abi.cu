@@ -141,7 +141,7 @@ bool valid_rows(const void* x, int64_t stride, int dtype, int V) {
 }
 
 bool markov_grad_supported(int rows, int V, int rank) {
-    return rows >= 0 && V > 0 && rank > 0 && rank % 64 == 0 && rank <= 512 && V % 8 == 0 && V <= DSPARK_ROWS_MAX_V && rows <= (1 << 20);
+    return rows >= 0 && V > 0 && rank > 0 && rank % 64 == 0 && rank <= 512 && V % 8 == 0 && V <= DSPARK_ROWS_MAX_V && rows <= (1 << 19);
 }
 
 // Process-wide settings of the grid-wide waits (see dspark_set_wait_limit_ns).

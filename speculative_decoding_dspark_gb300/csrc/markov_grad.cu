@@ -35,8 +35,7 @@ constexpr int kThreads = 32 * (kEpilogueWarps + 2);
 constexpr int kPiece = 32 * 32 * 4;    // 32 rows of 32 sums: what a warp hands to one store
 constexpr uint32_t kIdescATransposed = 1u << 15;
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr int kGatherRows = 16;
-constexpr int kKnown = 2560;           // stages (of rows) whose words are looked at once; a multiple of kThreads
+constexpr int kMaxRows = 1 << 19;
 constexpr int kGridSms = 152;          // what the parts of a sum are counted for
 
 // A tile of kCtas x 128 rows and 256 columns by kCtas CTAs: each holds its rows of A and
@@ -56,7 +55,8 @@ struct Product {
     int tiles_n, tiles;    // tiles along the columns, in all
     int parts, per;        // parts of a sum, stages in each
     int accumulate;
-    const uint64_t* drop;  // a bit per row of g that is to be cleared (dW2), a word per stage
+    const uint8_t* drop;   // rows of g that are to be cleared (dW2)
+    int rows;              // of g (dW2)
     int inject;            // 1 (tests): no stage is ever complete
     int32_t* dev_status;
 };
@@ -65,7 +65,7 @@ struct Barriers {
     uint64_t full[6], empty[6], land[6], tfull[2], tempty[2], drain;
     uint32_t tmem;
     int abort_flag;
-    uint32_t has_drop[kKnown / 32];  // a bit per stage: some of its rows are to be cleared
+    uint32_t has_drop[kMaxRows / kBlockK / 32];  // a bit per stage: some of its rows are to be cleared
 };
 
 // ---- what a pair of CTAs does together (a pair's first CTA issues the products of both)
@@ -228,12 +228,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (kCtas > 1) pair_sync();
     tc::tc_fence_after();
     const uint32_t tmem = sh.tmem;
-    launch_dependents();
     wait_prior_grid();
+    launch_dependents();
+    auto marked = [&](int n) { return n < p.rows && __ldcg(p.drop + n) != 0; };
     if (kSumRows) {
-        for (int k = tid; k < kKnown; k += kThreads) {
-            const unsigned any = __ballot_sync(0xFFFFFFFFu, k < p.blocks && __ldcg(p.drop + k) != 0);
-            if (lane == 0) sh.has_drop[k >> 5] = any;
+        for (int w = warp; 32 * w < p.blocks; w += kThreads / 32) {
+            uint32_t any = 0;
+#pragma unroll 8
+            for (int k = 32 * w; k < min(32 * w + 32, p.blocks); ++k)
+                if (__any_sync(0xFFFFFFFFu, marked(kBlockK * k + lane) || marked(kBlockK * k + 32 + lane))) any |= 1u << (k & 31);
+            if (lane == 0) sh.has_drop[w] = any;
         }
         __syncthreads();
     }
@@ -257,12 +261,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // rows that give nothing and hold a NaN or an infinity: cleared once they have landed.  (Clearing every row without a
     // token instead made markov_step's dW2 309 us where it is 264.)
-    auto dropped = [&](int k) -> uint64_t {
-        if (!kSumRows || (k < kKnown && !(sh.has_drop[k >> 5] >> (k & 31) & 1u))) return 0;
-        return __ldcg(p.drop + k);
-    };
+    auto dropped = [&](int k) { return kSumRows && (sh.has_drop[k >> 5] >> (k & 31) & 1u); };
     uint32_t landed = 0;  // parities
-    auto clear = [&](uint64_t drop, int s) {
+    auto clear = [&](int k, int s) {
+        uint64_t drop = __ballot_sync(0xFFFFFFFFu, marked(kBlockK * k + lane));
+        drop |= (uint64_t)__ballot_sync(0xFFFFFFFFu, marked(kBlockK * k + 32 + lane)) << 32;
         const bool go = __all_sync(0xFFFFFFFFu, wait_bounded(&sh.land[s], landed >> s & 1u, abort_flag));
         landed ^= 1u << s;
         if (go) {
@@ -291,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t bytes = kABytes + cols / 64 * kGroup;
                 for (int k = x.k0; k < x.k1; ++k, ++i) {
                     const int s = i % kStages;
-                    const bool fix = dropped(k) != 0;
+                    const bool fix = dropped(k);
                     if (i >= kStages && !(go = wait_bounded(&sh.empty[s], (i / kStages - 1) & 1, abort_flag))) break;
                     unsigned char* a = ring + s * R::kStageBytes;
                     unsigned char* b = a + kABytes;
@@ -323,8 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Unit x = unit_of(u);
             if (cta != 0) {  // the other CTA of a pair has rows to clear, at most
                 for (int k = x.k0; go && k < x.k1; ++k, ++i) {
-                    const uint64_t drop = dropped(k);
-                    if (drop) go = clear(drop, i % kStages);
+                    if (dropped(k)) go = clear(k, i % kStages);
                 }
                 continue;
             }
@@ -338,8 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int c1 = min(x.k1, c0 + kChain);
                 for (int k = c0; k < c1; ++k, ++i) {
                     const int s = i % kStages;
-                    const uint64_t drop = dropped(k);
-                    if (drop && !(go = clear(drop, s))) break;
+                    if (dropped(k) && !(go = clear(k, s))) break;
                     if (!(go = __all_sync(0xFFFFFFFFu, wait_bounded(&sh.full[s], (i / kStages) & 1, abort_flag)))) break;
                     tc::tc_fence_after();
                     const uint32_t sa = tc::smem_u32(ring + s * R::kStageBytes);
@@ -448,32 +449,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// ---- W1 rows of the previous tokens (zeros where there is none); no row marked yet
-__global__ void __launch_bounds__(32 * kGatherRows) gather_kernel(const MarkovGradParams p, uint16_t* E, uint64_t* drop) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int n = blockIdx.x * kGatherRows + warp;
-    wait_prior_grid();
-    if (n < p.rows) {
-        const int a = p.prev[n];
-        const bool there = a >= 0 && a < p.V;
-        if (lane == 0) {
-            if (a >= p.V) report(p.dev_status, DSPARK_ERR_DEVICE_INPUT);
-            if (n % kBlockK == 0) drop[n / kBlockK] = 0;
-        }
-        for (int i = lane; i < p.rank / 8; i += 32)
-            reinterpret_cast<uint4*>(E + (size_t)n * p.rank)[i] =
-                there ? __ldg(reinterpret_cast<const uint4*>(p.W1 + (size_t)a * p.rank) + i) : make_uint4(0, 0, 0, 0);
-    }
-    launch_dependents();
-}
-
 // ---- the parts of grad_prev: every group of threads adds its own in order, then the groups in order.
-// A row without a token gives nothing, and its sums are not all finite if a NaN or an infinity stands in
-// it: such rows are marked, to be cleared on their way into dW2's products (where their W1 row is zeros,
-// which would do for any others).
+// The row's W1 row goes to E, what dW2's products take of it: zeros for a row without a token, which gives
+// nothing.  If a NaN or an infinity stands in such a row zeros do not do, and its sums are not all finite: it is
+// marked, to be cleared on its way into the products.
 constexpr int kJoinThreads = 512;  // at most
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const MarkovGradParams p, const float* part, int parts,
-                                                            unsigned long long* drop) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const MarkovGradParams p, const float* part, int parts, uint16_t* E,
+                                                            uint8_t* drop) {
     __shared__ float4 sums[kJoinThreads];
     const int n = blockIdx.x, quads = p.rank / 4, groups = blockDim.x / quads;
     const int i = threadIdx.x % quads, g = threadIdx.x / quads;
@@ -492,50 +474,78 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const MarkovGradPara
     }
     sums[threadIdx.x] = s;
     __syncthreads();
+    const int a = p.prev[n];
+    const bool there = a >= 0 && a < p.V;
+    if (threadIdx.x < p.rank / 8)
+        reinterpret_cast<uint4*>(E + (size_t)n * p.rank)[threadIdx.x] =
+            there ? __ldg(reinterpret_cast<const uint4*>(p.W1 + (size_t)a * p.rank) + threadIdx.x) : make_uint4(0, 0, 0, 0);
+    bool odd = false;
     if (g == 0) {
-        const int a = p.prev[n];
         for (int o = 1; o < groups; ++o) {
             const float4 x = sums[o * quads + i];
             s = make_float4(s.x + x.x, s.y + x.y, s.z + x.z, s.w + x.w);
         }
-        if ((a < 0 || a >= p.V) && !(fabsf(s.x) < INFINITY && fabsf(s.y) < INFINITY && fabsf(s.z) < INFINITY && fabsf(s.w) < INFINITY))
-            atomicOr(drop + n / kBlockK, 1ull << (n % kBlockK));
+        odd = !there && !(fabsf(s.x) < INFINITY && fabsf(s.y) < INFINITY && fabsf(s.z) < INFINITY && fabsf(s.w) < INFINITY);
         if (a < 0) s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (a >= p.V) s = make_float4(NAN, NAN, NAN, NAN);
         reinterpret_cast<float4*>(p.grad_prev + (size_t)n * p.rank)[i] = s;
     }
+    odd = __syncthreads_or(odd);
+    if (threadIdx.x == 0) {
+        drop[n] = odd;
+        if (a >= p.V) report(p.dev_status, DSPARK_ERR_DEVICE_INPUT);
+    }
     launch_dependents();
 }
 
-// ---- dW1: the first row of each previous token adds up all of them, in order
-__global__ void __launch_bounds__(128) scatter_kernel(const MarkovGradParams p) {
-    const int n = blockIdx.x;
-    wait_prior_grid();
-    const int a = p.prev[n];
-    if (a < 0 || a >= p.V) return;
-    int seen = 0;
-    for (int m = threadIdx.x; m < n; m += 128) seen |= p.prev[m] == a;
-    if (__syncthreads_or(seen)) return;
-    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const int i = threadIdx.x;
-    for (int m0 = n; m0 < p.rows; m0 += 32) {
-        const int m = m0 + (threadIdx.x & 31);
-        unsigned same = __ballot_sync(0xFFFFFFFFu, m < p.rows && p.prev[m] == a);
-        for (; same; same &= same - 1) {
-            if (4 * i < p.rank) {
-                const float4 x =
-                    reinterpret_cast<const float4*>(p.grad_prev + (size_t)(m0 + __ffs(same) - 1) * p.rank)[i];
-                s = make_float4(s.x + x.x, s.y + x.y, s.z + x.z, s.w + x.w);
+// ---- dW1: the first row of each previous token adds up all of them, in order.  A row to a warp; the tokens are
+// looked through in shared memory.  Launched after dW2's product, it runs on the SMs that the product has left: it
+// may start once the product has itself waited for join_kernel, whose sums are all that this needs.  (What others wrote
+// is read from L2: a kernel that has not waited may find older lines in L1.)
+constexpr int kScatterRows = 16, kScatterTile = 2048;
+__global__ void __launch_bounds__(32 * kScatterRows) scatter_kernel(const MarkovGradParams p) {
+    __shared__ int32_t token[kScatterTile];
+    const int lane = threadIdx.x & 31, n = blockIdx.x * kScatterRows + (threadIdx.x >> 5);
+    if (!p.dW2) wait_prior_grid();
+    const int a = n < p.rows ? __ldcg(p.prev + n) : -1;
+    bool mine = a >= 0 && a < p.V;  // until an earlier row has the token
+    constexpr int kQuads = 4;       // rank <= 512
+    float4 s[kQuads];
+#pragma unroll
+    for (int q = 0; q < kQuads; ++q) s[q] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int m0 = 0; m0 < p.rows; m0 += kScatterTile) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < min(kScatterTile, p.rows - m0); i += 32 * kScatterRows) token[i] = __ldcg(p.prev + m0 + i);
+        if (!__syncthreads_or(mine)) break;
+        for (int i0 = 0; mine && i0 < min(kScatterTile, p.rows - m0); i0 += 32) {
+            const int m = m0 + i0 + lane;
+            unsigned same = __ballot_sync(0xFFFFFFFFu, m < p.rows && token[i0 + lane] == a);
+            if (same && m0 + i0 + __ffs(same) - 1 < n) mine = false;
+            for (; mine && same; same &= same - 1) {
+                const float4* x = reinterpret_cast<const float4*>(p.grad_prev + (size_t)(m0 + i0 + __ffs(same) - 1) * p.rank);
+#pragma unroll
+                for (int q = 0; q < kQuads; ++q)
+                    if (4 * (lane + 32 * q) < p.rank) {
+                        const float4 y = __ldcg(x + lane + 32 * q);
+                        s[q] = make_float4(s[q].x + y.x, s[q].y + y.y, s[q].z + y.z, s[q].w + y.w);
+                    }
             }
         }
     }
-    if (4 * i >= p.rank) return;
-    float4* d = reinterpret_cast<float4*>(p.dW1 + (size_t)a * p.rank) + i;
-    if (p.accumulate) {
-        const float4 o = *d;
-        s = make_float4(o.x + s.x, o.y + s.y, o.z + s.z, o.w + s.w);
+    if (mine) {
+        float4* d = reinterpret_cast<float4*>(p.dW1 + (size_t)a * p.rank);
+#pragma unroll
+        for (int q = 0; q < kQuads; ++q)
+            if (4 * (lane + 32 * q) < p.rank) {
+                float4 y = s[q];
+                if (p.accumulate) {
+                    const float4 o = __ldcg(d + lane + 32 * q);
+                    y = make_float4(o.x + y.x, o.y + y.y, o.z + y.z, o.w + y.w);
+                }
+                d[lane + 32 * q] = y;
+            }
     }
-    *d = s;
+    if (p.dW2) wait_prior_grid();  // (it ends after the product, as what follows it expects)
 }
 
 // ------------------------------------------------------------------------------- host
@@ -572,7 +582,7 @@ Layout layout_of(int rows, int V, int rank) {
     Layout L;
     size_t off = 0;
     L.E = off; off += align256((size_t)rows * rank * 2);
-    L.drop = off; off += align256((size_t)up(rows, kBlockK) * 8);
+    L.drop = off; off += align256((size_t)rows);
     L.parts = parts_of(rows, V, rank);
     L.part = off; off += align256((size_t)L.parts * rows * rank * 4);
     L.total = std::max<size_t>(off, 256);
@@ -669,9 +679,6 @@ cudaError_t launch_markov_grad(const MarkovGradParams& p, cudaStream_t stream) {
         !encode(&w2, p.W2, p.rank, p.V, p.rank, kBlockK) || !encode(&before, E, p.rank, p.rows, p.rank, kBlockK) ||
         !encode_sums(&sums, part, p.rank, p.rows, parts) || (p.dW2 && !encode_sums(&dW2, p.dW2, p.rank, p.V, 1)))
         return cudaErrorInvalidValue;
-    if ((e = launch_after(gather_kernel, dim3(up(p.rows, kGatherRows)), 32 * kGatherRows, 0, stream, p, E,
-                          reinterpret_cast<uint64_t*>(w + L.drop))) != cudaSuccess)
-        return e;
     Product q{};
     q.rank = p.rank;
     q.dev_status = p.dev_status;
@@ -682,15 +689,14 @@ cudaError_t launch_markov_grad(const MarkovGradParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     // (groups of threads, four parts each)
     const int quads = p.rank / 4, groups = std::min(std::max(parts / 4, 1), kJoinThreads / quads);
-    if ((e = launch_after(join_kernel, dim3(p.rows), quads * groups, 0, stream, p, part, parts,
-                          reinterpret_cast<unsigned long long*>(w + L.drop))) != cudaSuccess)
-        return e;
-    if (p.dW1 && (e = launch_after(scatter_kernel, dim3(p.rows), 128, 0, stream, p)) != cudaSuccess) return e;
+    uint8_t* drop = w + L.drop;
+    if ((e = launch_after(join_kernel, dim3(p.rows), quads * groups, 0, stream, p, part, parts, E, drop)) != cudaSuccess) return e;
     if (p.dW2) {
         q.M = p.V; q.blocks = up(p.rows, kBlockK); q.parts = 1; q.accumulate = p.accumulate;
-        q.drop = reinterpret_cast<const uint64_t*>(w + L.drop);
+        q.drop = drop; q.rows = p.rows;
         if ((e = launch_product<true, 2>(q, g_cols, before, dW2, n_sm, stream)) != cudaSuccess) return e;
     }
+    if (p.dW1 && (e = launch_after(scatter_kernel, dim3(up(p.rows, kScatterRows)), 32 * kScatterRows, 0, stream, p)) != cudaSuccess) return e;
     return cudaSuccess;
 }
 

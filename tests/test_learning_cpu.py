@@ -72,7 +72,7 @@ def test_distill_refusals(lib, change, status):
     (dict(rows=-1), INVALID), (dict(V=0), INVALID), (dict(rank=0), INVALID), (dict(g=None), INVALID), (dict(prev=None), INVALID),
     (dict(W1=None), INVALID), (dict(W2=None), INVALID), (dict(gp=None), INVALID), (dict(stride=992), INVALID),
     (dict(flags=2), INVALID), (dict(rank=96), UNSUPPORTED), (dict(rank=576), UNSUPPORTED), (dict(V=996), UNSUPPORTED),
-    (dict(stride=1004), UNSUPPORTED), (dict(rows=(1 << 20) + 1), UNSUPPORTED), (dict(V=(1 << 22) + 8, stride=1 << 23), UNSUPPORTED), (dict(g=vp(4104)), UNSUPPORTED),
+    (dict(stride=1004), UNSUPPORTED), (dict(rows=(1 << 19) + 1), UNSUPPORTED), (dict(V=(1 << 22) + 8, stride=1 << 23), UNSUPPORTED), (dict(g=vp(4104)), UNSUPPORTED),
     (dict(W2=vp(4104)), UNSUPPORTED), (dict(dW2=vp(4104)), UNSUPPORTED), (dict(ws=None), WORKSPACE),
     (dict(ws=vp(4096 + 16)), WORKSPACE), (dict(ws_bytes=100), WORKSPACE),
 ])
