@@ -8,8 +8,9 @@
 // The K best: a thread's largest value is one of the row's values, so whatever K
 // of the threads' maxima reach, at least K values reach: a bound found by bisecting
 // the values' bits until K maxima or few more reach it (one warp, the maxima in its
-// registers).  In a cluster of C CTAs each finds the bound that K / C of its own
-// maxima reach, and the lowest serves.  The pass leaves the maximum of every batch
+// registers).  In a cluster of C CTAs each finds the bounds that K / C and that K of its
+// own maxima reach; the lowest of the former serves, or the highest of the latter
+// if that is higher (a mask may leave a CTA nothing).  The pass leaves the maximum of every batch
 // of 32 elements in shared memory; only batches whose maximum reaches the bound are
 // read again (from L2, by as many threads as there are pieces), and the values that
 // reach it, the candidates, are ranked by counting: the value falls, then the place
@@ -48,6 +49,7 @@ struct Shared {
     SoftSum part[kWarps];
     SoftSum row;      // this CTA's part of the row
     float bound;      // what at least K / C of its threads' maxima reach
+    float own_bound;  // what at least K of them reach (C > 1)
     uint32_t n_cand;  // leader: candidates of all CTAs
     uint32_t n_hits;  // batches whose maximum reaches the bound
     uint32_t hits[kHits];
@@ -292,6 +294,10 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsParams
         const float bound = bound_of(sh.maxima, (p.top_k + size - 1) / size);
         if (lane == 0) sh.bound = bound;
     }
+    if (kTop && warp == 2 && size > 1) {
+        const float bound = bound_of(sh.maxima, p.top_k);
+        if (lane == 0) sh.own_bound = bound;
+    }
     if (size > 1)
         cluster_sync();
     else
@@ -309,7 +315,14 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsParams
     }
     if (kTop) {
         float bound = sh.bound;
-        for (uint32_t c = 0; c < size; ++c) bound = fminf(bound, cluster_ld_f32(cluster_map(&sh.bound, c)));
+        if (size > 1) {
+            float own = -INFINITY;
+            for (uint32_t c = 0; c < size; ++c) {
+                bound = fminf(bound, cluster_ld_f32(cluster_map(&sh.bound, c)));
+                own = fmaxf(own, cluster_ld_f32(cluster_map(&sh.own_bound, c)));
+            }
+            bound = fmaxf(bound, own);
+        }
         const uint32_t list = cluster_map(sh.cand, 0), count = cluster_map(&sh.n_cand, 0);
         auto offer = [&](float x, int v) {
             const uint32_t c = size > 1 ? cluster_atomic_add(count, 1u) : atomicAdd(&sh.n_cand, 1u);

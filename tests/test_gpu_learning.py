@@ -117,7 +117,7 @@ def test_logprobs_without_tokens_or_lists(B):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("kind", ["equal", "few", "rising", "falling", "thread", "zeros", "masked", "lowest", "peak", "steps"])
+@pytest.mark.parametrize("kind", ["equal", "few", "rising", "falling", "thread", "zeros", "masked", "lowest", "peak", "steps", "window"])
 @pytest.mark.parametrize("V,top", [(5000, 128), (70001, 128), (70001, 3), (300, 20), (151936, 1)])
 def test_logprobs_orders(B, dtype, kind, V, top):
     """Values that come in orders and in numbers that a list of candidates is not made for."""
@@ -134,6 +134,7 @@ def test_logprobs_orders(B, dtype, kind, V, top):
         "lowest": lambda: torch.where(v % 97 == 5, v % 13, float(torch.finfo(dtype).min)),
         "peak": lambda: torch.where(v == V // 2, 80.0, -30.0 + v / V),
         "steps": lambda: torch.floor(v / 1100) % 7,
+        "window": lambda: torch.where((v > 0.6 * V) & (v < 0.65 * V), torch.randn(V, generator=g, device="cuda"), -INF),
     }[kind]()
     x = torch.stack([x, x.flip(0), x.roll(V // 3)]).to(dtype)
     check_logprobs(B, x, i32([0, V - 1, V // 2]), 1.0, top)
