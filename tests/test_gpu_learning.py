@@ -648,6 +648,88 @@ def test_chain_in_a_graph_and_on_another_stream(B):
     assert int(status.item()) == 0
 
 
+def test_markov_grad_calls_in_turn(B):
+    """Calls one after the other without a wait, one workspace and one set of buffers whose contents change in between."""
+    rows, V, rank = 300, 4104, 320
+    sets = [markov_case(k, rows, V, rank) for k in (31, 32, 33)]
+    want = [markov(B, *s)[:3] for s in sets]
+    g, prev, W1, W2 = (t.clone() for t in sets[0])
+    gp, d1, d2 = torch.empty(rows, rank, device="cuda"), torch.zeros(V, rank, device="cuda"), torch.empty(V, rank, device="cuda")
+    ws = B.workspace(B.dspark_workspace_size(B.DSPARK_OP_MARKOV_GRAD, 0, 0, V, rank, rows))
+    got = []
+    for k in [0, 1, 2, 0, 0, 2, 1, 1, 0] * 3:
+        for to, source in zip((g, prev, W1, W2), sets[k]):
+            to.copy_(source)
+        d1.zero_()
+        B.dspark_markov_grad(g, prev, W1, W2, gp, dW1=d1, dW2=d2, ws=ws)
+        got.append((k, gp.clone(), d1.clone(), d2.clone()))
+    torch.cuda.synchronize()
+    for k, *o in got:
+        assert all(torch.equal(a, b) for a, b in zip(o, want[k]))
+
+
+def test_two_streams_at_once(B):
+    """The chain on two streams at the same time, each with buffers and a workspace of its own."""
+    runs, outs = [], []
+    for k in range(2):
+        w, d = H.cycle_inputs("batched_sampling", seed_offset=k, R=40, V=8192, gamma=5, rank=128, w_sigma=0.2)
+        run, o, status, _ = chain(B, w, d)
+        run()
+        torch.cuda.synchronize()
+        runs.append(run)
+        outs.append((o, {n: t.clone() for n, t in o.items()}, status))
+    streams = [torch.cuda.Stream() for _ in runs]
+    for o, _, _ in outs:
+        for t in o.values():
+            t.zero_()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for run, stream in zip(runs, streams):
+            run(stream.cuda_stream)
+    torch.cuda.synchronize()
+    for o, first, status in outs:
+        assert int(status.item()) == 0 and all(torch.equal(o[n], first[n]) for n in o)
+
+
+def test_offsets_past_32_bits(B):
+    """More than 2^31 elements in the rows, and a stride that passes 2^31 bytes: the last rows are as good as the first."""
+    rows, V, rank = 17001, 129280, 64
+    x = torch.empty(rows, V, dtype=BF16, device="cuda")
+    for a in range(0, rows, 1000):
+        x[a:a + 1000].normal_(0.0, 3.0, generator=generator(a))
+    assert x.numel() > 2 ** 31
+    pick = torch.tensor([0, 1, 16611, 16612, rows - 2, rows - 1], device="cuda")  # row 16612 holds element 2^31
+    tokens = torch.randint(0, V, (rows,), generator=generator(1), device="cuda", dtype=I32)
+    lp, lse, ent, ids, val, status = logprobs(B, x, tokens, 1.0, 8)
+    assert status == 0
+    ref, tol = L.logprobs(x[pick], tokens[pick], 1.0, 8)
+    for got, r, t in zip((lp, lse, ent, val), (ref[0], ref[1], ref[2], ref[4]), tol):
+        close(got[pick], r, t, "logprobs")
+    assert torch.equal(ids[pick].long(), ref[3])
+    ref, tol = L.distill(x[pick], ids[pick], val[pick], 2.0, None, True, BF16)
+    loss, g, status = distill(B, x, ids, val, 2.0, rest=True, in_place=True)
+    assert status == 0
+    close(loss[pick], ref[0], tol[0], "loss")
+    close(g[pick], ref[1], tol[1], "grad")
+    W1, W2 = (normal(k, (V, rank), 0.05).to(BF16) for k in (1, 2))
+    prev = torch.arange(rows, device="cuda", dtype=I32)
+    gp, d1, d2, status = markov(B, g, prev, W1, W2)
+    assert status == 0
+    ref, tol = L.markov(g[pick], prev[pick], W1, W2)
+    close(gp[pick], ref[0], tol[0], "grad_prev")
+    close(d1[pick], ref[0], tol[0], "dW1")
+    part = g[:, -16:].double()
+    E = W1[:rows].double()
+    steps = (64 + rows / 1024 + 152) * 2.0 ** -22
+    close(d2[-16:], part.T @ E, steps * (part.abs().T @ E.abs()), "dW2")
+    # rows that lie far apart
+    far = torch.empty(3 * 2 ** 30, dtype=BF16, device="cuda").as_strided((3, 1001), (2 ** 30 + 5, 1), 3)
+    far.copy_(normal(2, (3, 1001), 3.0))
+    check_logprobs(B, far, i32([0, 1000, 500]), 1.0, 5)
+    ids, value = teacher_of(3, far, 5)
+    check_distill(B, far, ids, value, 1.0, BF16, rest=True, in_place=True)
+
+
 def test_same_results_every_time(B):
     x = normal(21, (40, 50001), 3.0).to(BF16)
     ids, value = teacher_of(22, x, 64)
