@@ -556,8 +556,22 @@ def dspark_prefix_attention(q, k_cache, v_cache, block_table, kv_len, cu_seqlens
     _raise("dspark_prefix_attention", st)
 
 
+def _arg(t, name, dtype, shape=None, optional=False):
+    """The address of a tensor that _check accepts."""
+    if t is None and optional:
+        return None
+    if not (t is not None and t.is_cuda and t.dtype is dtype and (shape is None or t.shape == shape) and t.is_contiguous()):
+        _check(t, name, dtype, shape)
+    return t.data_ptr()
+
+
 def _vocab_rows(t, name, dtype=None, shape=None):
     """A [rows, V] tensor whose rows may lie apart; the elements from row to row."""
+    if (t is not None and t.is_cuda and len(size := t.shape) == 2 and (shape is None or size == shape)
+            and (dtype is None or t.dtype is dtype)):
+        s0, s1 = t.stride()
+        if s1 == 1:
+            return s0 if size[0] > 1 else size[1]
     if t is None:
         raise ValueError(f"{name} is required")
     if not t.is_cuda:
@@ -576,68 +590,64 @@ def dspark_token_logprobs(logits, tokens, temperature, logprob, lse=None, entrop
                           top_logprobs=None, cu_seqlens=None, dev_status=None, stream=None):
     stride = _vocab_rows(logits, "logits")
     rows, V = logits.shape
-    R = width = 0
+    i32, f32 = torch.int32, torch.float32
+    R = width = top_k = 0
+    cu = None
     if cu_seqlens is not None:
         if tokens is None or tokens.dim() != 2:
             raise ValueError("tokens must have shape [R, width] beside cu_seqlens")
         R, width = tokens.shape
-        _check(cu_seqlens, "cu_seqlens", torch.int32, (R + 1,))
-    _check(tokens, "tokens", torch.int32, None if cu_seqlens is not None else (rows,), allow_none=True)
-    _check(logprob, "logprob", torch.float32, (rows,), allow_none=tokens is None)
-    _check(lse, "lse", torch.float32, (rows,), allow_none=True)
-    _check(entropy, "entropy", torch.float32, (rows,), allow_none=True)
+        cu = _arg(cu_seqlens, "cu_seqlens", i32, (R + 1,))
+    tok = _arg(tokens, "tokens", i32, None if cu else (rows,), True)
+    row = (rows,)
     if (top_ids is None) != (top_logprobs is None):
         raise ValueError("top_ids and top_logprobs go together")
-    top_k = 0
     if top_ids is not None:
         if top_ids.dim() != 2:
             raise ValueError("top_ids must have shape [rows, top_k]")
         top_k = top_ids.shape[1]
-        _check(top_ids, "top_ids", torch.int32, (rows, top_k))
-        _check(top_logprobs, "top_logprobs", torch.float32, (rows, top_k))
-    _check(dev_status, "dev_status", torch.int32, allow_none=True)
-    st = _L.dspark_token_logprobs(_ptr(logits), stride, _dtype_code(logits), _ptr(tokens), _ptr(cu_seqlens), R, width,
-                                  float(temperature), rows, V, top_k, _ptr(logprob), _ptr(lse), _ptr(entropy),
-                                  _ptr(top_ids), _ptr(top_logprobs), _ptr(dev_status), _stream(stream))
+    st = _L.dspark_token_logprobs(logits.data_ptr(), stride, _dtype_code(logits), tok, cu, R, width, float(temperature), rows,
+                                  V, top_k, _arg(logprob, "logprob", f32, row, tok is None), _arg(lse, "lse", f32, row, True),
+                                  _arg(entropy, "entropy", f32, row, True),
+                                  _arg(top_ids, "top_ids", i32, (rows, top_k), True),
+                                  _arg(top_logprobs, "top_logprobs", f32, (rows, top_k), True),
+                                  _arg(dev_status, "dev_status", i32, None, True), _stream(stream))
     _raise("dspark_token_logprobs", st)
 
 
 def dspark_distill_loss(student, teacher_ids, teacher_logprobs, temperature, loss, grad=None, row_weight=None,
                         rest=False, dev_status=None, stream=None):
     stride = _vocab_rows(student, "student")
-    rows, V = student.shape
+    rows, V = shape = student.shape
+    i32, f32 = torch.int32, torch.float32
     if teacher_ids is None or teacher_ids.dim() != 2:
         raise ValueError("teacher_ids must have shape [rows, top_k]")
     top_k = teacher_ids.shape[1]
-    _check(teacher_ids, "teacher_ids", torch.int32, (rows, top_k))
-    _check(teacher_logprobs, "teacher_logprobs", torch.float32, (rows, top_k))
-    _check(row_weight, "row_weight", torch.float32, (rows,), allow_none=True)
-    _check(loss, "loss", torch.float32, (rows,))
-    _check(dev_status, "dev_status", torch.int32, allow_none=True)
-    grad_stride = 0 if grad is None else _vocab_rows(grad, "grad", shape=student.shape)
-    st = _L.dspark_distill_loss(_ptr(student), stride, _dtype_code(student), _ptr(teacher_ids), _ptr(teacher_logprobs),
-                                top_k, _ptr(row_weight), float(temperature), rows, V, _ptr(loss), _ptr(grad),
-                                grad_stride, 0 if grad is None else _dtype_code(grad),
-                                DSPARK_DISTILL_REST if rest else 0, _ptr(dev_status), _stream(stream))
+    listed = (rows, top_k)
+    grad_stride = grad_code = 0
+    if grad is not None:
+        grad_stride, grad_code = _vocab_rows(grad, "grad", None, shape), _dtype_code(grad)
+    st = _L.dspark_distill_loss(student.data_ptr(), stride, _dtype_code(student), _arg(teacher_ids, "teacher_ids", i32, listed),
+                                _arg(teacher_logprobs, "teacher_logprobs", f32, listed), top_k,
+                                _arg(row_weight, "row_weight", f32, (rows,), True), float(temperature), rows, V,
+                                _arg(loss, "loss", f32, (rows,)), _ptr(grad), grad_stride, grad_code,
+                                DSPARK_DISTILL_REST if rest else 0, _arg(dev_status, "dev_status", i32, None, True),
+                                _stream(stream))
     _raise("dspark_distill_loss", st)
 
 
 def dspark_markov_grad(grad, prev, W1, W2, grad_prev, dW1=None, dW2=None, accumulate=False, ws=None, dev_status=None,
                        stream=None):
-    stride = _vocab_rows(grad, "grad", torch.bfloat16)
+    bf16, f32 = torch.bfloat16, torch.float32
+    stride = _vocab_rows(grad, "grad", bf16)
     rows, V = grad.shape
     rank = W1.shape[1]
-    _check(prev, "prev", torch.int32, (rows,))
-    _check(W1, "W1", torch.bfloat16, (V, rank))
-    _check(W2, "W2", torch.bfloat16, (V, rank))
-    _check(grad_prev, "grad_prev", torch.float32, (rows, rank))
-    _check(dW1, "dW1", torch.float32, (V, rank), allow_none=True)
-    _check(dW2, "dW2", torch.float32, (V, rank), allow_none=True)
-    _check(ws, "ws", torch.uint8)
-    _check(dev_status, "dev_status", torch.int32, allow_none=True)
-    st = _L.dspark_markov_grad(_ptr(grad), stride, _ptr(prev), _ptr(W1), _ptr(W2), rows, V, rank, _ptr(grad_prev),
-                               _ptr(dW1), _ptr(dW2), DSPARK_GRAD_ACCUMULATE if accumulate else 0, _ptr(ws), ws.numel(),
-                               _ptr(dev_status), _stream(stream))
+    factor = (V, rank)
+    st = _L.dspark_markov_grad(grad.data_ptr(), stride, _arg(prev, "prev", torch.int32, (rows,)), _arg(W1, "W1", bf16, factor),
+                               _arg(W2, "W2", bf16, factor), rows, V, rank, _arg(grad_prev, "grad_prev", f32, (rows, rank)),
+                               _arg(dW1, "dW1", f32, factor, True), _arg(dW2, "dW2", f32, factor, True),
+                               DSPARK_GRAD_ACCUMULATE if accumulate else 0, _arg(ws, "ws", torch.uint8), ws.numel(),
+                               _arg(dev_status, "dev_status", torch.int32, None, True), _stream(stream))
     _raise("dspark_markov_grad", st)
 
 

@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return x;
     };
     // rows that give nothing and hold a NaN or an infinity: cleared once they have landed.  (Clearing every row without a
-    // token instead made markov_step's dW2 309 us where it is 264.)
+    // token instead took dW2 of 2560 rows, 129280 tokens and rank 512 from 264 to 309 us.)
     auto dropped = [&](int k) { return kSumRows && (sh.has_drop[k >> 5] >> (k & 31) & 1u); };
     uint32_t landed = 0;  // parities
     auto clear = [&](int k, int s) {
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // 32 columns at a time through shared memory (16-byte pieces in the order the store's swizzle
             // undoes), then to memory by one store, which leaves out what lies past the result's rows.  Stores
-            // from registers, a row to a thread, took 210 us of markov_batch's second product where these take 136.
+            // from registers, a row to a thread: dW2 of 896 rows, 151936 tokens and rank 512 took 210 us where it took 136 with these.
             const int row = x.m0 + quad * 32;
             if (go && row < p.M) {
 #pragma unroll
