@@ -520,7 +520,7 @@ cudaError_t launch_distill(DistillParams p, cudaStream_t stream) {
     const int threads = small ? kSmall : kLarge;
     // Shared memory of a CTA, so that three large ones fit on an SM (a row's last batch is read again then, of 151936 fp32
     // over eight CTAs the fifth).  Three with all but that, two with all of it: 170 and 174 us for 896 rows of 151936 fp32.
-    const size_t kShare = 68 * 1024;
+    constexpr size_t kShare = 68 * 1024;
     int ctas = 1;
     auto batches_of = [&](int c) { return (int)(((pieces + c - 1) / c + kUnroll * threads - 1) / (kUnroll * threads)); };
     auto bits_of = [&](int c) { return (int)(((pieces + c - 1) / c * vec + 31) / 32 + 2); };
@@ -535,7 +535,9 @@ cudaError_t launch_distill(DistillParams p, cudaStream_t stream) {
     const size_t smem = smem_of(ctas, p.staged);
     const void* fn = p.dtype == DSPARK_F32 ? kernel_of<float>(p.grad != nullptr, p.grad_dtype, small)
                                            : kernel_of<uint16_t>(p.grad != nullptr, p.grad_dtype, small);
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // (the same for every call: two host threads may call at once)
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kShare);
+    static_assert(DSPARK_ROWS_MAX_V / 8 / 8 + 64 <= kShare, "the longest row's bits");
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.blockDim = dim3(threads + 32);

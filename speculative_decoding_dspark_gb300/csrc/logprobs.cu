@@ -31,6 +31,7 @@ constexpr int kBatch = 32;       // elements of a batch (a thread's, of as many 
 constexpr int kCandidates = 1024;
 constexpr int kHits = 1024;
 constexpr int kSms = 152;
+constexpr int kMaxShared = 64 * 1024;
 
 __device__ __forceinline__ uint32_t order_of(float x) {
     const uint32_t b = __float_as_uint(x + 0.0f);  // (-0 is 0)
@@ -435,7 +436,9 @@ cudaError_t launch_logprobs(const LogprobsParams& p, cudaStream_t stream) {
     const size_t smem = smem_of(ctas);
     const void* fn = p.dtype == DSPARK_F32 ? kernel_of<float>(p.entropy, p.top_k > 0)
                                            : kernel_of<uint16_t>(p.entropy, p.top_k > 0);
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // (the same for every call: two host threads may call at once)
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
+    static_assert(DSPARK_ROWS_MAX_V / 8 / (kBatch * kThreads) * kThreads * sizeof(float) <= kMaxShared, "the longest row's maxima");
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(places * ctas));

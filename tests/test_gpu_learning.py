@@ -772,3 +772,38 @@ def test_binding_refuses(B):
         B.dspark_markov_grad(x, tok, W, W, torch.empty(4, 64, device="cuda"), ws=B.workspace(1 << 20))
     with pytest.raises(B.DSparkError):
         B.dspark_markov_grad(x.to(BF16), tok, W, W, torch.empty(4, 64, device="cuda"), ws=B.workspace(256))
+
+
+def test_two_host_threads(B):
+    """Two host threads that call at once, with rows of different lengths: neither's call disturbs the other's."""
+    import threading
+    cases, errors = [], []
+    for V, top in ((151936, 128), (700, 3)):
+        x = normal(V, (5, V), 3.0)
+        ids, value = teacher_of(V, x, top)
+        want = logprobs(B, x, None, 1.0, top)[:5] + distill(B, x, ids, value, 1.0, F32, rest=True)[:2]
+        cases.append((x, ids, value, top, want))
+
+    def work(x, ids, value, top, want):
+        try:
+            stream = torch.cuda.Stream()
+            lp, lse, ent = (torch.empty(5, device="cuda") for _ in range(3))
+            oi, ov = torch.empty(5, top, dtype=I32, device="cuda"), torch.empty(5, top, device="cuda")
+            loss, g = torch.empty(5, device="cuda"), torch.empty_like(x)
+            stream.wait_stream(torch.cuda.default_stream())
+            for _ in range(200):
+                B.dspark_token_logprobs(x, None, 1.0, lp, lse, ent, oi, ov, stream=stream)
+                B.dspark_distill_loss(x, ids, value, 1.0, loss, grad=g, rest=True, stream=stream)
+            stream.synchronize()
+            for a, b in zip((lp, lse, ent, oi, ov, loss, g), want):
+                if not torch.equal(a, b):
+                    errors.append("results differ")
+        except Exception as e:  # noqa: BLE001 (shown by the test's own thread)
+            errors.append(repr(e))
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=c) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
