@@ -693,7 +693,7 @@ int dspark_prefix_attention(const void* q, const void* k_cache, const void* v_ca
  *                cu_seqlens given ([R + 1] int32, from 0, non-decreasing, up to rows): [R, width]
  *                int32; row cu_seqlens[r] + j has token tokens[r][j] (j >= width: none), rows
  *                from cu_seqlens[R] on are not touched
- *   logprob [rows] fp32 out (NULL iff tokens is NULL; 0 where no token was asked for)
+ *   logprob [rows] fp32 out (may be NULL where tokens is; 0 where no token was asked for)
  *   lse, entropy [rows] fp32 out or NULL
  *   top_ids [rows, top_k] int32, top_logprobs [rows, top_k] fp32 out (both NULL iff top_k == 0)
  * A row whose token is negative is not read: its logprob, lse and entropy are 0, its list is

@@ -331,6 +331,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsParams
         };
         if (x_edge >= bound && x_edge > -INFINITY) offer(x_edge, v_edge);
         if (t.m >= bound)
+#pragma unroll 4
             for (int b = 0; b < batch; ++b) {
                 const float top = batch_max[b * kThreads + tid];
                 if (top >= bound && top > -INFINITY) {
@@ -354,9 +355,9 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsParams
                     reach |= (x.x >= bound ? 1u << e : 0u) | (x.y >= bound ? 2u << e : 0u);
                 }
                 for (; reach; reach &= reach - 1) {
-                    const int e = __ffs(reach) - 1, v = view.head + i * kVec + e;
-                    const float x = view.at(v);
-                    if (x > -INFINITY) offer(x, v);
+                    const int e = __ffs(reach) - 1;
+                    const float x = Elem<T>::at(w, e);
+                    if (x > -INFINITY) offer(x, view.head + i * kVec + e);
                 }
             }
         }

@@ -120,6 +120,9 @@ template <> struct Elem<float> {
     static __device__ __forceinline__ Two pair(const uint4& w, int i) {
         return i == 0 ? two(__uint_as_float(w.x), __uint_as_float(w.y)) : two(__uint_as_float(w.z), __uint_as_float(w.w));
     }
+    static __device__ __forceinline__ float at(const uint4& w, int e) {
+        return __uint_as_float(e == 0 ? w.x : e == 1 ? w.y : e == 2 ? w.z : w.w);
+    }
     static __device__ __forceinline__ uint4 without(const uint4& w, uint32_t mask) {  // -inf where mask has a bit
         return make_uint4(mask & 1 ? kMinusInf : w.x, mask & 2 ? kMinusInf : w.y, mask & 4 ? kMinusInf : w.z,
                           mask & 8 ? kMinusInf : w.w);
@@ -142,6 +145,10 @@ template <> struct Elem<uint16_t> {
     static __device__ __forceinline__ Two pair(const uint4& w, int i) {
         const uint32_t u = i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
         return two(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+    }
+    static __device__ __forceinline__ float at(const uint4& w, int e) {
+        const uint32_t u = e < 2 ? w.x : e < 4 ? w.y : e < 6 ? w.z : w.w;
+        return __uint_as_float(e & 1 ? u & 0xFFFF0000u : u << 16);
     }
     static __device__ __forceinline__ uint32_t without(uint32_t u, uint32_t mask) {
         const uint32_t off = (mask & 1 ? 0xFFFFu : 0u) | (mask & 2 ? 0xFFFF0000u : 0u);
