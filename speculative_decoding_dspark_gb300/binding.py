@@ -162,12 +162,14 @@ def _stream(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+_DTYPE_CODES = {torch.float32: DSPARK_F32, torch.bfloat16: DSPARK_BF16}
+
+
 def _dtype_code(t):
-    if t.dtype == torch.float32:
-        return DSPARK_F32
-    if t.dtype == torch.bfloat16:
-        return DSPARK_BF16
-    raise TypeError(f"expected float32 or bfloat16, got {t.dtype}")
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"expected float32 or bfloat16, got {t.dtype}")
+    return code
 
 
 def _check(t, name, dtype=None, shape=None, allow_none=False, allow_pinned=False):
@@ -566,12 +568,12 @@ def _arg(t, name, dtype, shape=None, optional=False):
 
 
 def _vocab_rows(t, name, dtype=None, shape=None):
-    """A [rows, V] tensor whose rows may lie apart; the elements from row to row."""
+    """A [rows, V] tensor whose rows may lie apart: rows, V, and the elements from row to row."""
     if (t is not None and t.is_cuda and len(size := t.shape) == 2 and (shape is None or size == shape)
             and (dtype is None or t.dtype is dtype)):
-        s0, s1 = t.stride()
+        (rows, V), (s0, s1) = size, t.stride()
         if s1 == 1:
-            return s0 if size[0] > 1 else size[1]
+            return rows, V, s0 if rows > 1 else V
     if t is None:
         raise ValueError(f"{name} is required")
     if not t.is_cuda:
@@ -583,13 +585,12 @@ def _vocab_rows(t, name, dtype=None, shape=None):
     rows, V = t.shape
     if V > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return t.stride(0) if rows > 1 else V
+    return rows, V, t.stride(0) if rows > 1 else V
 
 
 def dspark_token_logprobs(logits, tokens, temperature, logprob, lse=None, entropy=None, top_ids=None,
                           top_logprobs=None, cu_seqlens=None, dev_status=None, stream=None):
-    stride = _vocab_rows(logits, "logits")
-    rows, V = logits.shape
+    rows, V, stride = _vocab_rows(logits, "logits")
     i32, f32 = torch.int32, torch.float32
     R = width = top_k = 0
     cu = None
@@ -602,45 +603,46 @@ def dspark_token_logprobs(logits, tokens, temperature, logprob, lse=None, entrop
     row = (rows,)
     if (top_ids is None) != (top_logprobs is None):
         raise ValueError("top_ids and top_logprobs go together")
+    listed = None
     if top_ids is not None:
-        if top_ids.dim() != 2:
+        listed = top_ids.shape
+        if len(listed) != 2 or listed[0] != rows:
             raise ValueError("top_ids must have shape [rows, top_k]")
-        top_k = top_ids.shape[1]
+        top_k = listed[1]
     st = _L.dspark_token_logprobs(logits.data_ptr(), stride, _dtype_code(logits), tok, cu, R, width, float(temperature), rows,
                                   V, top_k, _arg(logprob, "logprob", f32, row, tok is None), _arg(lse, "lse", f32, row, True),
                                   _arg(entropy, "entropy", f32, row, True),
-                                  _arg(top_ids, "top_ids", i32, (rows, top_k), True),
-                                  _arg(top_logprobs, "top_logprobs", f32, (rows, top_k), True),
+                                  _arg(top_ids, "top_ids", i32, None, True),
+                                  _arg(top_logprobs, "top_logprobs", f32, listed, True),
                                   _arg(dev_status, "dev_status", i32, None, True), _stream(stream))
-    _raise("dspark_token_logprobs", st)
+    if st:
+        _raise("dspark_token_logprobs", st)
 
 
 def dspark_distill_loss(student, teacher_ids, teacher_logprobs, temperature, loss, grad=None, row_weight=None,
                         rest=False, dev_status=None, stream=None):
-    stride = _vocab_rows(student, "student")
-    rows, V = shape = student.shape
+    rows, V, stride = _vocab_rows(student, "student")
     i32, f32 = torch.int32, torch.float32
-    if teacher_ids is None or teacher_ids.dim() != 2:
+    if teacher_ids is None or len(listed := teacher_ids.shape) != 2 or listed[0] != rows:
         raise ValueError("teacher_ids must have shape [rows, top_k]")
-    top_k = teacher_ids.shape[1]
-    listed = (rows, top_k)
-    grad_stride = grad_code = 0
+    grad_ptr, grad_stride, grad_code = None, 0, 0
     if grad is not None:
-        grad_stride, grad_code = _vocab_rows(grad, "grad", None, shape), _dtype_code(grad)
-    st = _L.dspark_distill_loss(student.data_ptr(), stride, _dtype_code(student), _arg(teacher_ids, "teacher_ids", i32, listed),
-                                _arg(teacher_logprobs, "teacher_logprobs", f32, listed), top_k,
+        _, _, grad_stride = _vocab_rows(grad, "grad", None, (rows, V))
+        grad_ptr, grad_code = grad.data_ptr(), _dtype_code(grad)
+    st = _L.dspark_distill_loss(student.data_ptr(), stride, _dtype_code(student), _arg(teacher_ids, "teacher_ids", i32),
+                                _arg(teacher_logprobs, "teacher_logprobs", f32, listed), listed[1],
                                 _arg(row_weight, "row_weight", f32, (rows,), True), float(temperature), rows, V,
-                                _arg(loss, "loss", f32, (rows,)), _ptr(grad), grad_stride, grad_code,
+                                _arg(loss, "loss", f32, (rows,)), grad_ptr, grad_stride, grad_code,
                                 DSPARK_DISTILL_REST if rest else 0, _arg(dev_status, "dev_status", i32, None, True),
                                 _stream(stream))
-    _raise("dspark_distill_loss", st)
+    if st:
+        _raise("dspark_distill_loss", st)
 
 
 def dspark_markov_grad(grad, prev, W1, W2, grad_prev, dW1=None, dW2=None, accumulate=False, ws=None, dev_status=None,
                        stream=None):
     bf16, f32 = torch.bfloat16, torch.float32
-    stride = _vocab_rows(grad, "grad", bf16)
-    rows, V = grad.shape
+    rows, V, stride = _vocab_rows(grad, "grad", bf16)
     rank = W1.shape[1]
     factor = (V, rank)
     st = _L.dspark_markov_grad(grad.data_ptr(), stride, _arg(prev, "prev", torch.int32, (rows,)), _arg(W1, "W1", bf16, factor),
@@ -648,7 +650,8 @@ def dspark_markov_grad(grad, prev, W1, W2, grad_prev, dW1=None, dW2=None, accumu
                                _arg(dW1, "dW1", f32, factor, True), _arg(dW2, "dW2", f32, factor, True),
                                DSPARK_GRAD_ACCUMULATE if accumulate else 0, _arg(ws, "ws", torch.uint8), ws.numel(),
                                _arg(dev_status, "dev_status", torch.int32, None, True), _stream(stream))
-    _raise("dspark_markov_grad", st)
+    if st:
+        _raise("dspark_markov_grad", st)
 
 
 def dspark_philox4x32_10(ctr, keys, out, stream=None):

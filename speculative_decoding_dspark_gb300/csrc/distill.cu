@@ -535,8 +535,9 @@ cudaError_t launch_distill(DistillParams p, cudaStream_t stream) {
     const size_t smem = smem_of(ctas, p.staged);
     const void* fn = p.dtype == DSPARK_F32 ? kernel_of<float>(p.grad != nullptr, p.grad_dtype, small)
                                            : kernel_of<uint16_t>(p.grad != nullptr, p.grad_dtype, small);
-    // (the same for every call: two host threads may call at once)
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kShare);
+    // (the same limit in every call that sets it: two host threads may call at once)
+    cudaError_t e = cudaSuccess;
+    if (smem > kSharedAnyway) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kShare);
     static_assert(DSPARK_ROWS_MAX_V / 8 / 8 + 64 <= kShare, "the longest row's bits");
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
@@ -549,10 +550,10 @@ cudaError_t launch_distill(DistillParams p, cudaStream_t stream) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    // as many clusters as there is room for at a time: they walk down the rows
+    // As many clusters as there is room for at a time: they walk down the rows.  Few rows need no asking (0.2 us).
     cfg.gridDim = dim3((unsigned)ctas);
-    int room = 0;
-    if ((e = cudaOccupancyMaxActiveClusters(&room, fn, &cfg)) != cudaSuccess) return e;
+    int room = p.rows;
+    if (p.rows > 8 && (e = cudaOccupancyMaxActiveClusters(&room, fn, &cfg)) != cudaSuccess) return e;
     cfg.gridDim = dim3((unsigned)(std::min(p.rows, std::max(1, room)) * ctas));
     void* args[] = {&p};
     return cudaLaunchKernelExC(&cfg, fn, args);

