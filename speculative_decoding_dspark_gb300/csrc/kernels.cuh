@@ -300,6 +300,9 @@ struct MarkovGradParams {
 
 size_t markov_grad_workspace(int rows, int V, int rank);
 cudaError_t launch_markov_grad(const MarkovGradParams& p, cudaStream_t stream);
+constexpr int kMarkovFewRows = 32;  // (two operands of rows)
+size_t markov_few_workspace(int rows, int rank);
+cudaError_t launch_markov_few(const MarkovGradParams& p, cudaStream_t stream);
 
 cudaError_t launch_commit(const int32_t* n_acc, const int32_t* l, int R, int gamma,
                           int32_t* commit_len, int32_t* cu_commit, int32_t* discard,

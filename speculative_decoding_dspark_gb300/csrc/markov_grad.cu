@@ -586,6 +586,7 @@ Layout layout_of(int rows, int V, int rank) {
     L.parts = parts_of(rows, V, rank);
     L.part = off; off += align256((size_t)L.parts * rows * rank * 4);
     L.total = std::max<size_t>(off, 256);
+    if (rows <= kMarkovFewRows) L.total = std::max(L.total, markov_few_workspace(rows, rank));
     return L;
 }
 
@@ -664,6 +665,8 @@ cudaError_t launch_markov_grad(const MarkovGradParams& p, cudaStream_t stream) {
         if (!p.dW2 || p.accumulate) return cudaSuccess;
         return cudaMemsetAsync(p.dW2, 0, (size_t)p.V * p.rank * sizeof(float), stream);
     }
+    // (what a test injects is in the products' waits)
+    if (p.rows <= kMarkovFewRows && !p.inject) return launch_markov_few(p, stream);
     int dev = 0, n_sm = 0;
     cudaError_t e;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;

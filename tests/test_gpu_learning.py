@@ -572,6 +572,114 @@ def test_markov_grad_no_tokens(B):
     assert status == 0 and (gp == 0).all() and (d1 == 3).all() and (d2 == 0).all()
 
 
+def markov_holds(B, g, prev, W1, W2, status=0, accumulate=False, start=(0.0, 0.0), seen=None):
+    """The three outputs against their definitions; `seen`: the gradient without what must not be seen."""
+    V, rank = W1.shape
+    gp, d1, d2, got = markov(B, g, prev, W1, W2, accumulate, start=start)
+    assert got == status
+    base = [torch.full((V, rank), x if accumulate else 0.0, device="cuda") for x in start]
+    ref, tol = L.markov(g if seen is None else seen, prev, W1, W2, *base)
+    there = torch.zeros(V, dtype=torch.bool, device="cuda")
+    there[prev[(prev >= 0) & (prev < V)].long()] = True
+    close(gp, ref[0], tol[0], "grad_prev")
+    close(d1[there], ref[1][there], tol[1][there], "dW1")
+    assert bool((d1[~there] == start[0]).all())
+    close(d2, ref[2], tol[2], "dW2")
+    return gp, d1, d2
+
+
+@pytest.mark.parametrize("rows", [1, 7, 8, 9, 16, 17, 32, 33])
+@pytest.mark.parametrize("V,rank,gap", [
+    (8, 64, 0), (128, 192, 8), (2424, 320, 0), (9736, 448, 24), (40000, 256, 0), (80008, 512, 0),
+])
+def test_markov_grad_few_rows(B, rows, V, rank, gap):
+    """A block's rows: fewer elements than CTAs, pieces of them that end inside a stretch, ranks that leave threads over."""
+    g, prev, W1, W2 = markov_case(40 + rows, rows, V, rank, gap)
+    markov_holds(B, g, prev, W1, W2, start=(7.0, 9.0))
+    markov_holds(B, g, prev, W1, W2, accumulate=True, start=(0.5, -2.0))
+
+
+@pytest.mark.parametrize("rows", [4, 13, 29])
+def test_markov_grad_few_rows_tokens(B, rows):
+    """Rows of one token, rows without one, and rows whose token is none, with anything in them and behind them."""
+    V, rank = 5000, 128
+    g, prev, W1, W2 = markov_case(60, rows, V, rank)
+    prev.fill_(V - 1)
+    markov_holds(B, g, prev, W1, W2)
+    prev.copy_(torch.arange(rows, device="cuda") % 3)
+    markov_holds(B, g, prev, W1, W2, accumulate=True, start=(1.0, 2.0))
+    prev[1], prev[3], prev[rows - 2] = -1, V, -2 ** 31
+    seen = g.clone()
+    seen[[1, 3, rows - 2]] = 0
+    g[1, ::7], g[3], g[rows - 2, V - 1] = NAN, INF, -INF
+    markov_holds(B, g, prev, W1, W2, status=DEVICE_INPUT, seen=seen)
+    prev.fill_(-1)
+    gp, d1, d2, status = markov(B, g, prev, W1, W2, start=(3.0, 4.0))
+    assert status == 0 and (gp == 0).all() and (d1 == 3).all() and (d2 == 0).all()
+
+
+def test_markov_grad_few_rows_infinities(B):
+    """An infinity in the factors or in a row reaches what it takes part in, and nothing else."""
+    rows, V, rank = 5, 3000, 64
+    g, prev, W1, W2 = markov_case(61, rows, V, rank)
+    g = torch.where(g == 0, torch.ones_like(g), g)
+    prev.copy_(i32([4, -1, 9, 9, 2000]))
+    W2[77, 3] = INF
+    gp, d1, d2, status = markov(B, g, prev, W1, W2)
+    assert status == 0 and (gp[1] == 0).all() and torch.isfinite(d2).all()
+    odd = ~torch.isfinite(gp)
+    assert odd[[0, 2, 3, 4], 3].all() and int(odd.sum()) == 4
+    odd = ~torch.isfinite(d1)
+    assert odd[[4, 9, 2000], 3].all() and int(odd.sum()) == 3
+    W2[77, 3] = 0
+    g[2, 1234] = NAN
+    gp, d1, d2, status = markov(B, g, prev, W1, W2)
+    odd = ~torch.isfinite(gp)
+    assert status == 0 and odd[2].all() and int(odd.sum()) == rank
+    odd = ~torch.isfinite(d1)
+    assert odd[9].all() and int(odd.sum()) == rank
+    odd = ~torch.isfinite(d2)
+    assert odd[1234].all() and int(odd.sum()) == rank
+
+
+@pytest.mark.parametrize("rows", [9, 20])
+@pytest.mark.parametrize("want", [(False, False), (True, False), (False, True)])
+def test_markov_grad_few_rows_in_part(B, want, rows):
+    g, prev, W1, W2 = markov_case(62, rows, 2000, 128)
+    all_of = markov(B, g, prev, W1, W2)
+    some = markov(B, g, prev, W1, W2, want=want)
+    for a, b in zip(all_of[:3], some[:3]):
+        assert b is None or torch.equal(a, b)
+
+
+def test_markov_grad_few_rows_replayed(B):
+    """Calls of a few rows and of many on one workspace, captured and replayed on new rows: the bits of calls by themselves."""
+    V, rank = 4104, 320
+    sets = [markov_case(70 + k, rows, V, rank) for k, rows in enumerate((7, 200, 16, 1, 31, 7))]
+    want = [markov(B, *s)[:3] for s in sets]
+    ws = B.workspace(max(B.dspark_workspace_size(B.DSPARK_OP_MARKOV_GRAD, 0, 0, V, rank, s[0].shape[0]) for s in sets))
+    at = [[torch.zeros_like(x) for x in s] for s in sets]
+    got = [[torch.full_like(x, 9.0) for x in w] for w in want]
+    for o in got:
+        o[1].zero_()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        for (g, prev, W1, W2), (gp, d1, d2) in zip(at, got):
+            B.dspark_markov_grad(g, prev, W1, W2, gp, dW1=d1, dW2=d2, ws=ws)
+    for s, t in zip(sets, at):
+        for x, y in zip(s, t):
+            y.copy_(x)
+    for _ in range(3):
+        for o in got:
+            o[1].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for o, w in zip(got, want):
+            assert all(torch.equal(a, b) for a, b in zip(o, w))
+
+
 # ------------------------------------------------------------------------------------------- all of them
 def chain(B, w, d, T=1.0, top=16):
     """A cycle's rows through the three of them: what the target says, what the drafter makes of it, what its head learns."""
