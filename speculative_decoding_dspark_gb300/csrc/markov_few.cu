@@ -110,7 +110,8 @@ __global__ void __launch_bounds__(kThreads, kRows == 16 ? 2 : 1) few_kernel(cons
         if (a >= p.V && blockIdx.x == 0) report(p.dev_status, DSPARK_ERR_DEVICE_INPUT);
     }
     __syncthreads();
-    // E's columns 2 m and 2 m + 1 (of eight) are interleaved by twos, so that a thread has four columns of dW2 side by side
+    // Of 16 columns the first product by E takes the even ones, the second the odd ones: a load brings both products', and a
+    // thread then has four columns of dW2 side by side.
     const int t = lane & 3, o = lane >> 2;
     uint32_t e[kTiles][8][2];
 #pragma unroll
@@ -118,13 +119,13 @@ __global__ void __launch_bounds__(kThreads, kRows == 16 ? 2 : 1) few_kernel(cons
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int a0 = token[16 * z + 8 * h + 2 * t], a1 = token[16 * z + 8 * h + 2 * t + 1];
-            const int col = slice * 64 + 4 * (o >> 1) + (o & 1);
-            const uint16_t *w0 = p.W1 + (int64_t)max(a0, 0) * p.rank + col, *w1 = p.W1 + (int64_t)max(a1, 0) * p.rank + col;
+            const uint32_t* w0 = reinterpret_cast<const uint32_t*>(p.W1 + (int64_t)max(a0, 0) * p.rank + slice * 64) + o;
+            const uint32_t* w1 = reinterpret_cast<const uint32_t*>(p.W1 + (int64_t)max(a1, 0) * p.rank + slice * 64) + o;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t lo = a0 >= 0 && active ? __ldg(w0 + 16 * (j >> 1) + 2 * (j & 1)) : 0;
-                const uint32_t hi = a1 >= 0 && active ? __ldg(w1 + 16 * (j >> 1) + 2 * (j & 1)) : 0;
-                e[z][j][h] = lo | hi << 16;
+            for (int m = 0; m < 4; ++m) {
+                const uint32_t x0 = a0 >= 0 && active ? __ldg(w0 + 8 * m) : 0, x1 = a1 >= 0 && active ? __ldg(w1 + 8 * m) : 0;
+                e[z][2 * m][h] = __byte_perm(x0, x1, 0x5410);
+                e[z][2 * m + 1][h] = __byte_perm(x0, x1, 0x7632);
             }
         }
     float acc[kTiles][8][4];
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, kRows == 16 ? 2 : 1) few_kernel(cons
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const int v = base + v0 + o + 8 * h;
-                            const float4 y = make_float4(d[0][2 * h], d[0][2 * h + 1], d[1][2 * h], d[1][2 * h + 1]);
+                            const float4 y = make_float4(d[0][2 * h], d[1][2 * h], d[0][2 * h + 1], d[1][2 * h + 1]);
                             float4* to = reinterpret_cast<float4*>(dW2 + v * p.rank + 16 * m);
                             if (v < n) {
                                 if (p.accumulate)

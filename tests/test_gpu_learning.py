@@ -591,6 +591,7 @@ def markov_holds(B, g, prev, W1, W2, status=0, accumulate=False, start=(0.0, 0.0
 @pytest.mark.parametrize("rows", [1, 7, 8, 9, 16, 17, 32, 33])
 @pytest.mark.parametrize("V,rank,gap", [
     (8, 64, 0), (128, 192, 8), (2424, 320, 0), (9736, 448, 24), (40000, 256, 0), (80008, 512, 0),
+    (160008, 64, 0), (100000, 128, 0), (120008, 192, 0), (90008, 320, 0), (70000, 384, 0), (60008, 448, 0),
 ])
 def test_markov_grad_few_rows(B, rows, V, rank, gap):
     """A block's rows: fewer elements than CTAs, pieces of them that end inside a stretch, ranks that leave threads over."""
