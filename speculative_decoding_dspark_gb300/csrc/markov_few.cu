@@ -11,9 +11,11 @@
 // it as it is.)  The CTAs of a cluster join their sums through distributed shared memory, few_join_kernel adds
 // those of the clusters in order, for dW1 too.
 //
-// Against the two products of markov_grad.cu: 13.9 and 22.9 us for 7 rows of 32000 at rank 256, 19.6 and 24.5 for 32 of these,
-// 84.8 and 97.5 for 7 rows of 151936 at rank 512 (70 us of bytes), 91.1 and 98.4 for 32.  On the CUDA cores, two rows to a
-// multiply-add, 7 rows took 17.5 and 90.7, 16 rows 26 and 145: there the multiply-adds bound it.
+// Against the two products of markov_grad.cu: 12.9 and 22.9 us for 7 rows of 32000 at rank 256 (7.4 us of bytes), 18.9 and
+// 24.5 for 32 of these, 83.9 and 97.5 for 7 rows of 151936 at rank 512 (70 us of bytes), 7.3 and 12.6 for 7 rows of 8000
+// at rank 64.  On the CUDA cores, two rows to a multiply-add, the first took 17.5 us and 16 rows of 151936
+// at rank 512 145: there the multiply-adds bound it.  A cluster of two CTAs, one by itself, four: 13.4, 15.7 and
+// 14.3 us for the first; two CTAs of 256 threads on an SM, one of 512: 13.9 and 14.7.
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -72,7 +74,6 @@ __global__ void __launch_bounds__(kThreads, kRows == 16 ? 2 : 1) few_kernel(cons
     const int slice = warp % slices, group = warp / slices;   // the warp's columns, and which of the elements
     const bool active = group < groups;
     const int begin = min((int)blockIdx.x * per, p.V), n = min(per, p.V - begin);  // the CTA's elements
-    launch_dependents();
     wait_prior_grid();
 
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(memory) + warp * kStages * kStage;
@@ -219,6 +220,7 @@ __global__ void __launch_bounds__(kThreads, kRows == 16 ? 2 : 1) few_kernel(cons
         }
         reinterpret_cast<float4*>(part)[(int64_t)cluster * p.rows * quads + at] = s;
     }
+    launch_dependents();  // (earlier, and few_join_kernel's CTAs take room on the SMs: 16.9 instead of 15.6 us for 16 rows)
     cluster_sync();  // (no CTA's memory goes while another reads it)
 }
 
@@ -235,12 +237,16 @@ __global__ void __launch_bounds__(kJoinThreads) few_join_kernel(const MarkovGrad
     // (threads 0 to 63: a column each)
     auto sum_of = [&](int m) {
         float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        constexpr int kGroups = kJoinThreads / 16;
+        constexpr int kGroups = kJoinThreads / 16, kEach = (clusters<16>() + kGroups - 1) / kGroups;
+        float4 x[kEach];
 #pragma unroll
-        for (int q = 0; q < (clusters<16>() + kGroups - 1) / kGroups; ++q) {
+        for (int q = 0; q < kEach; ++q) {
             const int z = group + q * kGroups;
-            if (z < parts) s = plus(s, __ldcg(reinterpret_cast<const float4*>(part + ((int64_t)z * p.rows + m) * p.rank + col) + i));
+            x[q] = z < parts ? __ldcg(reinterpret_cast<const float4*>(part + ((int64_t)z * p.rows + m) * p.rank + col) + i)
+                             : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
+#pragma unroll
+        for (int q = 0; q < kEach; ++q) s = plus(s, x[q]);
         const float4 y = make_float4(__shfl_down_sync(~0u, s.x, 16), __shfl_down_sync(~0u, s.y, 16),
                                      __shfl_down_sync(~0u, s.z, 16), __shfl_down_sync(~0u, s.w, 16));
         if ((tid & 31) < 16) sums[tid / 32][i] = plus(s, y);
@@ -270,7 +276,8 @@ int up(int a, int b) { return (a + b - 1) / b; }
 
 template <int kRows>
 cudaError_t launch_few(const MarkovGradParams& p, cudaStream_t stream) {
-    const int per = up(up(p.V, 16), clusters<kRows>() * kCluster) * 16, parts = up(up(p.V, per), kCluster);
+    const int groups = kWarps / (p.rank / 64);  // (a stage for each warp at least)
+    const int per = std::max(up(up(p.V, 16), clusters<kRows>() * kCluster), groups) * 16, parts = up(up(p.V, per), kCluster);
     float* part = static_cast<float*>(p.ws);
     const auto kernel = few_kernel<kRows>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared_bytes<kRows>());
