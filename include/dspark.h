@@ -395,7 +395,7 @@ int dspark_verify_static_scratch(const float* target_logits, const int32_t* cu_s
  * wait runs out after the limit above; with DSPARK_INJECT_ATTENTION_QUERIES the
  * attention kernels' queries are never complete, and the wait for them runs out
  * after 2 s; with DSPARK_INJECT_MARKOV_OPERANDS those of dspark_markov_grad's
- * products, likewise.  Returns the previous mask; 0 turns
+ * products, likewise (a call of a few rows takes these products too then).  Returns the previous mask; 0 turns
  * injection off.  Both settings are read when a call is enqueued.
  */
 #define DSPARK_INJECT_VERIFY_BARRIER 1u

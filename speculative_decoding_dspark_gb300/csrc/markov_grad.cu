@@ -16,7 +16,8 @@
 // The tensor cores may cut off what lies below the accumulator's last bit, so a
 // chain of products ends after 32 of them (512 terms); the epilogue's threads
 // hold the tile in registers and add the chains in fp32.  (dW2 of 896 rows against
-// 64 bits, relative: 1.2e-6 with chains of 1024 terms, 8e-7 with these, at 1 % of the time.)
+// 64 bits, relative: 1.2e-6 with chains of 1024 terms, 7e-7 with these, at 1 % of the time.)
+// Up to 32 rows, which would leave most of a tile empty, have a kernel of their own (markov_few.cu).
 #include <algorithm>
 
 #include "kernels.cuh"
