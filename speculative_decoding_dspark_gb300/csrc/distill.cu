@@ -159,6 +159,7 @@ __global__ void __launch_bounds__(kThreads + 32, kThreads == kLarge ? 3 : 9) dis
     constexpr int kBatch = kUnroll * kThreads;  // pieces
     extern __shared__ uint4 dyn[];
     __shared__ Shared<kThreads> sh;
+    static_assert(sizeof(Shared<kThreads>) + kSharedAnyway <= 48 * 1024, "what a launch may have without asking");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const bool keeper = warp == kWarps;
     const int rank = (int)cluster_rank(), size = 1 << p.log_ctas;

@@ -228,6 +228,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobsParams
     constexpr int kVec = Elem<T>::kVec, kUnroll = kBatch / kVec;
     extern __shared__ float batch_max[];  // [batches of this CTA][thread]
     __shared__ Shared sh;
+    static_assert(sizeof(Shared) + kSharedAnyway <= 48 * 1024, "what a launch may have without asking");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank(), size = cluster_size();
     // ---- which row, which token (the same for all CTAs of the cluster)
