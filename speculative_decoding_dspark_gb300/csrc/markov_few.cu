@@ -26,12 +26,15 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kChunk = 128;    // elements of g's rows that stand in shared memory at a time
+// Stages of W2 to a warp.  Four and two: 12.9 and 14.5 us for 7 rows of 32000 at rank 256 (three or four stages in all, which are
+// best on their way at once), 82.8 and 79.8 for 7 rows of 151936 at rank 512.
 constexpr int kStages = 4;
 constexpr int kStage = 16 * 64 * 2;  // bytes of W2
 constexpr int kCluster = 2;
 template <int kRows> constexpr int clusters() { return kRows == 16 ? 152 : 76; }  // at most: two CTAs to an SM, or one
 template <int kRows> constexpr int g_bytes() { return kChunk * kRows * 2; }
 template <int kRows> constexpr int shared_bytes() { return kWarps * kStages * kStage + 2 * g_bytes<kRows>(); }
+static_assert(kWarps * 32 * 64 * 4 <= shared_bytes<32>(), "the sums take the stages' place");
 
 __device__ __forceinline__ float4 cluster_ld_f32x4(uint32_t a) {
     float4 v;
