@@ -14,8 +14,8 @@
 // Against the two products of markov_grad.cu: 12.9 and 22.9 us for 7 rows of 32000 at rank 256 (7.4 us of bytes), 18.9 and
 // 24.5 for 32 of these, 83.9 and 97.5 for 7 rows of 151936 at rank 512 (70 us of bytes), 7.3 and 12.6 for 7 rows of 8000
 // at rank 64.  On the CUDA cores, two rows to a multiply-add, the first took 17.5 us and 16 rows of 151936
-// at rank 512 145: there the multiply-adds bound it.  A cluster of two CTAs, one by itself, four: 13.4, 15.7 and
-// 14.3 us for the first; two CTAs of 256 threads on an SM, one of 512: 13.9 and 14.7.
+// at rank 512 145: there the multiply-adds bound it.  A cluster of two CTAs, one by itself, four: 14.0, 14.5 and
+// 14.6 us for the first with nothing in L2; two CTAs of 256 threads on an SM, one of 512: 13.9 and 14.7.
 #include <algorithm>
 
 #include "kernels.cuh"
