@@ -164,6 +164,7 @@ __global__ void __launch_bounds__(kThreads + 32, kThreads == kLarge ? 3 : 9) dis
     const bool keeper = warp == kWarps;
     const int rank = (int)cluster_rank(), size = 1 << p.log_ctas;
     const int clusters = gridDim.x >> p.log_ctas;
+    cluster_arrive();  // (this CTA has started: the others may write to its shared memory once all have)
     uint4* stage = dyn + tid;  // [p.staged batches][kUnroll][kThreads]
     uint32_t* bits = reinterpret_cast<uint32_t*>(dyn + p.staged * kBatch);
     for (int i = tid; i < p.bit_words; i += kAllThreads) bits[i] = 0;
@@ -298,6 +299,7 @@ __global__ void __launch_bounds__(kThreads + 32, kThreads == kLarge ? 3 : 9) dis
         }
     }
     __syncthreads();
+    cluster_wait();  // (over by now: the first row's copies are on their way)
 
     Share<T> s(p, min(row, (int64_t)p.rows - 1), rank);
     for (int parity = 0; row < p.rows; parity ^= 1) {
