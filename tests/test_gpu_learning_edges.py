@@ -39,3 +39,45 @@ def test_distill_beside_other_work(B, V):
     torch.cuda.synchronize()
     assert int(status.item()) == 0
     assert all(torch.equal(losses[k], want[0]) and torch.equal(grads[k], want[1]) for k in range(40))
+
+
+@pytest.mark.parametrize("grad", [F32, None])
+@pytest.mark.parametrize("others,left", [(5e-7, 5e-7), (1e-3, 1e-6), (0.4, 1e-5), (0.2, 1e-4), (0.3, 0.0), (0.0, 3e-8), (0.2, 1e-3)])
+def test_distill_a_rest_next_to_nothing(B, others, left, grad):
+    """A teacher that leaves next to nothing to the tokens that are not listed, and a drafter that leaves them twice as
+    much: what their gradient is depends on every bit of the difference.
+
+    The teacher's share of the rest is (1 - p of its surest token) - sum of the others, in 32 bits: the first off by a step
+    of it (2u), the others by a step each and eight sums (10u), the difference by u: 13u (1 - p_top) in all, u = 2^-24,
+    and the listed mass likewise by 13u where nothing is left; where less than 2^-10 of what the surest token leaves is
+    left, it is taken in 64 bits (a sum of 64 exponentials: below 2^-46) and rounded.  The rest as in
+    learning_reference.py: q (3u|a| + v + e_s + 12u), the share of the rest likewise with its own reference, the
+    roundings of the type."""
+    rows, V, top = 4, 3000, 64
+    p = torch.rand(rows, top, generator=generator(31), device="cuda", dtype=torch.float64)
+    p[:, 1:] *= others / p[:, 1:].sum(1, keepdim=True)
+    p[:, 0] = 1 - others - left
+    value = p.log().float()
+    ids = torch.stack([torch.randperm(V, generator=generator(k), device="cuda")[:top] for k in range(rows)]).to(I32)
+    exact_left = (1 - value.double().exp().sum(1)).clamp(min=0)
+    free = torch.ones(rows, V, dtype=torch.bool, device="cuda").scatter_(1, ids.long(), False)
+    x = normal(32, (rows, V), 0.5) + np.log(2 * max(left, 1e-7) / V)
+    x.scatter_(1, ids.long(), value.clamp(min=-80.0))
+    loss, g, status = distill(B, x, ids, value, 1.0, grad, rest=True)
+    assert status == 0
+    ref, tol = L.distill(x, ids, value, 1.0, None, True, grad)
+    close(loss, ref[0], tol[0], "loss")
+    if grad is None:
+        return
+    close(g, ref[1], tol[1], "grad")
+    t, m, a, q, log_s, e_s, a1, a2, _, _ = L._sums(x, 1.0)
+    free_a = torch.where(free, a, torch.full_like(a, L.NEG))
+    share = torch.softmax(free_a, 1)
+    extra = exact_left[:, None] * share
+    own = 3 * L.U * (a - free_a.amax(1, keepdim=True)).abs()
+    want = q - extra
+    beside = -torch.expm1(value[:, :1].double())
+    d_left = torch.where(exact_left[:, None] < beside * 2.0 ** -11, L.U * exact_left[:, None] + 2.0 ** -46, 13 * L.U * beside)
+    tol = (q * (3 * L.U * a.abs() + L.V2 + e_s[:, None] + 25 * L.U) + extra * (own + 2 * L.V2 + 2 * e_s[:, None] + 8 * L.U) +
+           share * d_left + 5 * L.U * want.abs() + 2.0 ** -120)
+    close(g[free], want[free], tol[free], "the rest's gradient")
