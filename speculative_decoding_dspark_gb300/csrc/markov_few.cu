@@ -5,7 +5,7 @@
 // one pass over V, two launches in all instead of four.  A warp has 64 columns of the factors and walks down V, 16
 // elements at a time: W2's 16 x 64 arrive in shared memory by asynchronous copies, three of these ahead, and g's 16 x rows
 // stand there for all warps.  Sixteen rows are one operand of mma.sync in either direction:
-//   grad_prev += g (rows x 16) . W2 (16 x 64),  sums in registers all the way down;
+//   grad_prev += g (rows x 16) . W2 (16 x 64),  sums in registers for 512 terms at a time;
 //   dW2        = g^T (16 x rows) . E (rows x 64),  E, the rows' W1 rows, in registers.
 // (The tensor cores' 128-row tiles would be empty but for these, and the sums over V in parts need more steps; the bytes bound
 // it as it is.)  The CTAs of a cluster join their sums through distributed shared memory, few_join_kernel adds
@@ -34,6 +34,11 @@ constexpr int kCluster = 2;
 template <int kRows> constexpr int clusters() { return kRows == 16 ? 152 : 76; }  // at most: two CTAs to an SM, or one
 template <int kRows> constexpr int g_bytes() { return kChunk * kRows * 2; }
 template <int kRows> constexpr int shared_bytes() { return kWarps * kStages * kStage + 2 * g_bytes<kRows>(); }
+// A chain of products ends after 512 terms, as in markov_grad.cu, and is added up in fp32; the sums of a warp that has more
+// stand in shared memory of its own.  (One chain to a warp: grad_prev of 32 rows of 2^22 elements at rank 512, all terms of one sign,
+// was off by 1.4e-4 of itself, 8e-7 with these; 151936 elements 1.9e-6 and 8e-7.)
+constexpr int kChain = 32;  // steps of 16 terms
+template <int kRows> constexpr int chain_bytes() { return kWarps * kRows * 64 * 4; }
 static_assert(kWarps * 32 * 64 * 4 <= shared_bytes<32>(), "the sums take the stages' place");
 
 __device__ __forceinline__ float4 cluster_ld_f32x4(uint32_t a) {
@@ -140,6 +145,19 @@ __global__ void __launch_bounds__(kThreads, kRows == 16 ? 2 : 1) few_kernel(cons
 #pragma unroll
             for (int q = 0; q < 4; ++q) acc[z][j][q] = 0.0f;
 
+    float4* const chains = reinterpret_cast<float4*>(memory + shared_bytes<kRows>()) + warp * kTiles * 8 * 32 + lane;
+    auto end_chain = [&](bool first) {
+#pragma unroll
+        for (int z = 0; z < kTiles; ++z)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float4 s = make_float4(acc[z][j][0], acc[z][j][1], acc[z][j][2], acc[z][j][3]);
+                if (!first) s = plus(chains[(z * 8 + j) * 32], s);
+                chains[(z * 8 + j) * 32] = s;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[z][j][q] = 0.0f;
+            }
+    };
     unsigned char* const g_at = memory + kWarps * kStages * kStage;
     float* dW2 = p.dW2 + (int64_t)begin * p.rank + slice * 64 + 4 * t;
     const int block = lane >> 3, in_block = lane & 7;
@@ -156,6 +174,7 @@ __global__ void __launch_bounds__(kThreads, kRows == 16 ? 2 : 1) few_kernel(cons
         const uint32_t g_s = (uint32_t)__cvta_generic_to_shared(g);
         if (active)
             for (int v0 = 16 * group; v0 < min(kChunk, n - base); v0 += 16 * groups, ++k) {
+                if (k > 0 && k % kChain == 0) end_chain(k == kChain);
                 copies_wait<kStages - 2>();
                 __syncwarp();  // (every lane's copies; and every lane has read the stage that is filled next)
                 fetch(k + kStages - 1);
@@ -199,6 +218,17 @@ __global__ void __launch_bounds__(kThreads, kRows == 16 ? 2 : 1) few_kernel(cons
             }
     }
 
+    if (k > kChain)
+#pragma unroll
+        for (int z = 0; z < kTiles; ++z)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float4 s = chains[(z * 8 + j) * 32];
+                acc[z][j][0] += s.x;
+                acc[z][j][1] += s.y;
+                acc[z][j][2] += s.z;
+                acc[z][j][3] += s.w;
+            }
     // the groups' sums in order, and those of the cluster's CTAs: a half of the columns to each
     copies_wait<0>();
     __syncthreads();  // (W2 and g have been read)
@@ -283,7 +313,8 @@ cudaError_t launch_few(const MarkovGradParams& p, cudaStream_t stream) {
     const int per = std::max(up(up(p.V, 16), clusters<kRows>() * kCluster), groups) * 16, parts = up(up(p.V, per), kCluster);
     float* part = static_cast<float*>(p.ws);
     const auto kernel = few_kernel<kRows>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared_bytes<kRows>());
+    constexpr int most = shared_bytes<kRows>() + chain_bytes<kRows>();  // (two CTAs of 16 rows still have room on an SM)
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -294,7 +325,7 @@ cudaError_t launch_few(const MarkovGradParams& p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(parts * kCluster);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = shared_bytes<kRows>();
+    cfg.dynamicSmemBytes = up(per / 16, groups) > kChain ? most : shared_bytes<kRows>();
     cfg.stream = stream;
     cfg.attrs = at;
     cfg.numAttrs = 2;

@@ -81,3 +81,31 @@ def test_distill_a_rest_next_to_nothing(B, others, left, grad):
     tol = (q * (3 * L.U * a.abs() + L.V2 + e_s[:, None] + 25 * L.U) + extra * (own + 2 * L.V2 + 2 * e_s[:, None] + 8 * L.U) +
            share * d_left + 5 * L.U * want.abs() + 2.0 ** -120)
     close(g[free], want[free], tol[free], "the rest's gradient")
+
+
+# ------------------------------------------------------------------------------ the Markov factors' gradient
+def grad_prev_of(g, W2):
+    """sum_v g W2 and sum_v |g W2| in 64 bits, a stretch of V at a time."""
+    s, size = (torch.zeros(g.shape[0], W2.shape[1], dtype=torch.float64, device="cuda") for _ in range(2))
+    for a in range(0, g.shape[1], 1 << 17):
+        x, y = g[:, a:a + (1 << 17)].double(), W2[a:a + (1 << 17)].double()
+        s += x @ y
+        size += x.abs() @ y.abs()
+    return s, size
+
+
+@pytest.mark.parametrize("rows", [7, 16, 17, 32, 33])
+@pytest.mark.parametrize("V,rank", [((1 << 21) + 8, 512), ((1 << 22), 64), (151936, 512)])
+def test_markov_grad_long_sums(B, rows, V, rank):
+    """Terms of one sign: what an accumulator cuts off goes the same way every time.
+
+    A chain ends after 512 terms, 32 steps of which each may cut off 2^-22 of the sum so far; the chains' sums (at most 64
+    to a warp or part here), those of eight groups, of two CTAs and of 152 parts are added in fp32, u each."""
+    g = normal(rows, (rows, V)).abs_().to(BF16)
+    W2 = torch.empty(V, rank, dtype=BF16, device="cuda").normal_(0.0, 0.05, generator=generator(2)).abs_()
+    W1 = torch.zeros(V, rank, dtype=BF16, device="cuda")
+    prev = torch.arange(rows, device="cuda", dtype=I32)
+    gp, _, _, status = markov(B, g, prev, W1, W2, want=(False, False))
+    assert status == 0
+    ref, size = grad_prev_of(g, W2)
+    close(gp, ref, (32 * 2.0 ** -22 + (64 + 8 + 2 + 152) * L.U) * size, "grad_prev")
