@@ -109,3 +109,43 @@ def test_markov_grad_long_sums(B, rows, V, rank):
     assert status == 0
     ref, size = grad_prev_of(g, W2)
     close(gp, ref, (32 * 2.0 ** -22 + (64 + 8 + 2 + 152) * L.U) * size, "grad_prev")
+
+
+@pytest.mark.parametrize("rows", [1, 7, 16, 17, 32, 33, 128, 129, 300])
+@pytest.mark.parametrize("V,rank", [(8, 64), (640, 192), (40008, 256), (80008, 512), (151936, 64), (151936, 512)])
+def test_markov_grad_every_term(B, rows, V, rank):
+    """Whole numbers whose sums fp32 holds exactly, in any order: every term is there once, in all three gradients."""
+    g = torch.randint(-2, 3, (rows, V), generator=generator(V + rows), device="cuda").to(BF16)
+    W1, W2 = (torch.randint(-3, 4, (V, rank), generator=generator(V + k), device="cuda").to(BF16) for k in (1, 2))
+    prev = torch.randint(-1, max(1, min(V, rows // 2 + 1)), (rows,), generator=generator(3), device="cuda", dtype=I32)
+    assert V * 6 < 2 ** 24 and rows * V * 6 < 2 ** 53
+    gp, d1, d2, status = markov(B, g, prev, W1, W2)
+    assert status == 0
+    there = prev >= 0
+    want, _ = grad_prev_of(g, W2)
+    want *= there[:, None]
+    assert torch.equal(gp.double(), want)
+    at = prev.clamp(min=0).long()
+    sums = torch.zeros(V, rank, dtype=torch.float64, device="cuda").index_add_(0, at, want)
+    assert float(sums.abs().max()) < 2 ** 24 and torch.equal(d1.double(), sums)
+    E = W1.double()[at] * there[:, None]
+    assert torch.equal(d2.double(), g.double().t() @ E)
+
+
+@pytest.mark.parametrize("rows,rank", [(7, 256), (20, 512), (33, 64), (200, 512)])
+def test_markov_grad_last_terms(B, rows, rank):
+    """A gradient of one element, at the beginnings and ends of what CTAs, stages and parts may have."""
+    V = 50008
+    W1, W2 = (normal(k, (V, rank)).to(BF16) for k in (4, 5))
+    prev = torch.arange(rows, device="cuda", dtype=I32) % 5
+    places = [0, 15, 16, 63, 64, 127, 128, 255, 256, V // 2, V - 257, V - 65, V - 64, V - 17, V - 16, V - 9, V - 8, V - 1]
+    for v in places:
+        g = torch.zeros(rows, V, dtype=BF16, device="cuda")
+        g[rows - 1, v] = 2.0
+        gp, d1, d2, status = markov(B, g, prev, W1, W2)
+        assert status == 0
+        want = torch.zeros_like(gp)
+        want[rows - 1] = 2 * W2[v].float()
+        assert torch.equal(gp, want), v
+        assert torch.equal(d1[int(prev[rows - 1])], want[rows - 1]) and int((d1 != 0).any(1).sum()) == 1, v
+        assert torch.equal(d2[v], 2 * W1[int(prev[rows - 1])].float()) and int((d2 != 0).any(1).sum()) == 1, v
