@@ -149,3 +149,38 @@ def test_markov_grad_last_terms(B, rows, rank):
         assert torch.equal(gp, want), v
         assert torch.equal(d1[int(prev[rows - 1])], want[rows - 1]) and int((d1 != 0).any(1).sum()) == 1, v
         assert torch.equal(d2[v], 2 * W1[int(prev[rows - 1])].float()) and int((d2 != 0).any(1).sum()) == 1, v
+
+
+@pytest.mark.parametrize("rows,V,rank", [(2560, 136, 512), (20000, 64, 64), (4100, 72, 320), (33, 64, 64)])
+@pytest.mark.parametrize("every", [1, 3])
+def test_markov_grad_many_equal_tokens(B, rows, V, rank, every):
+    """One token before all rows, or three in turn: dW1's error does not grow with their number.
+
+    A compensated sum of n terms: 2u sum |x| and the second order, n u^2 sum |x|, a few times (here four); then the sum to
+    the given value, one rounding."""
+    g = normal(rows, (rows, V)).abs_().to(BF16)
+    W1, W2 = (normal(k, (V, rank)).abs_().to(BF16) for k in (1, 2))
+    prev = (torch.arange(rows, device="cuda") % every * 7).to(I32)
+    for accumulate, start in ((False, 3.0), (True, 3.0)):
+        gp, d1, _, status = markov(B, g, prev, W1, W2, accumulate, want=(True, False), start=(start, 0.0))
+        assert status == 0
+        for t in range(every):
+            x = gp[prev == 7 * t].double()
+            size = x.abs().sum(0) + start * accumulate
+            want = x.sum(0) + start * accumulate
+            close(d1[7 * t], want, (2 * L.U + 4 * rows * L.U ** 2) * size + L.U * want.abs(), "dW1")
+        assert bool((d1[1:7] == start).all())
+
+
+def test_markov_grad_equal_tokens_infinite(B):
+    """An infinity among the rows of a token stays one in its sum, two of them of either sign are none."""
+    rows, V, rank = 200, 136, 64
+    g, prev, W1, W2 = markov_case(12, rows, V, rank)
+    g = torch.where(g == 0, torch.ones_like(g), g).abs()
+    prev.copy_(torch.arange(rows, device="cuda") % 2)
+    W2.zero_()
+    W2[0] = 1.0
+    g[20, 0], g[21, 0], g[101, 0] = float("inf"), float("inf"), -float("inf")
+    gp, d1, _, status = markov(B, g, prev, W1, W2, want=(True, False))
+    assert status == 0 and bool((gp[20] == float("inf")).all()) and bool((gp[101] == -float("inf")).all())
+    assert bool((d1[0] == float("inf")).all()) and bool(d1[1].isnan().all())
