@@ -157,8 +157,8 @@ int dspark_version(void);
 /* Bytes of workspace one call of `op` needs for these sizes (0 on bad
  * arguments).  For DSPARK_OP_DRAFT pass the weights' element type and the
  * draft flags; for DSPARK_OP_VERIFY, max_rows bounds cu_seqlens[R]; for
- * DSPARK_OP_MARKOV_GRAD max_rows is the rows of the gradient; other arguments may
- * be 0 where unused. */
+ * DSPARK_OP_MARKOV_GRAD max_rows is the most rows of a gradient (any fewer do with
+ * as much); other arguments may be 0 where unused. */
 size_t dspark_workspace_size(int op, int R, int gamma, int V, int rank, int max_rows,
                              int w_dtype, unsigned flags);
 
@@ -766,7 +766,7 @@ int dspark_distill_loss(const void* student, int64_t student_stride, int student
  *   prev         [rows] int32, the token before each row: the anchor, then the drafted ones
  *   W1, W2       [V, rank] bf16
  *   grad_prev    [rows, rank] fp32 out;  dW1, dW2 [V, rank] fp32, or NULL: not wanted
- *   ws, ws_bytes dspark_workspace_size(DSPARK_OP_MARKOV_GRAD, 0, 0, V, rank, rows, DSPARK_BF16, 0)
+ *   ws, ws_bytes dspark_workspace_size(DSPARK_OP_MARKOV_GRAD, 0, 0, V, rank, rows, DSPARK_BF16, 0), for these rows or more
  * A row with prev >= V is reported (DSPARK_ERR_DEVICE_INPUT), gives nothing to dW1 and dW2, and
  * its grad_prev is NaN.  rows == 0 gives zeros (dW2) without DSPARK_GRAD_ACCUMULATE.
  * Limits (DSPARK_ERR_UNSUPPORTED): rank % 64 == 0 up to 512, V % 8 == 0 up to

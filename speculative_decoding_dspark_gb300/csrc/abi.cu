@@ -193,7 +193,7 @@ int dspark_markov_draft_uses_tensor_cores(int u_dtype, int w_dtype, int R, int V
 size_t dspark_workspace_size(int op, int R, int gamma, int V, int rank, int max_rows,
                              int w_dtype, unsigned flags) {
     if (op == DSPARK_OP_CALIBRATE) return (gamma <= 0 || gamma > 16) ? 0 : calibrate_workspace(gamma);
-    if (op == DSPARK_OP_MARKOV_GRAD) return markov_grad_supported(max_rows, V, rank) ? markov_grad_workspace(max_rows, V, rank) : 0;
+    if (op == DSPARK_OP_MARKOV_GRAD) return markov_grad_supported(max_rows, V, rank) ? markov_grad_workspace_up_to(max_rows, V, rank) : 0;
     if (R <= 0) return 0;
     switch (op) {
         case DSPARK_OP_DRAFT:

@@ -298,7 +298,8 @@ struct MarkovGradParams {
     void* ws;
 };
 
-size_t markov_grad_workspace(int rows, int V, int rank);
+size_t markov_grad_workspace(int rows, int V, int rank);        // of a call
+size_t markov_grad_workspace_up_to(int rows, int V, int rank);  // of any call of up to `rows`
 cudaError_t launch_markov_grad(const MarkovGradParams& p, cudaStream_t stream);
 constexpr int kMarkovFewRows = 32;  // (two operands of rows)
 size_t markov_few_workspace(int rows, int rank);

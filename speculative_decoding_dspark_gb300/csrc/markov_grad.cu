@@ -695,6 +695,20 @@ cudaError_t launch_product(Product p, const CUtensorMap& a, const CUtensorMap& b
 
 size_t markov_grad_workspace(int rows, int V, int rank) { return layout_of(rows, V, rank).total; }
 
+// Fewer rows are cut into more parts, and may take more room than many.  Rows of as many tiles: the fewest have the most
+// parts (a part's way to memory, which is what grows with them, counts against its number).
+size_t markov_grad_workspace_up_to(int rows, int V, int rank) {
+    size_t part = 0;
+    for (int n = 1; n <= std::min(rows, kMarkovFewRows); ++n) part = std::max(part, (size_t)parts_of(n, V, rank) * n);
+    for (int low = kMarkovFewRows + 1; low <= rows;) {
+        const int tile = kTileM * ctas_of(low), high = std::min(rows, up(low, tile) * tile);
+        part = std::max(part, (size_t)std::max(parts_of(low, V, rank), parts_of(high, V, rank)) * high);
+        low = high + 1;
+    }
+    const size_t total = align256((size_t)rows * rank * 2) + align256((size_t)rows) + align256(part * rank * 4);
+    return std::max({total, markov_few_workspace(std::min(rows, kMarkovFewRows), rank), (size_t)256});
+}
+
 cudaError_t launch_markov_grad(const MarkovGradParams& p, cudaStream_t stream) {
     if (p.rows == 0) {
         if (!p.dW2 || p.accumulate) return cudaSuccess;

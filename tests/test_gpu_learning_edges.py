@@ -184,3 +184,17 @@ def test_markov_grad_equal_tokens_infinite(B):
     gp, d1, _, status = markov(B, g, prev, W1, W2, want=(True, False))
     assert status == 0 and bool((gp[20] == float("inf")).all()) and bool((gp[101] == -float("inf")).all())
     assert bool((d1[0] == float("inf")).all()) and bool(d1[1].isnan().all())
+
+
+@pytest.mark.parametrize("V,rank,most", [(4104, 64, 700), (32000, 256, 896)])
+def test_markov_grad_workspace_of_the_largest_call(B, V, rank, most):
+    """One workspace, as large as the largest call's, holds calls of any fewer rows: the bits of calls with their own."""
+    g, prev, W1, W2 = markov_case(17, most, V, rank)
+    ws = B.workspace(B.dspark_workspace_size(B.DSPARK_OP_MARKOV_GRAD, 0, 0, V, rank, most))
+    status = torch.zeros(1, dtype=I32, device="cuda")
+    for rows in (1, 16, 17, 32, 33, 64, 128, 129, 256, 257, 400, 512, 513, 640, most):
+        want = markov(B, g[:rows], prev[:rows], W1, W2)
+        gp, d1, d2 = (torch.zeros_like(x) for x in want[:3])
+        B.dspark_markov_grad(g[:rows], prev[:rows], W1, W2, gp, dW1=d1, dW2=d2, ws=ws, dev_status=status)
+        assert all(torch.equal(a, b) for a, b in zip((gp, d1, d2), want[:3])), rows
+    assert int(status.item()) == 0
