@@ -428,9 +428,11 @@ cudaError_t launch_logprobs(const LogprobsParams& p, cudaStream_t stream) {
         return (size_t)(p.top_k ? (per * vec + kBatch * kThreads - 1) / (kBatch * kThreads) * kThreads * sizeof(float) : 0);
     };
     // Rows are shared by more CTAs until there are eight to an SM, as long as a CTA keeps 4096 pieces, or 1024 where an SM
-    // would have none.  One, two, four and eight CTAs to a row: 21.0, 13.7, 9.5 and 7.3 us for one row of 151936 fp32; 61, 53, 48
-    // and 55 for 350 such rows asked for among 560; 127, 138, 168 and 251 for 2560 rows of 129280 bf16; 15.5, 17.1, 23 and 35 for 333 rows
-    // of 50001 bf16.
+    // would have none.  One, two, four and eight CTAs to a row, us: 15.5, 10.7, 7.6 and 6.9 for one row of 151936 fp32; 128, 143, 172
+    // and 257 for 2560 rows of 129280 bf16; 15.4, 16.5, 21.4 and 35 for 333 rows of 50001 bf16.  Beside cu_seqlens the
+    // places count, of which the kernel alone knows how many have a row and are asked for: 41.6, 48.3, 48.4 and 63.6 for 349 rows of 151936
+    // fp32 in 1024 places (two by this rule; with the places held to the 544 rows there are it would be four), 36.9, 24.9, 27.1 and
+    // 32.9 for those of 512 places (four), 27.0, 20.0, 15.9 and 17.3 for those of 256 (eight).
     auto larger = [&](int c) {
         return smem_of(c) > 48 * 1024 || (places * c < 8 * kSms && pieces / (2 * c) >= (places * c < kSms ? 1024 : 4096));
     };
