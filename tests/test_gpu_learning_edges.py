@@ -198,3 +198,66 @@ def test_markov_grad_workspace_of_the_largest_call(B, V, rank, most):
         B.dspark_markov_grad(g[:rows], prev[:rows], W1, W2, gp, dW1=d1, dW2=d2, ws=ws, dev_status=status)
         assert all(torch.equal(a, b) for a, b in zip((gp, d1, d2), want[:3])), rows
     assert int(status.item()) == 0
+
+
+# ------------------------------------------------------------------------------------------- all of them
+def test_chain_on_a_verify_s_packed_rows(B):
+    """From the rows a verify read to the factors' gradient.  The target's rows are packed (cu_seqlens[r] + j), the
+    drafter's lie by blocks (r * gamma + j): the teacher's lists are laid beside the drafter's rows, and rows that no
+    target row stands beside (behind a request's length) have no list: loss and gradient 0.  A request's last packed row is
+    the bonus token's, beside which the drafter has nothing."""
+    from speculative_decoding_dspark_gb300 import inputs
+    R, gamma, V, rank, top, T = 17, 5, 8192, 64, 16, 0.7
+    w, d = H.cycle_inputs("varlen_verify", R=R, V=V, gamma=gamma, rank=rank, w_sigma=0.2)
+    g = H.gpu_draft(d, T, 2)
+    l = inputs.verify_lengths(w)
+    assert l.min() < gamma and l.max() > 0
+    target = H.dev(inputs.pack_rows(inputs.target_full(w, d["U"]), l))
+    cu = H.dev(inputs.cu_from_lengths(l))
+    rows = target.shape[0]
+    status = torch.zeros(1, dtype=I32, device="cuda")
+    n_acc, out = torch.empty(R, dtype=I32, device="cuda"), torch.empty(R, gamma + 1, dtype=I32, device="cuda")
+    ws = B.workspace(max(B.dspark_workspace_size(B.DSPARK_OP_VERIFY, R, gamma, V, 0, rows),
+                         B.dspark_workspace_size(B.DSPARK_OP_MARKOV_GRAD, 0, 0, V, rank, R * gamma)))
+    B.dspark_verify(target, cu, g["y_dev"], g["q_logits_dev"], g["q_lse_dev"], g["q_tok_dev"], H.dev(d["seeds"]), 2, T, rows,
+                    n_acc, out, None, ws, dev_status=status)
+    ids, val = torch.empty(rows, top, dtype=I32, device="cuda"), torch.empty(rows, top, device="cuda")
+    B.dspark_token_logprobs(target, None, T, None, None, None, ids, val, dev_status=status)
+    # each packed row's place among the drafter's
+    row = torch.arange(rows, device="cuda")
+    r = torch.searchsorted(cu.long(), row, right=True) - 1
+    j = row - cu.long()[r]
+    drafted = (j < H.dev(l).long()[r]).nonzero()[:, 0]
+    at = (r * gamma + j)[drafted]
+    teacher_ids = torch.full((R * gamma, top), -1, dtype=I32, device="cuda")
+    teacher = torch.zeros(R * gamma, top, device="cuda")
+    teacher_ids[at], teacher[at] = ids[drafted], val[drafted]
+    # (q_logits are scaled already: temperature 1, and the gradient of U + W2 W1[prev] has 1 / T more)
+    student = g["q_logits_dev"].reshape(R * gamma, V)
+    weight = torch.full((R * gamma,), 1 / T, device="cuda")
+    loss, grad = torch.empty(R * gamma, device="cuda"), torch.empty(R * gamma, V, dtype=BF16, device="cuda")
+    B.dspark_distill_loss(student, teacher_ids, teacher, 1.0, loss, grad=grad, row_weight=weight, rest=True, dev_status=status)
+    prev = torch.cat([H.dev(d["anchor"])[:, None], g["y_dev"][:, :-1]], 1).reshape(-1).contiguous()
+    W1, W2 = H.dev(d["W1"]), H.dev(d["W2"])
+    gp, d1, d2 = (torch.zeros(*s, device="cuda") for s in ((R * gamma, rank), (V, rank), (V, rank)))
+    B.dspark_markov_grad(grad, prev, W1, W2, gp, dW1=d1, dW2=d2, ws=ws, dev_status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    # every step against its definition, row by row of a block: the target's row for position j stands at cu[r] + j
+    behind = torch.ones(R * gamma, dtype=torch.bool, device="cuda")
+    for q in range(R):
+        n = int(l[q])
+        behind[q * gamma:q * gamma + n] = False
+        if n == 0:
+            continue
+        first = int(cu[q])
+        ref, _ = L.logprobs(target[first:first + n], None, T, top)
+        mine = slice(q * gamma, q * gamma + n)
+        assert torch.equal(teacher_ids[mine].long(), ref[3])
+        ref, tol = L.distill(student[mine], ids[first:first + n], val[first:first + n], 1.0, weight[mine], True, BF16)
+        close(loss[mine], ref[0], tol[0], "loss")
+        close(grad[mine], ref[1], tol[1], "grad")
+    assert bool(behind.any()) and bool((loss[behind] == 0).all()) and bool((grad[behind] == 0).all())
+    ref, tol = L.markov(grad, prev, W1, W2)
+    for got, want, t, name in zip((gp, d1, d2), ref, tol, ("grad_prev", "dW1", "dW2")):
+        close(got, want, t, name)
