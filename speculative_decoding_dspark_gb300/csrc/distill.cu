@@ -36,9 +36,9 @@ constexpr int kLarge = 256, kSmall = 64;
 constexpr int kUnroll = 4;     // pieces of a batch
 constexpr int kMaxCtas = 8;    // of a cluster
 constexpr int kPerLane = DSPARK_TOP_MAX / 32;
-// Rows of at most this many pieces take the small CTA, of which nine fit on an SM.  4096 rows, large and small, us: of 500,
-// 4096, 8192 and 16384 fp32 37 and 18, 44 and 30, 53 and 57, 76 and 132; of 4096, 16384 and 32000 bf16 57 and 29, 75 and
-// 76, 109 and 177.
+// Rows of at most this many pieces take the small CTA, of which nine fit on an SM.  4096 rows, 64 tokens, bf16 gradient, large
+// and small, us: of 500, 4096, 8192 and 16384 fp32 43 and 20, 46 and 30, 54 and 57, 77 and 133; of 4096, 16384 and 32000
+// bf16 50 and 27, 69 and 75, 105 and 174.
 constexpr int kSmallPieces = 1792;
 
 // What is known of a row's listed tokens before its sums are.  (Sixteen bytes, one load: with a fifth word 896 rows of
